@@ -278,6 +278,15 @@ int paro_w4_linear_noalloc(const paro_rotation* r, const uint16_t* x, const uint
                            uint16_t* y, int64_t M, int64_t N, int64_t d, int32_t group,
                            hipStream_t stream);
 
+/* Activations of the products with an epilogue. */
+typedef enum {
+  PARO_ACT_NONE = 0,
+  PARO_ACT_SILU = 1,      /* z / (1 + e^-z) */
+  PARO_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  PARO_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  PARO_ACT_RELU = 4       /* max(z, 0) */
+} paro_activation;
+
 /* Which transform paro_rotation_backward differentiates. */
 typedef enum {
   PARO_SIDE_ACTIVATION = 0, /* X' = X T^-1, as paro_rotate computes it */
@@ -379,6 +388,144 @@ int paro_layer_loss(const paro_rotation* r, const uint16_t* x, const uint16_t* w
                     const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros, int64_t M,
                     int64_t N, int64_t d, int32_t group, float* loss, float* dtheta, float* dalpha,
                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The W4 linear with its bias, an activation and a residual in the epilogue:
+ *   Y[m][n] = act(Z[m][n]) + R[m][n],
+ *   Z[m][n] = sum_k X'[m][k] W_hat[n][k] + bias[n],
+ * X', W_hat, sizes, alignment, workspace (paro_w4_linear_workspace_size) and
+ * kernels as for paro_w4_linear; Z, the activation and the sum in fp32, one
+ * rounding to fp16.
+ *   residual  device fp16 [M][N], 16-byte aligned, or NULL; may be y itself
+ *             (each value is read before it is replaced), no other overlap.
+ *   act       a paro_activation.
+ * Errors: those of paro_w4_linear, PARO_ERR_VALUE (unknown activation).
+ */
+int paro_w4_linear_act(const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
+                       const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias,
+                       const uint16_t* residual, int32_t act, uint16_t* y, int64_t M, int64_t N,
+                       int64_t d, int32_t group, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * The gated feed-forward product, both projections and their product in one
+ * kernel:
+ *   Y[m][n] = act(Zg[m][n]) Zu[m][n],
+ *   Zg[m][n] = sum_k X'[m][k] W_hat[n][k] + bias[n],
+ *   Zu[m][n] = sum_k X'[m][k] W_hat[N + n][k] + bias[N + n].
+ * The weight block has 2 N rows, the gate projection's first, then the up
+ * projection's: what paro_quantize_weights makes of the two [N][d] weights
+ * laid one after the other. Both projections read the same X', so a plan r is
+ * shared by them.
+ *   qweight [2N][d/2], scales and zeros [2N][d/group], bias [2N] or NULL,
+ *   y fp16 [M][N]; N % 16 == 0 and N d < 2^31, else as paro_w4_linear with
+ *   2 N rows, the workspace (paro_w4_gated_workspace_size) included.
+ * Errors: those of paro_w4_linear, PARO_ERR_VALUE (unknown activation).
+ */
+size_t paro_w4_gated_workspace_size(const paro_rotation* r, int64_t M, int64_t N, int64_t d);
+int paro_w4_gated(const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
+                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, int32_t act,
+                  uint16_t* y, int64_t M, int64_t N, int64_t d, int32_t group, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of the two products above with respect to their pre-activations
+ * and to X', for learning through them (the transform's own gradients follow
+ * from dX' by paro_rotation_backward; the 4-bit weights are constants).
+ * paro_w4_linear_act_backward, for dY = dL/dY:
+ *   dZ = dY act'(Z),  dX' = dZ W_hat  (and dL/dR is dY itself).
+ * paro_w4_gated_backward:
+ *   dZg = dY Zu act'(Zg),  dZu = dY act(Zg),  dX' = [dZg dZu] W_hat.
+ * Z is computed again from X' rather than kept by the forward call: a kept Z
+ * would cost 2 M (2) N bytes and its fp16 rounding. dZ is the bias gradient
+ * before its sum over the tokens, and dZ^T X' would be the weights'.
+ *   x     device fp16 [M][d]: X', the transformed activations (not needed,
+ *         may be NULL, for a linear without activation);
+ *   dy    device fp16 [M][N];
+ *   dz    device fp16 [M][N], gated [M][2N] (gate, then up), overwritten; may
+ *         be NULL for a linear without activation, where dZ is dY;
+ *   dx    device fp16 [M][d], overwritten, or NULL (dz alone);
+ *   all 16-byte aligned and not overlapping; act, bias, sizes as for the
+ *   forward calls, at most 2^22 weight rows; M == 0 is a no-op.
+ *   workspace: at least the ..._workspace_size bytes (W_hat transposed in
+ *         fp16, 2 d (2) N bytes, is the largest part), 256-byte aligned,
+ *         zero-filled once after allocation (its first 16 KiB hold arrival
+ *         counters, which every call leaves zero).
+ * Arithmetic: fp32 sums and epilogues. dZ is rounded to fp16, which is what
+ * dX' is then summed from, so gradients far below fp16's normal range
+ * (6e-5) lose accuracy: scale the loss, as is usual with fp16 gradients.
+ * relu'(0) is 0. Results do not depend on timing.
+ * Errors: those of paro_w4_linear, PARO_ERR_VALUE (unknown activation).
+ */
+size_t paro_w4_linear_act_backward_workspace_size(int64_t M, int64_t N, int64_t d, int32_t act);
+int paro_w4_linear_act_backward(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+                                const uint8_t* zeros, const uint16_t* bias, int32_t act,
+                                const uint16_t* dy, uint16_t* dz, uint16_t* dx, int64_t M, int64_t N,
+                                int64_t d, int32_t group, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+size_t paro_w4_gated_backward_workspace_size(int64_t M, int64_t N, int64_t d);
+int paro_w4_gated_backward(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+                           const uint8_t* zeros, const uint16_t* bias, int32_t act, const uint16_t* dy,
+                           uint16_t* dz, uint16_t* dx, int64_t M, int64_t N, int64_t d, int32_t group,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Element types of the AdamW step's tensors. */
+typedef enum { PARO_TYPE_F32 = 0, PARO_TYPE_F16 = 1, PARO_TYPE_BF16 = 2 } paro_type;
+
+/* Plan of an AdamW step over a fixed list of tensors. Immutable after creation. */
+typedef struct paro_adamw paro_adamw;
+
+/* Values of each moment for `count` tensors of n[i] values: every tensor's
+ * moments start at a multiple of 256, so this is the sum of n[i] rounded up to
+ * 256. -1 for a bad list (a negative or too large size). */
+int64_t paro_adamw_moments(int32_t count, const int64_t* n);
+
+/*
+ * AdamW over many tensors at once, the optimizer of the angles and scales
+ * (paper notes, "损失函数 / 训练策略"), for step t:
+ *   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2,
+ *   p <- p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32; p is rounded once to its type (with fp16 or bf16 parameters an
+ * update below half a step of the value is lost).
+ *
+ * paro_adamw_create (host only, no GPU work) makes the plan of a list of
+ * tensors; the caller owns the tensors and keeps them where they are.
+ *   count, n            tensors and their values, n[i] >= 0 (0: skipped);
+ *   params, grads       host arrays of device pointers, contiguous, aligned to
+ *                       their element type (16 bytes: the fast accesses);
+ *   param_type, grad_type  a paro_type for all of them;
+ *   state_bits          32: m and v device fp32 [paro_adamw_moments]; scales
+ *                       unused.
+ *                       8: m and v device bytes [paro_adamw_moments], e4m3
+ *                       numbers, and m_scale and v_scale device fp32 [moments
+ *                       / 256]: block b of 256 consecutive values of a tensor
+ *                       stands for m = e4m3 * m_scale[b] and sqrt(v) = e4m3 *
+ *                       v_scale[b], scale = largest magnitude / 448 (rounded
+ *                       to nearest even; sqrt(v) is not rounded to zero where
+ *                       v > 0; a block below 2^-100 is held as zero). A
+ *                       gradient that is not finite leaves its block's scale
+ *                       infinite or NaN, and the block's moments NaN.
+ *                       Zero-fill all of them before the first step, the
+ *                       padding between the tensors included.
+ * Errors: PARO_ERR_NULL, PARO_ERR_VALUE (unknown type; parameters, moments or
+ * scales that overlap each other or a gradient), PARO_ERR_UNSUPPORTED
+ * (state_bits, out of host memory), PARO_ERR_SHAPE, PARO_ERR_ALIGN.
+ *
+ * paro_adamw_step runs step t >= 1 on the current device: a launch for every
+ * 120 tensors, without upload, allocation or synchronisation. A captured call
+ * replays the t and the rates it was captured with. Steps of one plan must
+ * not run at the same time.
+ * Errors: PARO_ERR_NULL, PARO_ERR_VALUE (step < 1; lr or weight_decay
+ * negative, beta outside [0, 1), eps <= 0, or one of them not finite),
+ * PARO_ERR_HIP.
+ */
+int paro_adamw_create(int32_t count, const int64_t* n, void* const* params, int32_t param_type,
+                      const void* const* grads, int32_t grad_type, int32_t state_bits, void* m,
+                      void* v, float* m_scale, float* v_scale, paro_adamw** out);
+void paro_adamw_destroy(paro_adamw* h);
+int paro_adamw_step(const paro_adamw* h, int64_t step, double lr, double beta1, double beta2,
+                    double eps, double weight_decay, hipStream_t stream);
 
 /*
  * Channel-pair selection (host only, synchronous, no GPU): fills pairs

@@ -9,7 +9,8 @@ Names follow the C ABI: ``paro_device_init``, ``paro_rotation_create`` / ``Rotat
 ``paro_rotate``, ``paro_quantize_weights``, ``paro_w4_linear``,
 ``paro_w4_linear_workspace_size``, ``paro_w4_linear_noalloc``, ``paro_rotation_backward``,
 ``paro_rotation_backward_workspace_size``, ``paro_layer_loss``,
-``paro_layer_loss_workspace_size``, ``paro_pairs_random``, ``paro_pairs_by_gap``,
+``paro_layer_loss_workspace_size``, ``paro_w4_linear_act``, ``paro_w4_gated``, their
+``..._backward``, ``paro_adamw_create`` / ``AdamW``, ``paro_pairs_random``, ``paro_pairs_by_gap``,
 ``paro_sparsify_angles``.
 """
 from __future__ import annotations
@@ -47,6 +48,7 @@ def load_library() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -m rotated_w4_linear_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
+    c_f64 = ctypes.c_double
     c_i64, c_i32, vp, c_size = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
     lib.paro_status_string.restype = ctypes.c_char_p
     lib.paro_status_string.argtypes = [ctypes.c_int]
@@ -82,6 +84,28 @@ def load_library() -> ctypes.CDLL:
     lib.paro_layer_loss.restype = ctypes.c_int
     lib.paro_layer_loss.argtypes = [vp, vp, vp, vp, vp, vp, c_i64, c_i64, c_i64, c_i32, vp, vp, vp,
                                     vp, c_size, vp]
+    lib.paro_w4_linear_act.restype = ctypes.c_int
+    lib.paro_w4_linear_act.argtypes = [vp, vp, vp, vp, vp, vp, vp, c_i32, vp, c_i64, c_i64, c_i64, c_i32, vp,
+                                       c_size, vp]
+    lib.paro_w4_gated_workspace_size.restype = c_size
+    lib.paro_w4_gated_workspace_size.argtypes = [vp, c_i64, c_i64, c_i64]
+    lib.paro_w4_gated.restype = ctypes.c_int
+    lib.paro_w4_gated.argtypes = [vp, vp, vp, vp, vp, vp, c_i32, vp, c_i64, c_i64, c_i64, c_i32, vp, c_size, vp]
+    lib.paro_w4_linear_act_backward_workspace_size.restype = c_size
+    lib.paro_w4_linear_act_backward_workspace_size.argtypes = [c_i64, c_i64, c_i64, c_i32]
+    lib.paro_w4_gated_backward_workspace_size.restype = c_size
+    lib.paro_w4_gated_backward_workspace_size.argtypes = [c_i64, c_i64, c_i64]
+    for fn in (lib.paro_w4_linear_act_backward, lib.paro_w4_gated_backward):
+        fn.restype = ctypes.c_int
+        fn.argtypes = [vp, vp, vp, vp, vp, c_i32, vp, vp, vp, c_i64, c_i64, c_i64, c_i32, vp, c_size, vp]
+    lib.paro_adamw_moments.restype = c_i64
+    lib.paro_adamw_moments.argtypes = [c_i32, vp]
+    lib.paro_adamw_create.restype = ctypes.c_int
+    lib.paro_adamw_create.argtypes = [c_i32, vp, vp, c_i32, vp, c_i32, c_i32, vp, vp, vp, vp, ctypes.POINTER(vp)]
+    lib.paro_adamw_destroy.restype = None
+    lib.paro_adamw_destroy.argtypes = [vp]
+    lib.paro_adamw_step.restype = ctypes.c_int
+    lib.paro_adamw_step.argtypes = [vp, c_i64, c_f64, c_f64, c_f64, c_f64, c_f64, vp]
     lib.paro_pairs_random.restype = ctypes.c_int
     lib.paro_pairs_random.argtypes = [c_i64, c_i32, c_i32, ctypes.c_uint64, vp]
     lib.paro_pairs_by_gap.restype = ctypes.c_int
@@ -300,6 +324,220 @@ def paro_layer_loss(r: Rotation, x, w, qweight, scales, zeros, gradients: bool =
         _dptr(dal, "dalpha", torch.float32) if gradients else None, ws_ptr, ws_bytes,
         _stream(stream)))
     return loss, dth, dal
+
+
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _expect(t, name, shape, dtype):
+    """Device pointer of a contiguous tensor of this shape and type on the current device (None: NULL)."""
+    import torch
+    if t is None:
+        return None
+    p = _dptr(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device")
+    return p
+
+
+def _weights(qweight, scales, zeros, rows, d, group):
+    import torch
+    return (_expect(qweight, "qweight", (rows, d // 2), torch.uint8),
+            _expect(scales, "scales", (rows, d // group), torch.float16),
+            _expect(zeros, "zeros", (rows, d // group), torch.uint8))
+
+
+def _workspace(workspace, need, device):
+    import torch
+    if workspace is None:
+        workspace = torch.zeros(need, dtype=torch.uint8, device=device) if need else None
+    if workspace is None:
+        return None, None, 0
+    return workspace, _dptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, residual=None,
+                       act: str = "none", y=None, group: int = 128, workspace=None, stream=None):
+    """Y = act(rot(X) dequant(W)^T + b) + residual (fp16 [M][N]); ``y`` may be ``residual``.
+    The workspace is paro_w4_linear's (``new_workspace``)."""
+    import torch
+    M, d = x.shape
+    N = qweight.shape[0]
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+    need = 0 if workspace is not None else paro_w4_linear_workspace_size(r, M, N, d)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+    _check(load_library().paro_w4_linear_act(
+        _handle(r), _expect(x, "x", (M, d), torch.float16), *_weights(qweight, scales, zeros, N, d, group),
+        _expect(bias, "bias", (N,), torch.float16), _expect(residual, "residual", (M, N), torch.float16), _act(act),
+        _expect(y, "y", (M, N), torch.float16), M, N, d, group, ws_ptr, ws_bytes, _stream(stream)))
+    return y
+
+
+def paro_w4_gated_workspace_size(r: Optional[Rotation], M: int, N: int, d: int) -> int:
+    return int(load_library().paro_w4_gated_workspace_size(_handle(r), M, N, d))
+
+
+def new_gated_workspace(r: Optional[Rotation], M: int, N: int, d: int, device="cuda"):
+    """A zero-filled workspace for paro_w4_gated (None when none is needed)."""
+    return _workspace(None, paro_w4_gated_workspace_size(r, M, N, d), device)[0]
+
+
+def paro_w4_gated(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, act: str = "silu", y=None,
+                  group: int = 128, workspace=None, stream=None):
+    """Y = act(rot(X) Wg^T + bg) * (rot(X) Wu^T + bu) (fp16 [M][N]) on a weight block of 2 N rows
+    (gate, then up: quantize the two weights concatenated along their rows)."""
+    import torch
+    M, d = x.shape
+    N = qweight.shape[0] // 2
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+    need = 0 if workspace is not None else paro_w4_gated_workspace_size(r, M, N, d)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+    _check(load_library().paro_w4_gated(
+        _handle(r), _expect(x, "x", (M, d), torch.float16), *_weights(qweight, scales, zeros, 2 * N, d, group),
+        _expect(bias, "bias", (2 * N,), torch.float16), _act(act), _expect(y, "y", (M, N), torch.float16), M, N, d,
+        group, ws_ptr, ws_bytes, _stream(stream)))
+    return y
+
+
+def new_linear_act_backward_workspace(M: int, N: int, d: int, act: str = "none", device="cuda"):
+    """A zero-filled workspace for paro_w4_linear_act_backward (None when none is needed)."""
+    need = int(load_library().paro_w4_linear_act_backward_workspace_size(M, N, d, _act(act)))
+    return _workspace(None, need, device)[0]
+
+
+def new_gated_backward_workspace(M: int, N: int, d: int, device="cuda"):
+    """A zero-filled workspace for paro_w4_gated_backward (None when none is needed)."""
+    return _workspace(None, int(load_library().paro_w4_gated_backward_workspace_size(M, N, d)), device)[0]
+
+
+def _backward(fn, new_workspace_, rows, cols, computes, x, qweight, scales, zeros, dy, bias, act, dz, dx, want_dx,
+              group, workspace, stream):
+    import torch
+    M, N = dy.shape
+    d = 2 * qweight.shape[1]
+    if dz is None and computes:
+        dz = torch.empty((M, cols), dtype=torch.float16, device=dy.device)
+    if dx is None and want_dx:
+        dx = torch.empty((M, d), dtype=torch.float16, device=dy.device)
+    workspace, ws_ptr, ws_bytes = _workspace(new_workspace_() if workspace is None else workspace, 0, dy.device)
+    _check(fn(_expect(x, "x", (M, d), torch.float16), *_weights(qweight, scales, zeros, rows, d, group),
+              _expect(bias, "bias", (rows,), torch.float16), _act(act), _expect(dy, "dy", (M, N), torch.float16),
+              _expect(dz, "dz", (M, cols), torch.float16), _expect(dx, "dx", (M, d), torch.float16), M, N, d, group,
+              ws_ptr, ws_bytes, _stream(stream)))
+    return dx, dz
+
+
+def paro_w4_linear_act_backward(x, qweight, scales, zeros, dy, bias=None, act: str = "none", dz=None, dx=None,
+                                want_dx: bool = True, group: int = 128, workspace=None, stream=None):
+    """Gradients of paro_w4_linear_act for the transformed activations ``x`` (X'; may be None without
+    activation) and dy = dL/dY: returns (dx fp16 [M][d] or None, dz fp16 [M][N] or None where dZ is dy)."""
+    M, N = dy.shape
+    return _backward(load_library().paro_w4_linear_act_backward,
+                     lambda: new_linear_act_backward_workspace(M, N, 2 * qweight.shape[1], act, dy.device), N, N,
+                     act != "none", x, qweight, scales, zeros, dy, bias, act, dz, dx, want_dx, group, workspace,
+                     stream)
+
+
+def paro_w4_gated_backward(x, qweight, scales, zeros, dy, bias=None, act: str = "silu", dz=None, dx=None,
+                           want_dx: bool = True, group: int = 128, workspace=None, stream=None):
+    """Gradients of paro_w4_gated for the transformed activations ``x`` (X') and dy = dL/dY: returns
+    (dx fp16 [M][d] or None, dz fp16 [M][2N]: the gate's columns, then the up projection's)."""
+    M, N = dy.shape
+    return _backward(load_library().paro_w4_gated_backward,
+                     lambda: new_gated_backward_workspace(M, N, 2 * qweight.shape[1], dy.device), 2 * N, 2 * N,
+                     True, x, qweight, scales, zeros, dy, bias, act, dz, dx, want_dx, group, workspace, stream)
+
+
+def paro_adamw_moments(sizes) -> int:
+    """Values of each moment of tensors of these sizes (each rounded up to 256)."""
+    n = np.ascontiguousarray(np.asarray(list(sizes), dtype=np.int64))
+    total = int(load_library().paro_adamw_moments(len(n), _ptr(n)))
+    if total < 0:
+        raise ValueError("bad tensor sizes")
+    return total
+
+
+class AdamW:
+    """``paro_adamw_create`` / ``paro_adamw_step``: AdamW over a fixed list of tensors.
+
+    ``params`` and ``grads``: contiguous device tensors, one type each (fp32,
+    fp16 or bf16), stepped in place and read where they are; ``m``, ``v`` (and
+    for 8-bit moments ``m_scale``, ``v_scale``): the moments, zero-filled ones
+    are made when they are not given: fp32, or with ``state_bits=8`` e4m3 with
+    fp32 scales (``v`` then holds sqrt(v)).
+    """
+
+    def __init__(self, params, grads, m=None, v=None, m_scale=None, v_scale=None, state_bits: int = 32):
+        import torch
+        params, grads = list(params), list(grads)
+        if len(params) != len(grads) or not params:
+            raise ValueError("params and grads must be lists of the same length, not empty")
+        types = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        ptype, gtype = params[0].dtype, grads[0].dtype
+        if ptype not in types or gtype not in types:
+            raise TypeError("params and grads must be fp32, fp16 or bf16")
+        total = paro_adamw_moments(p.numel() for p in params)
+        if m is not None:
+            state_bits = 8 * m.element_size()
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        state = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        new = lambda n, t: torch.zeros(n, dtype=torch.uint8 if t != torch.float32 else t,  # noqa: E731
+                                       device=params[0].device).view(t)
+        self.m = new(total, state) if m is None else m
+        self.v = new(total, state) if v is None else v
+        self.m_scale, self.v_scale = m_scale, v_scale
+        if state_bits == 8:
+            self.m_scale = new(total // 256, torch.float32) if m_scale is None else m_scale
+            self.v_scale = new(total // 256, torch.float32) if v_scale is None else v_scale
+        elif m_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to 8-bit moments")
+        self.params, self.grads = params, grads  # kept alive: the plan holds their addresses
+        n = np.array([p.numel() for p in params], dtype=np.int64)
+        ptrs = np.array([_expect(p, "a parameter", p.shape, ptype).value or 0 for p in params], dtype=np.uint64)
+        gptrs = np.array([_expect(g, "a gradient", p.shape, gtype).value or 0 for p, g in zip(params, grads)],
+                         dtype=np.uint64)
+        scales = [None if s is None else _expect(s, "a scale", (total // 256,), torch.float32)
+                  for s in (self.m_scale, self.v_scale)]
+        self._device = params[0].device.index
+        h = ctypes.c_void_p()
+        _check(load_library().paro_adamw_create(
+            len(n), _ptr(n), _ptr(ptrs), types[ptype], _ptr(gptrs), types[gtype], state_bits,
+            _expect(self.m, "m", (total,), state), _expect(self.v, "v", (total,), state), *scales, ctypes.byref(h)))
+        self._h = h
+
+    def step(self, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+             stream=None):
+        """Step ``step`` (from 1 on) with the gradients as they are."""
+        import torch
+        if self._device != torch.cuda.current_device():
+            raise ValueError("the tensors must be on the current device")
+        _check(load_library().paro_adamw_step(self._h, step, lr, betas[0], betas[1], eps, weight_decay,
+                                              _stream(stream)))
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            load_library().paro_adamw_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+paro_adamw_create = AdamW
 
 
 def paro_rotation_plan_host(pairs, theta, alpha, group: int) -> Tuple[np.ndarray, dict]:

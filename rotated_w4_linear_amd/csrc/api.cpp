@@ -4,6 +4,7 @@
 #include <string>
 
 #include "paro_internal.h"
+#include "w4_epilogue.h"
 
 namespace paro {
 
@@ -245,7 +246,6 @@ size_t paro_w4_linear_workspace_size(const paro_rotation* r, int64_t M, int64_t 
 }  // extern "C"
 
 namespace paro {
-namespace {
 
 // Argument checks shared by paro_w4_linear and paro_w4_linear_noalloc
 // (everything but the workspace). Returns PARO_OK, or an error with the
@@ -305,17 +305,19 @@ size_t w4_linear_min_workspace(const paro_rotation* r, int64_t M, int64_t N, int
   return kDecodeCounterBytes + (((size_t)M * (size_t)d * 2 + 255) & ~(size_t)255);
 }
 
-// The launches of the W4 linear on a checked workspace ws of ws_bytes bytes
-// (at least w4_linear_min_workspace; NULL when that is 0).
-int run_w4_linear(const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
+// The launches of a W4 product on a checked workspace ws of ws_bytes bytes
+// (at least w4_linear_min_workspace of the weight block's rows; NULL when that
+// is 0). N: output channels.
+int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, uint16_t* y,
                   int64_t M, int64_t N, int64_t d, int32_t group, char* ws, size_t ws_bytes,
                   hipStream_t stream) {
   hipError_t e = hipSuccess;
+  const int64_t P = epi_gated(epi) ? 2 * N : N;  // rows of the weight block
   if (M <= kDecodeMaxM) {
     const paro_rotation* fused = r;
     const uint16_t* xin = x;
-    if (r && !decode_fuses_rotation(r, M, N, d)) {
+    if (r && !decode_fuses_rotation(r, M, P, d)) {
       // stand-alone transform into the workspace tail, then the plain kernel
       uint16_t* xr = (uint16_t*)(ws + ws_bytes - (((size_t)M * (size_t)d * 2 + 255) & ~(size_t)255));
       e = launch_rotate(r, x, xr, M, stream);
@@ -323,7 +325,12 @@ int run_w4_linear(const paro_rotation* r, const uint16_t* x, const uint8_t* qwei
       xin = xr;
       fused = nullptr;
     }
-    e = launch_w4_decode(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, stream);
+    if (epi == kEpiAct)
+      e = launch_w4_decode_act(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, ep, stream);
+    else if (epi == kEpiGated)
+      e = launch_w4_decode_gated(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, ep, stream);
+    else
+      e = launch_w4_decode(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, stream);
   } else {
     const uint16_t* xin = x;
     const size_t xbytes = r ? (((size_t)M * (size_t)d * 2 + 255) & ~(size_t)255) : 0;
@@ -334,16 +341,21 @@ int run_w4_linear(const paro_rotation* r, const uint16_t* x, const uint8_t* qwei
       xin = xr;
     }
     // split-k partial tiles after the counters and X', when the workspace holds them
-    const GemmPlan plan = plan_w4_gemm(M, N, d);
+    const GemmPlan plan = plan_w4_gemm(M, P, d);
     const bool split = plan.partial_bytes && ws && ws_bytes >= kDecodeCounterBytes + xbytes + plan.partial_bytes;
-    e = launch_w4_gemm(xin, qweight, scales, zeros, bias, y, M, N, d, group, split ? (uint32_t*)ws : nullptr,
-                       split ? (float*)(ws + kDecodeCounterBytes + xbytes) : nullptr, stream);
+    uint32_t* cnt = split ? (uint32_t*)ws : nullptr;
+    float* part = split ? (float*)(ws + kDecodeCounterBytes + xbytes) : nullptr;
+    if (epi == kEpiAct)
+      e = launch_w4_gemm_act(xin, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, ep, stream);
+    else if (epi == kEpiGated)
+      e = launch_w4_gemm_gated(xin, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, ep, stream);
+    else
+      e = launch_w4_gemm(xin, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, stream);
   }
   if (e != hipSuccess) return hip_fail(e, "paro_w4_linear launch");
   return PARO_OK;
 }
 
-}  // namespace
 }  // namespace paro
 
 extern "C" {
@@ -365,8 +377,8 @@ int paro_w4_linear(const paro_rotation* r, const uint16_t* x, const uint8_t* qwe
     set_error("paro_w4_linear: workspace must be 256-byte aligned");
     return PARO_ERR_ALIGN;
   }
-  return run_w4_linear(r, x, qweight, scales, zeros, bias, y, M, N, d, group, (char*)workspace,
-                       workspace ? workspace_bytes : 0, stream);
+  return run_w4_product(kEpiPlain, W4Epilogue{}, r, x, qweight, scales, zeros, bias, y, M, N, d, group,
+                        (char*)workspace, workspace ? workspace_bytes : 0, stream);
 }
 
 int paro_w4_linear_noalloc(const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
@@ -392,7 +404,8 @@ int paro_w4_linear_noalloc(const paro_rotation* r, const uint16_t* x, const uint
     set_error("paro_w4_linear_noalloc: paro_device_init has not run on this device");
     return PARO_ERR_UNSUPPORTED;
   }
-  return run_w4_linear(r, x, qweight, scales, zeros, bias, y, M, N, d, group, ws, kNoallocScratchBytes, stream);
+  return run_w4_product(kEpiPlain, W4Epilogue{}, r, x, qweight, scales, zeros, bias, y, M, N, d, group, ws,
+                        kNoallocScratchBytes, stream);
 }
 
 

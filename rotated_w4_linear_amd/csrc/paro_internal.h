@@ -146,6 +146,10 @@ hipError_t launch_nt_gemm_f32(const uint16_t* a, int64_t lda, const uint16_t* b,
 hipError_t launch_nt_gemm_loss(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t d,
                                const uint16_t* yq, uint16_t* dy, int64_t ldd, float* part,
                                hipStream_t stream);
+//  * launch_nt_gemm_f16: C fp16 [M][ldc].
+hipError_t launch_nt_gemm_f16(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb,
+                              int64_t M, int64_t N, int64_t K, uint16_t* c, int64_t ldc,
+                              hipStream_t stream);
 hipError_t launch_transpose_pad(const uint16_t* in, int64_t R, int64_t C, uint16_t* out, int64_t ldo,
                                 hipStream_t stream);
 // Large-batch linear (M > 16) on already transformed activations. The plan
@@ -164,6 +168,12 @@ GemmPlan plan_w4_gemm(int64_t M, int64_t N, int64_t d);
 hipError_t launch_w4_gemm(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                           const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M,
                           int64_t N, int64_t d, int group, uint32_t* cnt, float* part, hipStream_t stream);
+// What an epilogue of the W4 products needs beside the bias: aux, the residual
+// (may be NULL) or dy, fp16 [M][N]; act, a paro_activation.
+struct W4Epilogue {
+  const uint16_t* aux = nullptr;
+  int32_t act = 0;
+};
 // Whether paro_device_init found workgroup b running on XCD b % 8.
 bool xcd_dispatch_is_round_robin();
 
@@ -194,4 +204,72 @@ hipError_t launch_w4_decode(const uint16_t* x, const uint8_t* qweight, const uin
                             const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M,
                             int64_t N, int64_t d, int group, const paro_rotation* r, void* ws,
                             hipStream_t stream);
+// The same kernels with an epilogue (w4_epilogue.h). N: output channels; the
+// gated ones take a weight block of 2 N rows, and launch_w4_gemm_gated_grad
+// writes [M][2 N].
+hipError_t launch_w4_gemm_act(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    uint32_t* cnt, float* part, const W4Epilogue& ep, hipStream_t stream);
+hipError_t launch_w4_gemm_gated(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    uint32_t* cnt, float* part, const W4Epilogue& ep, hipStream_t stream);
+hipError_t launch_w4_gemm_act_grad(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    uint32_t* cnt, float* part, const W4Epilogue& ep, hipStream_t stream);
+hipError_t launch_w4_gemm_gated_grad(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    uint32_t* cnt, float* part, const W4Epilogue& ep, hipStream_t stream);
+hipError_t launch_w4_decode_act(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    const paro_rotation* r, void* ws, const W4Epilogue& ep, hipStream_t stream);
+hipError_t launch_w4_decode_gated(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    const paro_rotation* r, void* ws, const W4Epilogue& ep, hipStream_t stream);
+
+// Gradient of a W4 product at its input (w4_input_grad.hip): dx fp16 [M][d] =
+// dz [M][P] W_hat, P the rows of the weight block (a multiple of 16); ws holds
+// input_grad_scratch_bytes(M, P, d).
+size_t input_grad_scratch_bytes(int64_t M, int64_t P, int64_t d);
+hipError_t launch_w4_input_grad(const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
+                                const uint8_t* zeros, uint16_t* dx, int64_t M, int64_t P, int64_t d, int group,
+                                void* ws, hipStream_t stream);
+
+// One launch of the AdamW step (adamw.hip): up to kAdamTensors tensors, each
+// cut into chunks of kAdamChunk values; chunk0 is the tensor's first chunk of
+// the launch, block0 its first block of 256 moments.
+constexpr int kAdamTensors = 120;
+constexpr int kAdamChunk = 2048;
+struct AdamwTensor {
+  void* p;
+  const void* g;
+  int64_t n;
+  uint32_t chunk0, block0;
+};
+struct AdamwLaunch {
+  AdamwTensor t[kAdamTensors];
+  void *m, *v;
+  float *ms, *vs;
+  float b1, c1, b2, c2;          // b, 1 - b
+  float keep, rate, root, eps;   // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  int32_t count;
+};
+hipError_t launch_adamw(const AdamwLaunch& a, uint32_t chunks, int param_type, int grad_type, bool eight,
+                        hipStream_t stream);
+
+// Shared by the products' entry points (api.cpp): the argument checks (N: rows
+// of the weight block; *noop set when M == 0), the smallest workspace, and the
+// launches of the product with epilogue epi on a checked workspace.
+int check_w4_linear(const char* fn, const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
+                    const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, const uint16_t* y, int64_t M,
+                    int64_t N, int64_t d, int32_t group, bool* noop);
+size_t w4_linear_min_workspace(const paro_rotation* r, int64_t M, int64_t N, int64_t d);
+int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
+                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M,
+                   int64_t N, int64_t d, int32_t group, char* ws, size_t ws_bytes, hipStream_t stream);
 }  // namespace paro

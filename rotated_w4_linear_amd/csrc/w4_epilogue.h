@@ -1,0 +1,176 @@
+// Epilogues of the W4 products: what becomes of Z = X' W_hat^T (fp32) before
+// it is rounded to fp16.
+//   kEpiPlain      y = Z + b
+//   kEpiAct        y = act(Z + b) + R
+//   kEpiGated      y = act(Zg + bg) (Zu + bu), Zg and Zu the first and the
+//                  second N rows of the weight block
+//   kEpiActGrad    dz = dy act'(Z + b)
+//   kEpiGatedGrad  dzg = dy (Zu + bu) act'(Zg + bg), dzu = dy act(Zg + bg)
+// All in fp32 with one rounding to fp16 at the store.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/paro.h"
+#include "w4_common.h"
+
+namespace paro {
+
+enum { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2, kEpiActGrad = 3, kEpiGatedGrad = 4 };
+constexpr bool epi_gated(int epi) { return epi == kEpiGated || epi == kEpiGatedGrad; }
+
+// The activation as the kernels take it: silu and gelu_tanh are both
+// z * sigmoid(u), u = z (a + b z^2) (tanh(t) = 2 sigmoid(2 t) - 1), so one
+// instruction sequence with two coefficients covers them, and none and relu
+// are selected from it; the erf form is compiled separately (ERF).
+struct ActForm {
+  float a, b;
+  int kind;  // 0 none, 1 z sigmoid(u), 2 relu
+};
+
+inline ActForm act_form(int32_t act) {
+  constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+  switch (act) {
+    case PARO_ACT_SILU: return {1.0f, 0.0f, 1};
+    case PARO_ACT_GELU_TANH: return {c, c * 0.044715f, 1};
+    case PARO_ACT_RELU: return {0.0f, 0.0f, 2};
+    default: return {0.0f, 0.0f, 0};
+  }
+}
+
+namespace w4 {
+
+// sigmoid(u): exp2 and rcp of the hardware, each within an ulp or two of
+// fp32, two thousand times finer than the fp16 rounding of the result
+__device__ __forceinline__ float sigmoid(float u) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * u));
+}
+
+// (a NaN passes through every form: the relu keeps what is not below zero)
+template <bool ERF>
+__device__ __forceinline__ float act_value(float z, const ActForm& f) {
+  if constexpr (ERF) return 0.5f * z * erfcf(-0.7071067811865476f * z);
+  const float s = z * sigmoid(z * (f.a + f.b * z * z));
+  const float r = z < 0.0f ? 0.0f : z;
+  return f.kind == 1 ? s : f.kind == 2 ? r : z;
+}
+
+// act(z) and act'(z)
+template <bool ERF>
+__device__ __forceinline__ void act_both(float z, const ActForm& f, float& v, float& dv) {
+  if constexpr (ERF) {
+    const float phi = 0.5f * erfcf(-0.7071067811865476f * z);
+    v = z * phi;
+    dv = phi + z * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.7213475204444817f * z * z);
+  } else {
+    const float s = sigmoid(z * (f.a + f.b * z * z));
+    const float sv = z * s;
+    const float sd = s + sv * (1.0f - s) * (f.a + 3.0f * f.b * z * z);
+    const float r = z < 0.0f ? 0.0f : z;
+    v = f.kind == 1 ? sv : f.kind == 2 ? r : z;
+    dv = f.kind == 1 ? sd : f.kind == 2 ? (z > 0.0f ? 1.0f : 0.0f) : 1.0f;
+  }
+}
+
+// Epilogue of one block of a wavefront's outputs: 64 tokens (rows m0 .. + 63)
+// by NJ tiles of 32 weight rows, get(j, t, e) = Z of tile j, token 32 t +
+// lane % 32, tile row 8 (e / 4) + 4 (lane / 32) + e % 4. Plain weight rows are
+// output channels c0 + 32 j + ...; gated blocks interleave gate and up rows in
+// runs of eight (tile row r: channel 8 (r / 16) + r % 8, up when (r / 8) is
+// odd), so a lane holds both halves of its 16 NJ channels from c0 on.
+// `stage` is this wavefront's own 64 x 32 NJ halfs of LDS: the second operand
+// (residual or dy) comes in and the results go out through it as whole rows
+// (16-byte chunk c of row r at c ^ (r % chunks)), and the lane that reads an
+// element of the second operand replaces it in place by the result, so no
+// rounding happens in between. Its LDS accesses complete in order, so no
+// barrier is needed. y may be aux (every element is read before it is
+// written, by the same wavefront).
+template <int EPI, int NJ, bool ERF, class Get>
+__device__ __forceinline__ void epi_block(uint8_t* stage, Get get, int lane, int m0, int c0, int M, int N,
+                                          const uint16_t* bias, const uint16_t* aux, const ActForm& act, uint16_t* y) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  constexpr bool GT = epi_gated(EPI);
+  constexpr int CO = GT ? 2 * NJ : 4 * NJ;               // chunks of 8 output channels per token
+  constexpr int CR = EPI == kEpiGatedGrad ? 2 * CO : CO;  // chunks per staged row (dzg, then dzu)
+  constexpr int RB = 16 * CR;
+  const int l32 = lane & 31, g = lane >> 5;
+  auto at = [&](int row, int chunk) { return stage + row * RB + ((chunk ^ (row % CR)) << 4); };
+  auto half4 = [](u2 v, float* o) {
+    o[0] = half_lo(v[0]);
+    o[1] = half_hi(v[0]);
+    o[2] = half_lo(v[1]);
+    o[3] = half_hi(v[1]);
+  };
+  auto pack4 = [](const float* o) {
+    return u2{half_bits(o[0]) | (half_bits(o[1]) << 16), half_bits(o[2]) | (half_bits(o[3]) << 16)};
+  };
+  const bool has_aux = EPI == kEpiAct ? aux != nullptr : EPI != kEpiGated;
+  if (has_aux) {
+#pragma unroll
+    for (int rr = 0; rr < CO; ++rr) {
+      const int rl = (64 / CO) * rr + lane / CO, c = lane % CO;
+      const int m = m0 + rl, n = c0 + 8 * c;
+      u4 v = {0u, 0u, 0u, 0u};
+      if (m < M && n < N) v = *(const u4*)(aux + (size_t)m * N + n);
+      *(u4*)at(rl, c) = v;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+    for (int q = 0; q < 4; q += GT ? 2 : 1) {
+      // first of the lane's four channels inside the block
+      const int nl = GT ? 16 * j + 4 * q + 4 * g : 32 * j + 8 * q + 4 * g;
+      float b0[4] = {0.f, 0.f, 0.f, 0.f}, b1[4] = {0.f, 0.f, 0.f, 0.f};
+      if (bias && c0 + nl < N) {
+        half4(*(const u2*)(bias + c0 + nl), b0);
+        if constexpr (GT) half4(*(const u2*)(bias + N + c0 + nl), b1);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int rl = 32 * t + l32;
+        u2* p0 = (u2*)(at(rl, nl >> 3) + (((nl >> 2) & 1) << 3));
+        float o0[4], o1[4], a4[4] = {0.f, 0.f, 0.f, 0.f};
+        if (has_aux) half4(*p0, a4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float z0 = get(j, t, 4 * q + c) + b0[c];
+          if constexpr (EPI == kEpiAct) {
+            o0[c] = act_value<ERF>(z0, act) + a4[c];
+          } else if constexpr (EPI == kEpiActGrad) {
+            float v, dv;
+            act_both<ERF>(z0, act, v, dv);
+            o0[c] = a4[c] * dv;
+          } else {
+            const float z1 = get(j, t, 4 * (q + 1) + c) + b1[c];
+            if constexpr (EPI == kEpiGated) {
+              o0[c] = act_value<ERF>(z0, act) * z1;
+            } else {
+              float v, dv;
+              act_both<ERF>(z0, act, v, dv);
+              o0[c] = a4[c] * z1 * dv;
+              o1[c] = a4[c] * v;
+            }
+          }
+        }
+        *p0 = pack4(o0);
+        if constexpr (EPI == kEpiGatedGrad) *(u2*)(at(rl, CO + (nl >> 3)) + (((nl >> 2) & 1) << 3)) = pack4(o1);
+      }
+    }
+  }
+#pragma unroll
+  for (int rr = 0; rr < CR; ++rr) {
+    const int rl = (64 / CR) * rr + lane / CR, c = lane % CR;
+    const u4 v = *(const u4*)at(rl, c);
+    const int m = m0 + rl, n = c0 + 8 * (c % CO);
+    if (m < M && n < N) {
+      if constexpr (EPI == kEpiGatedGrad) *(u4*)(y + ((size_t)m * 2 + c / CO) * N + n) = v;
+      else *(u4*)(y + (size_t)m * N + n) = v;
+    }
+  }
+}
+
+}  // namespace w4
+}  // namespace paro

@@ -1,0 +1,15 @@
+// Gradient of the W4 linear at its pre-activation (w4_epilogue.h).
+#include "w4_gemm_kernels.h"
+
+#pragma clang fp contract(off)
+
+namespace paro {
+
+hipError_t launch_w4_gemm_act_grad(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    uint32_t* cnt, float* part, const W4Epilogue& ep, hipStream_t stream) {
+  return launch_w4_gemm_epi<kEpiActGrad>(x, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, ep, stream);
+}
+
+}  // namespace paro

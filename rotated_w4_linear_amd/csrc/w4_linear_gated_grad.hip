@@ -1,0 +1,15 @@
+// Gradients of the gated W4 product at its pre-activations (w4_epilogue.h).
+#include "w4_gemm_kernels.h"
+
+#pragma clang fp contract(off)
+
+namespace paro {
+
+hipError_t launch_w4_gemm_gated_grad(
+    const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+    const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
+    uint32_t* cnt, float* part, const W4Epilogue& ep, hipStream_t stream) {
+  return launch_w4_gemm_epi<kEpiGatedGrad>(x, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, ep, stream);
+}
+
+}  // namespace paro
