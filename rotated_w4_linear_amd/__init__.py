@@ -335,33 +335,36 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
-def _expect(t, name, shape, dtype):
-    """Device pointer of a contiguous tensor of this shape and type on the current device (None: NULL)."""
-    import torch
+def _expect(t, name, shape, dtype, device):
+    """Address of a contiguous tensor of this shape and type on this device (None: NULL)."""
     if t is None:
         return None
-    p = _dptr(t, name, dtype)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _dptr(t, name, dtype)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device")
-    return p
+    raise ValueError(f"{name} must be on the current device")
 
 
-def _weights(qweight, scales, zeros, rows, d, group):
+def _raw_stream(stream, device):
+    """Handle of ``stream``, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    return (_expect(qweight, "qweight", (rows, d // 2), torch.uint8),
-            _expect(scales, "scales", (rows, d // group), torch.float16),
-            _expect(zeros, "zeros", (rows, d // group), torch.uint8))
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _workspace(workspace, need, device):
+    """(workspace, its address, its bytes); a zero-filled one of ``need`` bytes where none is given."""
     import torch
     if workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=device) if need else None
-    if workspace is None:
-        return None, None, 0
-    return workspace, _dptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        if not need:
+            return None, None, 0
+        workspace = torch.zeros(need, dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, residual=None,
@@ -375,10 +378,12 @@ def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=No
         y = torch.empty((M, N), dtype=torch.float16, device=x.device)
     need = 0 if workspace is not None else paro_w4_linear_workspace_size(r, M, N, d)
     workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+    dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     _check(load_library().paro_w4_linear_act(
-        _handle(r), _expect(x, "x", (M, d), torch.float16), *_weights(qweight, scales, zeros, N, d, group),
-        _expect(bias, "bias", (N,), torch.float16), _expect(residual, "residual", (M, N), torch.float16), _act(act),
-        _expect(y, "y", (M, N), torch.float16), M, N, d, group, ws_ptr, ws_bytes, _stream(stream)))
+        _handle(r), _expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (N, d // 2), u8, dev),
+        _expect(scales, "scales", (N, d // group), f16, dev), _expect(zeros, "zeros", (N, d // group), u8, dev),
+        _expect(bias, "bias", (N,), f16, dev), _expect(residual, "residual", (M, N), f16, dev), _act(act),
+        _expect(y, "y", (M, N), f16, dev), M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
     return y
 
 
@@ -402,10 +407,12 @@ def paro_w4_gated(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, a
         y = torch.empty((M, N), dtype=torch.float16, device=x.device)
     need = 0 if workspace is not None else paro_w4_gated_workspace_size(r, M, N, d)
     workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+    dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     _check(load_library().paro_w4_gated(
-        _handle(r), _expect(x, "x", (M, d), torch.float16), *_weights(qweight, scales, zeros, 2 * N, d, group),
-        _expect(bias, "bias", (2 * N,), torch.float16), _act(act), _expect(y, "y", (M, N), torch.float16), M, N, d,
-        group, ws_ptr, ws_bytes, _stream(stream)))
+        _handle(r), _expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (2 * N, d // 2), u8, dev),
+        _expect(scales, "scales", (2 * N, d // group), f16, dev),
+        _expect(zeros, "zeros", (2 * N, d // group), u8, dev), _expect(bias, "bias", (2 * N,), f16, dev), _act(act),
+        _expect(y, "y", (M, N), f16, dev), M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
     return y
 
 
@@ -430,10 +437,12 @@ def _backward(fn, new_workspace_, rows, cols, computes, x, qweight, scales, zero
     if dx is None and want_dx:
         dx = torch.empty((M, d), dtype=torch.float16, device=dy.device)
     workspace, ws_ptr, ws_bytes = _workspace(new_workspace_() if workspace is None else workspace, 0, dy.device)
-    _check(fn(_expect(x, "x", (M, d), torch.float16), *_weights(qweight, scales, zeros, rows, d, group),
-              _expect(bias, "bias", (rows,), torch.float16), _act(act), _expect(dy, "dy", (M, N), torch.float16),
-              _expect(dz, "dz", (M, cols), torch.float16), _expect(dx, "dx", (M, d), torch.float16), M, N, d, group,
-              ws_ptr, ws_bytes, _stream(stream)))
+    dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
+    _check(fn(_expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (rows, d // 2), u8, dev),
+              _expect(scales, "scales", (rows, d // group), f16, dev),
+              _expect(zeros, "zeros", (rows, d // group), u8, dev), _expect(bias, "bias", (rows,), f16, dev),
+              _act(act), _expect(dy, "dy", (M, N), f16, dev), _expect(dz, "dz", (M, cols), f16, dev),
+              _expect(dx, "dx", (M, d), f16, dev), M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
     return dx, dz
 
 
@@ -504,16 +513,16 @@ class AdamW:
             raise ValueError("scales belong to 8-bit moments")
         self.params, self.grads = params, grads  # kept alive: the plan holds their addresses
         n = np.array([p.numel() for p in params], dtype=np.int64)
-        ptrs = np.array([_expect(p, "a parameter", p.shape, ptype).value or 0 for p in params], dtype=np.uint64)
-        gptrs = np.array([_expect(g, "a gradient", p.shape, gtype).value or 0 for p, g in zip(params, grads)],
+        self._device = dev = torch.cuda.current_device()
+        ptrs = np.array([_expect(p, "a parameter", p.shape, ptype, dev) for p in params], dtype=np.uint64)
+        gptrs = np.array([_expect(g, "a gradient", p.shape, gtype, dev) for p, g in zip(params, grads)],
                          dtype=np.uint64)
-        scales = [None if s is None else _expect(s, "a scale", (total // 256,), torch.float32)
-                  for s in (self.m_scale, self.v_scale)]
-        self._device = params[0].device.index
+        scales = [_expect(s, "a scale", (total // 256,), torch.float32, dev) for s in (self.m_scale, self.v_scale)]
         h = ctypes.c_void_p()
         _check(load_library().paro_adamw_create(
             len(n), _ptr(n), _ptr(ptrs), types[ptype], _ptr(gptrs), types[gtype], state_bits,
-            _expect(self.m, "m", (total,), state), _expect(self.v, "v", (total,), state), *scales, ctypes.byref(h)))
+            _expect(self.m, "m", (total,), state, dev), _expect(self.v, "v", (total,), state, dev), *scales,
+            ctypes.byref(h)))
         self._h = h
 
     def step(self, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
@@ -523,7 +532,7 @@ class AdamW:
         if self._device != torch.cuda.current_device():
             raise ValueError("the tensors must be on the current device")
         _check(load_library().paro_adamw_step(self._h, step, lr, betas[0], betas[1], eps, weight_decay,
-                                              _stream(stream)))
+                                              _raw_stream(stream, self._device)))
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:

@@ -84,7 +84,7 @@ int run_backward(const char* fn, bool gated, const uint16_t* x, const uint8_t* q
   }
   const int64_t P = gated ? 2 * N : N;
   const bool product = gated || act != PARO_ACT_NONE;  // whether dz has to be computed
-  if (P > (int64_t(1) << 22)) return fail(PARO_ERR_UNSUPPORTED, f + ": at most 2^22 weight rows");
+  if (P > (int64_t(1) << 21)) return fail(PARO_ERR_UNSUPPORTED, f + ": at most 2^21 weight rows");
   // (x and dz are not read when dz is dy itself: dy stands in for them in the checks)
   bool noop = false;
   const int st = check_w4_linear(fn, nullptr, product ? x : dy, qweight, scales, zeros, product ? bias : nullptr,
@@ -112,14 +112,15 @@ int run_backward(const char* fn, bool gated, const uint16_t* x, const uint8_t* q
     if (e != hipSuccess) return hip_fail(e, fn);
   }
   if (dx) {
-    e = launch_w4_input_grad(product ? dz : dy, qweight, scales, zeros, dx, M, P, d, group, ws + first, stream);
+    e = launch_w4_input_grad(product ? dz : dy, qweight, scales, zeros, dx, M, P, d, group, (uint32_t*)ws, ws + first,
+                             stream);
     if (e != hipSuccess) return hip_fail(e, fn);
   }
   return PARO_OK;
 }
 
 size_t backward_size(bool gated, int64_t M, int64_t N, int64_t d, int32_t act) {
-  if (M <= 0 || N <= 0 || d <= 0 || N > (int64_t(1) << 22) || d > (int64_t(1) << 22)) return 0;
+  if (M <= 0 || N <= 0 || d <= 0 || N > (int64_t(1) << 21) || d > (int64_t(1) << 22)) return 0;
   const int64_t P = gated ? 2 * N : N;
   return product_scratch(gated || act != PARO_ACT_NONE, M, P, d) + input_grad_scratch_bytes(M, P, d);
 }

@@ -41,14 +41,13 @@ constexpr int DG_M = 128, DG_N = 128, DG_K = 64;
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
 constexpr int kWaitVmLgkm0 = 0x70;      // s_waitcnt vmcnt(0) lgkmcnt(0)
 
-enum { EPI_STORE_F32 = 0, EPI_LOSS = 1, EPI_STORE_F16 = 2 };
+enum { EPI_STORE_F32 = 0, EPI_LOSS = 1 };
 
 __device__ __forceinline__ uint16_t f16_bits(float f) {
   return __builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
-// EPI_STORE_F32: c[m * ldc + n] = acc (fp32). EPI_STORE_F16: dy[m * ldd + n] =
-// fp16(acc).
+// EPI_STORE_F32: c[m * ldc + n] = acc (fp32).
 // EPI_LOSS: part[tile] = sum over the tile of (yq[m][n] - acc)^2 (fixed
 // order), and with dy != NULL dy[m * ldd + n] = fp16(2 (yq - acc)) for n < N,
 // 0 for N <= n < ldd.
@@ -145,7 +144,7 @@ void nt_gemm_kernel(const uint16_t* __restrict__ a, int lda, const uint16_t* __r
   }
 
   // acc[mm][nn][e] = C[m = m0 + 64 wm + 32 mm + 8 (e / 4) + 4 g + e % 4][n = n0 + 64 wn + 32 nn + l32]
-  if constexpr (EPI == EPI_STORE_F32 || EPI == EPI_STORE_F16) {
+  if constexpr (EPI == EPI_STORE_F32) {
 #pragma unroll
     for (int mm = 0; mm < 2; ++mm)
 #pragma unroll
@@ -154,10 +153,7 @@ void nt_gemm_kernel(const uint16_t* __restrict__ a, int lda, const uint16_t* __r
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int m = m0 + 64 * wm + 32 * mm + 8 * (e >> 2) + 4 * g + (e & 3);
-          if (m < M && n < N) {
-            if constexpr (EPI == EPI_STORE_F32) c[(size_t)m * ldc + n] = acc[mm][nn][e];
-            else dy[(size_t)m * ldd + n] = f16_bits(acc[mm][nn][e]);
-          }
+          if (m < M && n < N) c[(size_t)m * ldc + n] = acc[mm][nn][e];
         }
       }
   } else {
@@ -247,14 +243,6 @@ hipError_t launch_nt_gemm_f32(const uint16_t* a, int64_t lda, const uint16_t* b,
   if (M == 0 || N == 0) return hipSuccess;
   return launch_nt<EPI_STORE_F32>(a, (int)lda, b, (int)ldb, (int)M, (int)N, (int)K, c, (int)ldc,
                                   nullptr, nullptr, 0, nullptr, stream);
-}
-
-hipError_t launch_nt_gemm_f16(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb,
-                              int64_t M, int64_t N, int64_t K, uint16_t* c, int64_t ldc,
-                              hipStream_t stream) {
-  if (M == 0 || N == 0) return hipSuccess;
-  return launch_nt<EPI_STORE_F16>(a, (int)lda, b, (int)ldb, (int)M, (int)N, (int)K, nullptr, 0, nullptr, c,
-                                  (int)ldc, nullptr, stream);
 }
 
 hipError_t launch_nt_gemm_loss(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t d,

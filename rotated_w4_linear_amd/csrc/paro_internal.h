@@ -146,10 +146,6 @@ hipError_t launch_nt_gemm_f32(const uint16_t* a, int64_t lda, const uint16_t* b,
 hipError_t launch_nt_gemm_loss(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t d,
                                const uint16_t* yq, uint16_t* dy, int64_t ldd, float* part,
                                hipStream_t stream);
-//  * launch_nt_gemm_f16: C fp16 [M][ldc].
-hipError_t launch_nt_gemm_f16(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb,
-                              int64_t M, int64_t N, int64_t K, uint16_t* c, int64_t ldc,
-                              hipStream_t stream);
 hipError_t launch_transpose_pad(const uint16_t* in, int64_t R, int64_t C, uint16_t* out, int64_t ldo,
                                 hipStream_t stream);
 // Large-batch linear (M > 16) on already transformed activations. The plan
@@ -233,12 +229,12 @@ hipError_t launch_w4_decode_gated(
     const paro_rotation* r, void* ws, const W4Epilogue& ep, hipStream_t stream);
 
 // Gradient of a W4 product at its input (w4_input_grad.hip): dx fp16 [M][d] =
-// dz [M][P] W_hat, P the rows of the weight block (a multiple of 16); ws holds
-// input_grad_scratch_bytes(M, P, d).
+// dz [M][P] W_hat, P the rows of the weight block (a multiple of 16); cnt are
+// arrival counters (zero between calls), ws holds input_grad_scratch_bytes(M, P, d).
 size_t input_grad_scratch_bytes(int64_t M, int64_t P, int64_t d);
 hipError_t launch_w4_input_grad(const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
                                 const uint8_t* zeros, uint16_t* dx, int64_t M, int64_t P, int64_t d, int group,
-                                void* ws, hipStream_t stream);
+                                uint32_t* cnt, void* ws, hipStream_t stream);
 
 // One launch of the AdamW step (adamw.hip): up to kAdamTensors tensors, each
 // cut into chunks of kAdamChunk values; chunk0 is the tensor's first chunk of

@@ -181,6 +181,6 @@ def test_python_refusals(paro):
     with pytest.raises(ValueError, match="act"):
         paro._act("swish")
     with pytest.raises(TypeError):
-        paro._expect(torch.zeros(4), "x", (4,), torch.float32)   # not a device tensor
+        paro._expect(torch.zeros(4), "x", (4,), torch.float32, 0)   # not a device tensor
     with pytest.raises(ValueError):
         paro.AdamW([], [])

@@ -148,7 +148,8 @@ def test_gated(paro, M, d, N, G):
 
 GRADS = [(1, 128, 16, 128), (2, 640, 80, 64), (16, 1024, 528, 128), (64, 512, 272, 256), (65, 2560, 1040, 64),
          (130, 4096, 256, 128), (333, 768, 2064, 256), (1000, 1024, 4112, 128), (2048, 8192, 2048, 128),
-         (2600, 512, 4368, 128)]
+         (2600, 512, 4368, 128),
+         (2048, 4096, 4096, 128), (700, 384, 12304, 128), (3, 4096, 8192, 128)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
