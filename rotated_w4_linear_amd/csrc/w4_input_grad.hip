@@ -8,6 +8,7 @@
 // contraction index is contiguous. W_hat^T costs 2.5 P d bytes moved whatever
 // M is.
 #include <algorithm>
+#include <type_traits>
 
 #include "paro_internal.h"
 #include "w4_common.h"
@@ -91,14 +92,18 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const u4* __restrict__ in
 //   <4, 4, 2>  256 (n) x 256 (m) per workgroup: 8 operand reads per 16 MFMAs;
 //   <4, 2, 2>  256 (n) x 128 (m);
 //   <2, 2, 4>  256 (n) x 64 (m), for few tokens.
-// k-tiles of 64 of both operands go straight from global memory into two LDS
-// stages (16-byte load-to-LDS DMA; row r keeps its chunk c at c ^ ((r >> 1) &
-// 7), which spreads the 16 rows of an operand read over all 16-byte
-// positions). While the MFMAs of a 16-wide step run, the wavefront reads the
-// next step's operands; after step 2 it waits for the DMA of the next k-tile
-// and the barrier, and step 3 reads that k-tile's first operands and sends the
-// DMA of the one after it into the stage that nobody reads any more, so a DMA
-// has a whole k-tile to land.
+// k-tiles of 64 of both operands go straight from global memory into LDS
+// (16-byte load-to-LDS DMA; row r keeps its chunk c at c ^ ((r >> 1) & 7), which
+// spreads the 16 rows of an operand read over all 16-byte positions), wt into a
+// ring of three stages, dz into one of two. While the MFMAs of a 16-wide step
+// run, the wavefront reads the next step's operands; after step 2 of k-tile kt
+// it waits for the operands of kt + 1 and the barrier, and step 3 reads the
+// first of them. Nobody reads the stages of kt any more then: step 3 sends dz
+// of kt + 2, and steps 0 and 1 of the next k-tile wt of kt + 3. The loads take
+// the CU's path of 64 bytes a cycle for half of the MFMAs' time; all in step 3,
+// as two stages of each operand would have it, they hold it for twice its
+// length (matrix cores busy 48%), and k-tiles of 32 in four stages read half
+// lines (59%, at a lower clock for the doubled L2 requests).
 // k may be split over ksplit workgroups of one tile (consecutive slots of one
 // XCD): fp32 partial tiles in the workspace, the last to arrive adds them in
 // split order, as in the W4 kernels.
@@ -106,7 +111,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const u4* __restrict__ in
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int IG_N = 256, IG_K = 64;
+constexpr int IG_N = 256, IG_K = 64;  // channels per workgroup, k-tile
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
 constexpr int kWaitVmLgkm0 = 0x70;      // s_waitcnt vmcnt(0) lgkmcnt(0)
 constexpr int kAuxL2R = 1;              // sc0: skip the per-CU cache
@@ -121,9 +126,8 @@ void input_grad_kernel(const uint16_t* __restrict__ wt, const uint16_t* __restri
   static_assert(32 * TN * NWN == IG_N, "256 channels per workgroup");
   constexpr int CA = IG_N / 32, CB = BM / 32;  // load-to-LDS instructions per lane and k-tile
   constexpr int NF = TN * TM;                  // MFMAs per step
-  __shared__ __attribute__((aligned(1024))) _Float16 A0[IG_N * IG_K], A1[IG_N * IG_K];
+  __shared__ __attribute__((aligned(1024))) _Float16 A0[IG_N * IG_K], A1[IG_N * IG_K], A2[IG_N * IG_K];
   __shared__ __attribute__((aligned(1024))) _Float16 B0[BM * IG_K], B1[BM * IG_K];
-  __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = w % NWN, wm = w / NWN;
@@ -156,14 +160,17 @@ void input_grad_kernel(const uint16_t* __restrict__ wt, const uint16_t* __restri
     const int r = 8 * (CB * w + c) + (lane >> 3);
     boff[c] = (uint32_t)(min(r, M - 1 - m0) * pp + 8 * ((lane & 7) ^ ((r >> 1) & 7))) * 2u;
   }
-  // quarter q of a k-tile's DMA
-  auto dma4 = [&](int q, int kt, _Float16* as, _Float16* bs) {
-    const int k = (kt0 + kt) * IG_K * 2;
+  // (past the last k-tile: the last one again, into a stage nobody reads)
+  auto dma_a = [&](int kt, int half, _Float16* as) {  // in two halves
+    const int k = (kt0 + min(kt, KT - 1)) * IG_K * 2;
 #pragma unroll
-    for (int c = CA / 4 * q; c < CA / 4 * (q + 1); ++c)
+    for (int c = CA / 2 * half; c < CA / 2 * (half + 1); ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)&as[(CA * w + c) * 512], 16, aoff[c], k, 0, 0);
+  };
+  auto dma_b = [&](int kt, _Float16* bs) {
+    const int k = (kt0 + min(kt, KT - 1)) * IG_K * 2;
 #pragma unroll
-    for (int c = CB * q / 4; c < CB * (q + 1) / 4; ++c)
+    for (int c = 0; c < CB; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)&bs[(CB * w + c) * 512], 16, boff[c], k, 0, 0);
   };
   f16v acc[4][4];
@@ -186,55 +193,74 @@ void input_grad_kernel(const uint16_t* __restrict__ wt, const uint16_t* __restri
       b[i] = *(const h8*)(bs + r * IG_K + 8 * ((4 * g + s) ^ ((r >> 1) & 7)));
     }
   };
-  auto mma = [&](int f0, int f1, const h8* a, const h8* b) {
-#pragma unroll
-    for (int f = f0; f < f1; ++f)
-      acc[f / TM][f % TM] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[f / TM], b[f % TM], acc[f / TM][f % TM], 0, 0, 0);
-  };
+  // one step: its MFMAs on the operands in hand, behind the next step's reads,
+  // with NL loads spread among them
   h8 a[4], b[4], an[4], bn[4];
-  auto next = [&]() {
+  auto step = [&](auto loads) {
+    constexpr int NL = decltype(loads)::value, PER = NL == 0 || NF < NL ? 1 : NF / (NL == 0 ? 1 : NL);
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+      acc[f / TM][f % TM] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[f / TM], b[f % TM], acc[f / TM][f % TM], 0, 0, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
+#pragma unroll
+    for (int c = 0; c < NL; ++c) {
+      __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+      __builtin_amdgcn_sched_group_barrier(0x004, 1, 0);  // the load's M0 write
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (t < TN) a[t] = an[t];
       if (t < TM) b[t] = bn[t];
     }
   };
-  auto ktile = [&](int kt, _Float16* as, _Float16* bs, const _Float16* as1, const _Float16* bs1) {
+  // s_waitcnt with lgkmcnt(0) and vmcnt(v): at most v loads still on their way
+  constexpr auto wait_vm = [](int v) { return 0x70 | (v & 15) | ((v >> 4) << 14); };
+  // k-tile kt in (as, bs), kt + 1 in (as1, bs1); ap: the wt stage of kt - 1,
+  // which kt + 2 takes
+  auto ktile = [&](int kt, _Float16* ap, const _Float16* as, _Float16* bs, const _Float16* as1, const _Float16* bs1) {
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
+      if (s < 2) dma_a(kt + 2, s, ap);
       read(as, bs, s + 1, an, bn);
-      mma(0, NF, a, b);
-      __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, NF, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      next();
+      if (s < 2) step(std::integral_constant<int, CA / 2>{});
+      else step(std::integral_constant<int, 0>{});
     }
-    __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
+    // still on their way: wt of kt + 2
+    __builtin_amdgcn_s_waitcnt(wait_vm(CA));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const int kd = min(kt + 2, KT - 1);  // (past the end: the last k-tile again, into a stage nobody reads)
+    dma_b(kt + 2, bs);
     read(as1, bs1, 0, an, bn);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      mma(NF * q / 4, NF * (q + 1) / 4, a, b);
-      __builtin_amdgcn_sched_barrier(0);
-      dma4(q, kd, as, bs);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    next();
+    step(std::integral_constant<int, CB>{});
   };
 
-#pragma unroll
-  for (int q = 0; q < 4; ++q) dma4(q, 0, A0, B0);
-  __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
+  dma_a(0, 0, A0);
+  dma_a(0, 1, A0);
+  dma_b(0, B0);
+  dma_a(1, 0, A1);
+  dma_a(1, 1, A1);
+  dma_b(1, B1);
+  __builtin_amdgcn_s_waitcnt(wait_vm(CA + CB));
   __builtin_amdgcn_s_barrier();
-#pragma unroll
-  for (int q = 0; q < 4; ++q) dma4(q, 1, A1, B1);
   read(A0, B0, 0, a, b);
-  for (int kt = 0; kt < KT; kt += 2) {  // KT even: p is padded to whole pairs
-    ktile(kt, A0, B0, A1, B1);
-    ktile(kt + 1, A1, B1, A0, B0);
+  int kt = 0;
+  for (; kt + 6 <= KT; kt += 6) {  // both rings' periods; KT is even (p is padded to pairs)
+    ktile(kt, A2, A0, B0, A1, B1);
+    ktile(kt + 1, A0, A1, B1, A2, B0);
+    ktile(kt + 2, A1, A2, B0, A0, B1);
+    ktile(kt + 3, A2, A0, B1, A1, B0);
+    ktile(kt + 4, A0, A1, B0, A2, B1);
+    ktile(kt + 5, A1, A2, B1, A0, B0);
+  }
+  if (kt < KT) {
+    ktile(kt, A2, A0, B0, A1, B1);
+    ktile(kt + 1, A0, A1, B1, A2, B0);
+  }
+  if (kt + 2 < KT) {
+    ktile(kt + 2, A1, A2, B0, A0, B1);
+    ktile(kt + 3, A2, A0, B1, A1, B0);
   }
   __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);  // the last DMA writes a stage that is used below
   __builtin_amdgcn_s_barrier();
@@ -256,6 +282,7 @@ void input_grad_kernel(const uint16_t* __restrict__ wt, const uint16_t* __restri
     }
     __builtin_amdgcn_s_waitcnt(0);  // this wavefront's stores have reached L2 / memory
     __syncthreads();
+    volatile uint32_t& s_last = *(uint32_t*)B0;  // (the stages take all of LDS, and the epilogue uses A0)
     if (tid == 0) {
       uint32_t old;
       if (sys) old = __hip_atomic_fetch_add(&cnt[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
