@@ -72,6 +72,8 @@ constexpr int kAuxL2R = 1;
 constexpr int kAuxSysW = 17;
 // s_waitcnt immediate (gfx9 encoding): vmcnt(0) lgkmcnt(0), expcnt untouched
 constexpr int kWaitVmLgkm0 = 0x70;
+// vmcnt(8) lgkmcnt(0)
+constexpr int kWaitVm8Lgkm0 = 0x78;
 // lgkmcnt(0) alone (vmcnt and expcnt at their maxima)
 constexpr int kWaitLgkm0 = 0xC07F;
 // Output tiles (at 128 tokens) below which 64-token tiles are used: measured
@@ -470,9 +472,9 @@ constexpr int kModeTile = 0, kModeSkOne = 1, kModeSkMany = 2;
 // Instruction order inside a scheduling region of 16 MFMAs: the region's ND
 // LDS reads first, the first NW MFMAs alone (while those reads return), then
 // each MFMA followed by up to NV vector instructions (the next step's
-// dequantization); the first NG MFMAs are each followed by one global load
-// (the DMA of a k-tile), so that issuing the loads, which holds the
-// wavefront's in-order issue, overlaps running MFMAs.
+// dequantization); NG global loads (part of a k-tile's DMA) are spread evenly
+// among the MFMAs, so that issuing the loads, which holds the wavefront's
+// in-order issue, overlaps running MFMAs.
 // One chunk of four MFMAs: the chunk's ND LDS reads first, then each MFMA
 // followed by up to NV vector instructions and, for the first NG, one global
 // load with the scalar write of its LDS address (M0) before it.
@@ -497,7 +499,7 @@ __device__ __forceinline__ void sched_order() {
   for (int k = 0; k < 16; ++k) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if (k >= NW) __builtin_amdgcn_sched_group_barrier(0x002, NV, 0);
-    if (k < NG) {
+    if (NG > 0 && k % (16 / (NG > 0 ? NG : 1)) == 0) {
       __builtin_amdgcn_sched_group_barrier(0x004, 1, 0);  // the load's M0 write
       __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
@@ -525,7 +527,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
                          int d, int gsh, int mblk, int nblk, int slots, float* __restrict__ part,
                          uint32_t* __restrict__ cnt, int sys, const uint16_t* aux, ActForm act, int erf) {
   constexpr bool GT = epi_gated(EPI);
-  __shared__ __attribute__((aligned(1024))) _Float16 X0[GW_XSTAGE], X1[GW_XSTAGE];
+  __shared__ __attribute__((aligned(1024))) _Float16 X0[GW_XSTAGE], X1[GW_XSTAGE], X2[GW_XSTAGE];
   __shared__ __attribute__((aligned(1024))) u4 W0[GB_WSTAGE], W1[GB_WSTAGE];
   __shared__ __attribute__((aligned(16))) uint32_t S0[GB_N], S1[GB_N], Z0[GB_N], Z1[GB_N];
   // PANEL: the tile's scales and zeros of the groups a segment's k-tiles span
@@ -534,7 +536,6 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // spans are consecutive in LDS
   __shared__ __attribute__((aligned(1024))) uint16_t SPT[PANEL ? GB_N * kPanelGroups : 8];
   __shared__ __attribute__((aligned(1024))) uint8_t ZPT[PANEL ? GB_N * kPanelGroups : 16];
-  __shared__ uint32_t s_last;
   constexpr bool SK = MODE != kModeTile;
   const int tid_k = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid_k >> 6);  // wavefront 0..3
@@ -602,30 +603,26 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // group scale and zero: lane l of wavefront w fetches row 64 w + l
   const uint32_t szrow = (uint32_t)(weight_row<GT>(64 * w + lane, N, nw0) * groups);
 
-  // the DMA of one k-tile: twelve load-to-LDS instructions per lane (ten
-  // with PANEL: no scale and zero); dma3(q) issues instructions 3 q .. 3 q + 2
-  auto dma3 = [&](int q, int ktl, _Float16* xs, u4* ws, uint32_t* ss_l, uint32_t* zs_l) {
-    const int kt = kt0 + ktl;  // global k-tile
-    const uint32_t gi = (uint32_t)(kt >> gsh);
+  // the DMA of one k-tile: the X' rows in two halves of four load-to-LDS
+  // instructions per lane, then the codes (two) and, without PANEL, the scales
+  // and zeros (two more)
+  auto dma_x = [&](int half, int ktl, _Float16* xs) {
 #pragma unroll
-    for (int c0 = 3 * q; c0 < 3 * q + 3; ++c0) {
-      const int c = c0 + (PANEL ? 2 : 0);
-      if (c >= 12) break;
-      if (c == 0)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)&ss_l[64 * w], 2, (szrow + gi) * 2u, 0, 0, 0);
-      else if (c == 1)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rz, (lds_void*)&zs_l[64 * w], 1, szrow + gi, 0, 0, 0);
-      else if (c < 10)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)&xs[(8 * w + c - 2) * 64 * 8], 16, xoff[c - 2],
-                                                 kt * GB_K * 2, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)&ws[(2 * w + c - 10) * 64], 16, woff[c - 10],
-                                                 kt * (GB_K / 2), 0, 0);
-    }
+    for (int c = 4 * half; c < 4 * half + 4; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)&xs[(8 * w + c) * 64 * 8], 16, xoff[c],
+                                               (kt0 + ktl) * GB_K * 2, 0, 0);
   };
-  auto dma = [&](int kt, _Float16* xs, u4* ws, uint32_t* ss_l, uint32_t* zs_l) {
+  auto dma_w = [&](int ktl, u4* ws, uint32_t* ss_l, uint32_t* zs_l) {
+    const int kt = kt0 + ktl;  // global k-tile
 #pragma unroll
-    for (int q = 0; q < 4; ++q) dma3(q, kt, xs, ws, ss_l, zs_l);
+    for (int c = 0; c < 2; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)&ws[(2 * w + c) * 64], 16, woff[c], kt * (GB_K / 2), 0,
+                                               0);
+    if constexpr (!PANEL) {
+      const uint32_t gi = (uint32_t)(kt >> gsh);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)&ss_l[64 * w], 2, (szrow + gi) * 2u, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rz, (lds_void*)&zs_l[64 * w], 1, szrow + gi, 0, 0, 0);
+    }
   };
 
   // (arrays are sized for the largest WN and MTW and used up to WN, MTW: the
@@ -711,19 +708,27 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // and dequantizes the operands of step i + 1. After step 2 it waits for the
   // DMA of k-tile kt + 1 and the barrier, so that step 3 overlaps the first
   // operands of kt + 1 (read from the other stage). Past that barrier every
-  // wavefront has read all it needs of k-tile kt, so the DMA of kt + 2 into
-  // kt's stage goes out there, a whole k-tile before it is waited for; past
-  // the last tile it reloads the last tile, which is read but not used.
+  // wavefront has read all it needs of k-tile kt: step 3 sends the codes of kt +
+  // 2 into kt's stage, and steps 0 and 1 of the next k-tile the X' rows of kt +
+  // 3 into kt's X' stage, of which there are three. The loads of four
+  // wavefronts pass at 64 bytes a cycle; all of them in step 3, as two X' stages
+  // would have it, take longer than its MFMAs. Past the last tile the DMA
+  // reloads the last tile, which is read but not used.
   Params P, Pn;
   h8 a[4], b[8], an[4], bn[8];
-  auto tile = [&](int kt, _Float16* xb, u4* wl, uint32_t* sb, uint32_t* zb, const _Float16* xn,
+  // k-tile kt in (xb, wl, sb, zb), kt + 1 in (xn, wnx, sn, zn); xp: the X' stage
+  // of kt - 1, which kt + 2 takes
+  auto tile = [&](int kt, _Float16* xp, const _Float16* xb, u4* wl, uint32_t* sb, uint32_t* zb, const _Float16* xn,
                   const u4* wnx, const uint32_t* sn, const uint32_t* zn) {
+    const int kd = min(kt + 2, KT - 1);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
+      if (i < 2) dma_x(i, kd, xp);
       read_b(xb, i + 1, bn);
       deq(P, i + 1, an);
       mma(a, b);
-      sched_order<MTW, 0, WN + 1, 0>();
+      if (i < 2) sched_order<MTW, 0, WN + 1, 4>();
+      else sched_order<MTW, 0, WN + 1, 0>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
@@ -731,35 +736,31 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
         if (t < MTW) b[t] = bn[t];
       }
     }
-    __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
+    __builtin_amdgcn_s_waitcnt(kWaitVm8Lgkm0);  // still on their way: the X' rows of kt + 2
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    // step 3 in four chunks of four MFMAs, each with three of the twelve
-    // loads of the DMA of kt + 2 and a share of kt + 1's operand work
-    const int kd = min(kt + 2, KT - 1);
+    // step 3 in four chunks of four MFMAs, the first with the codes' DMA of kt +
+    // 2, each with a share of kt + 1's operand work
     Raw raw;
     read_raw(kt + 1, wnx, sn, zn, raw);
     read_b(xn, 0, bn);
     mma4(0, a, b);
-    dma3(0, kd, xb, wl, sb, zb);
-    sched_chunk<MTW + 3 * WN, 0, 3>();
+    dma_w(kd, wl, sb, zb);
+    sched_chunk<MTW + 3 * WN, 0, PANEL ? 2 : 4>();
     __builtin_amdgcn_sched_barrier(0);
     convert(raw, Pn);
     mma4(1, a, b);
-    dma3(1, kd, xb, wl, sb, zb);
-    sched_chunk<0, 3 * WN, 3>();
+    sched_chunk<0, 3 * WN, 0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < WN / 2; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.ss[j], Pn.zz16[j], Pn.ss16[j], one);
     mma4(2, a, b);
-    dma3(2, kd, xb, wl, sb, zb);
-    sched_chunk<0, (13 * WN / 2 + 3) / 4, 3>();
+    sched_chunk<0, (13 * WN / 2 + 3) / 4, 0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = WN / 2; j < WN; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.ss[j], Pn.zz16[j], Pn.ss16[j], one);
     mma4(3, a, b);
-    dma3(3, kd, xb, wl, sb, zb);
-    sched_chunk<0, (13 * WN / 2 + 3) / 4, 3>();
+    sched_chunk<0, (13 * WN / 2 + 3) / 4, 0>();
     __builtin_amdgcn_sched_barrier(0);
     P = Pn;
 #pragma unroll
@@ -804,16 +805,33 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
         for (int t = 0; t < 16; ++t) ZPT[(16 * c + t) * GB_N + rr] = (uint8_t)(zv[c][t >> 2] >> (8 * (t & 3)));
       }
   }
-  dma(0, X0, W0, S0, Z0);
+  dma_x(0, 0, X0);
+  dma_x(1, 0, X0);
+  dma_w(0, W0, S0, Z0);
   __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
   __builtin_amdgcn_s_barrier();
-  dma(min(1, KT - 1), X1, W1, S1, Z1);
+  dma_x(0, 1, X1);  // (KT is even: there is a second k-tile)
+  dma_x(1, 1, X1);
+  dma_w(1, W1, S1, Z1);
   load_params(0, W0, S0, Z0, P);
   read_b(X0, 0, b);
   deq(P, 0, a);
-  for (int kt = 0; kt < KT; kt += 2) {  // KT even (checked on the host)
-    tile(kt, X0, W0, S0, Z0, X1, W1, S1, Z1);
-    tile(kt + 1, X1, W1, S1, Z1, X0, W0, S0, Z0);
+  int kt = 0;
+  for (; kt + 6 <= KT; kt += 6) {  // the period of both rings; KT even (checked on the host)
+    tile(kt, X2, X0, W0, S0, Z0, X1, W1, S1, Z1);
+    tile(kt + 1, X0, X1, W1, S1, Z1, X2, W0, S0, Z0);
+    tile(kt + 2, X1, X2, W0, S0, Z0, X0, W1, S1, Z1);
+    tile(kt + 3, X2, X0, W1, S1, Z1, X1, W0, S0, Z0);
+    tile(kt + 4, X0, X1, W0, S0, Z0, X2, W1, S1, Z1);
+    tile(kt + 5, X1, X2, W1, S1, Z1, X0, W0, S0, Z0);
+  }
+  if (kt < KT) {
+    tile(kt, X2, X0, W0, S0, Z0, X1, W1, S1, Z1);
+    tile(kt + 1, X0, X1, W1, S1, Z1, X2, W0, S0, Z0);
+  }
+  if (kt + 2 < KT) {
+    tile(kt + 2, X1, X2, W0, S0, Z0, X0, W1, S1, Z1);
+    tile(kt + 3, X2, X0, W1, S1, Z1, X1, W0, S0, Z0);
   }
   // the last tile's step 3 read a stage that the epilogue below overwrites
   __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
@@ -852,6 +870,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
       const int ctr = xcd * slots + ja;
       __builtin_amdgcn_s_waitcnt(0);  // this wavefront's stores have reached L2 / memory
       __syncthreads();
+      volatile uint32_t& s_last = *(uint32_t*)W0;  // (the stages take all of LDS, and the epilogue uses X0)
       if (tid == 0) {
         uint32_t old;
         if (sys) old = __hip_atomic_fetch_add(&cnt[ctr], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
