@@ -325,7 +325,9 @@ int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const 
       xin = xr;
       fused = nullptr;
     }
-    if (epi == kEpiAct)
+    if (epi != kEpiPlain && !fused && M <= kRowsMaxM)
+      e = launch_w4_rows(epi == kEpiGated, xin, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream);
+    else if (epi == kEpiAct)
       e = launch_w4_decode_act(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, ep, stream);
     else if (epi == kEpiGated)
       e = launch_w4_decode_gated(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, ep, stream);

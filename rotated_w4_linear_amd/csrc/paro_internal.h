@@ -228,6 +228,13 @@ hipError_t launch_w4_decode_gated(
     const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
     const paro_rotation* r, void* ws, const W4Epilogue& ep, hipStream_t stream);
 
+// The act and gated products on at most kRowsMaxM tokens whose activations are
+// transformed already (decode_rows.hip); no workspace.
+constexpr int64_t kRowsMaxM = 16;
+hipError_t launch_w4_rows(bool gated, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+                          const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d,
+                          int group, const W4Epilogue& ep, hipStream_t stream);
+
 // Gradient of a W4 product at its input (w4_input_grad.hip): dx fp16 [M][d] =
 // dz [M][P] W_hat, P the rows of the weight block (a multiple of 16); cnt are
 // arrival counters (zero between calls), ws holds input_grad_scratch_bytes(M, P, d).

@@ -105,8 +105,8 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const u4* __restrict__ in
 // length (matrix cores busy 48%), and k-tiles of 32 in four stages read half
 // lines (59%, at a lower clock for the doubled L2 requests).
 // k may be split over ksplit workgroups of one tile (consecutive slots of one
-// XCD): fp32 partial tiles in the workspace, the last to arrive adds them in
-// split order, as in the W4 kernels.
+// XCD): the workgroups leave fp32 partial tiles in the workspace and the last
+// to arrive adds them in split order.
 // --------------------------------------------------------------------------
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -270,52 +270,69 @@ void input_grad_kernel(const uint16_t* __restrict__ wt, const uint16_t* __restri
       return __builtin_amdgcn_make_buffer_rsrc((void*)(part + ((size_t)tile * ksplit + k2) * (size_t)(IG_N * BM)),
                                                (short)0, IG_N * BM * 4, kRsrcWord3);
     };
-    const __amdgpu_buffer_rsrc_t rmine = rsrc(ks);
+    // (the stages take all of LDS; the epilogue uses A0)
+    // With two pieces the last keeps its own sums in registers (1024 x 4096 ->
+    // 4096: 127 -> 119 us with the product before it); the 256 x 256 tile's 256
+    // accumulators would spill for it (1001 -> 1013 us)
+    constexpr bool kKeep = NF < 16;
+    const bool last = meet_last(&cnt[tile], ksplit, sys, (uint32_t*)B0);
+    if (!last || !kKeep || ksplit > 2) {
+      const __amdgpu_buffer_rsrc_t rmine = rsrc(ks);
 #pragma unroll
-    for (int f = 0; f < 4 * NF; ++f) {
-      const int j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
-      const u4 v = __builtin_bit_cast(u4, f4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
-                                             acc[j][i][4 * q + 3]});
+      for (int f = 0; f < 4 * NF; ++f) {
+        const int j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
+        const u4 v = __builtin_bit_cast(u4, f4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
+                                               acc[j][i][4 * q + 3]});
+        const int off = ((w * 4 * NF + f) * 64 + lane) * 16;
+        if (sys) __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, kAuxSys);
+        else __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, 0);
+      }
+    }
+    if (!last) {
+      meet_report(&cnt[tile], sys);
+      return;
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // (its own partial tile, if it stored one)
+    meet_wait(&cnt[tile], ksplit, sys);
+    auto load4 = [&](const __amdgpu_buffer_rsrc_t rk, int f) {
       const int off = ((w * 4 * NF + f) * 64 + lane) * 16;
-      if (sys) __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, kAuxSys);
-      else __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, 0);
-    }
-    __builtin_amdgcn_s_waitcnt(0);  // this wavefront's stores have reached L2 / memory
-    __syncthreads();
-    volatile uint32_t& s_last = *(uint32_t*)B0;  // (the stages take all of LDS, and the epilogue uses A0)
-    if (tid == 0) {
-      uint32_t old;
-      if (sys) old = __hip_atomic_fetch_add(&cnt[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-      else old = __hip_atomic_fetch_add(&cnt[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s_last = old == (uint32_t)(ksplit - 1);
-    }
-    __syncthreads();
-    if (!s_last) return;
+      return __builtin_bit_cast(f4, sys ? __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxSys)
+                                        : __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxL2R));
+    };
+    if (kKeep && ksplit == 2) {  // one sum, the same in either order
+      const __amdgpu_buffer_rsrc_t rk = rsrc(1 - ks);
 #pragma unroll
-    for (int f0 = 0; f0 < 4 * NF; f0 += 4) {
-      f4 r[4];
-      for (int k2 = 0; k2 < ksplit; ++k2) {
-        const __amdgpu_buffer_rsrc_t rk = rsrc(k2);
-        f4 v[4];
+      for (int f0 = 0; f0 < 4 * NF; f0 += 8) {
+        f4 v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int off = ((w * 4 * NF + f0 + e) * 64 + lane) * 16;
-          v[e] = __builtin_bit_cast(f4, sys ? __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxSys)
-                                            : __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxL2R));
+        for (int e = 0; e < 8; ++e) v[e] = load4(rk, f0 + e);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int f = f0 + e, j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[j][i][4 * q + c] += v[e][c];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int f0 = 0; f0 < 4 * NF; f0 += 16) {
+        f4 r[16];
+        for (int k2 = 0; k2 < ksplit; ++k2) {
+          const __amdgpu_buffer_rsrc_t rk = rsrc(k2);
+          f4 v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = load4(rk, f0 + e);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = k2 == 0 ? v[e] : r[e] + v[e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = k2 == 0 ? v[e] : r[e] + v[e];
-      }
+        for (int e = 0; e < 16; ++e) {
+          const int f = f0 + e, j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int f = f0 + e, j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[j][i][4 * q + c] = r[e][c];
+          for (int c = 0; c < 4; ++c) acc[j][i][4 * q + c] = r[e][c];
+        }
       }
-    }
-    if (tid == 0) {
-      if (sys) __hip_atomic_store(&cnt[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-      else __hip_atomic_store(&cnt[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
 

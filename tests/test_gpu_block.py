@@ -125,9 +125,10 @@ def test_linear_act(paro, M, d, N, G):
     paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, residual=y, act="silu", y=y, group=G, workspace=ws)
     ref = paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, residual=dev(res), act="silu", group=G, workspace=ws)
     assert torch.equal(y, ref)
-    # no activation and no residual: paro_w4_linear's values
-    y = paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, group=G, workspace=ws)
-    assert torch.equal(y, paro.paro_w4_linear(None, c.xd, *c.dev, bias=c.bd, group=G, workspace=ws))
+    # no activation and no residual: paro_w4_linear's values (few tokens: sums in another order)
+    if M > 16:
+        y = paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, group=G, workspace=ws)
+        assert torch.equal(y, paro.paro_w4_linear(None, c.xd, *c.dev, bias=c.bd, group=G, workspace=ws))
     assert ws is None or not ws[:16384].any().item(), "arrival counters not left at zero"
 
 
@@ -194,7 +195,8 @@ def test_gradients(paro, M, d, N, G, gated):
 @pytest.mark.parametrize("M", [1, 4, 16, 33, 64, 200])
 @pytest.mark.parametrize("group,K", [(128, 8), (64, 3), (256, 8)])
 def test_with_transform_equals_transformed_first(paro, M, group, K):
-    """A plan r inside the call: the same values as on paro_rotate's output."""
+    """A plan r inside the call: the values of paro_rotate's output, the same
+    bits beyond 16 tokens (with few, the sums may be taken in another order)."""
     d, N = 1024, 528
     log(f"transform inside M={M} G={group} K={K}")
     x, layer, b = synthetic.linear_case(seed=M + K, M=M, d=d, N=2 * N, group=group, K=K)
@@ -203,11 +205,17 @@ def test_with_transform_equals_transformed_first(paro, M, group, K):
     xd = dev(x)
     xr = paro.paro_rotate(r, xd)
     bd = dev(b)
-    a = paro.paro_w4_gated(r, xd, *wq, bias=bd, group=group)
-    assert torch.equal(a, paro.paro_w4_gated(None, xr, *wq, bias=bd, group=group))
     res = torch.randn((M, 2 * N), device="cuda").half()
-    a = paro.paro_w4_linear_act(r, xd, *wq, bias=bd, residual=res, act="gelu_tanh", group=group)
-    assert torch.equal(a, paro.paro_w4_linear_act(None, xr, *wq, bias=bd, residual=res, act="gelu_tanh", group=group))
+    g = paro.paro_w4_gated(r, xd, *wq, bias=bd, group=group)
+    y = paro.paro_w4_linear_act(r, xd, *wq, bias=bd, residual=res, act="gelu_tanh", group=group)
+    if M > 16:
+        assert torch.equal(g, paro.paro_w4_gated(None, xr, *wq, bias=bd, group=group))
+        assert torch.equal(y, paro.paro_w4_linear_act(None, xr, *wq, bias=bd, residual=res, act="gelu_tanh",
+                                                      group=group))
+    w, xh = block.weights(*(host(t) for t in wq), group), host(xr)
+    within(host(g), block.gated(xh, w, b, "silu"), block.gated_tolerance(xh, w, b, "silu"), "gated")
+    within(host(y), block.linear_act(xh, w, b, host(res), "gelu_tanh"),
+           block.linear_tolerance(xh, w, b, host(res), "gelu_tanh"), "linear")
 
 
 def test_not_finite_stays_in_its_row(paro):
