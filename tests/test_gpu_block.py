@@ -92,7 +92,8 @@ def guarded(M, N, fill=777.0):
 SHAPES = [
     (1, 128, 16, 128), (1, 4096, 1024, 128), (2, 640, 80, 64), (3, 512, 48, 256), (4, 1024, 4096, 128),
     (5, 4096, 208, 128), (16, 2560, 1040, 64), (17, 1024, 272, 128), (32, 768, 512, 256), (33, 1536, 144, 128),
-    (64, 2048, 1040, 128), (1, 14336, 64, 128),
+    (64, 2048, 1040, 128), (1, 14336, 64, 128), (1, 4096, 8240, 128), (3, 5120, 8208, 128), (13, 4096, 10256, 64),
+    (16, 640, 8304, 128), (2, 8192, 8192, 256),
     (65, 128, 16, 128), (70, 1024, 528, 128), (100, 4096, 256, 128), (333, 2560, 1040, 64), (500, 384, 4112, 64),
     (1000, 1024, 2064, 256), (2100, 512, 4368, 128), (2048, 768, 16400, 128),
 ]
