@@ -205,11 +205,13 @@ void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
 // The same for layers with more 16-channel blocks than CUs: one workgroup per
 // CU goes from block to block. Its wavefronts keep their R chunks of k for
 // good, the X' operands of those in registers, and a wavefront's next codes
-// come into the other of its two LDS buffers while it multiplies: against a
-// workgroup per block, whose wavefronts all load, then all multiply, 4096 ->
-// 2 x 14336 at 1 token takes TIMES. One barrier per block: the sums of a
-// block go to one of two places in LDS, and wavefront (block % wavefronts) adds
-// them while the others go on.
+// come into the other of its two LDS buffers while it multiplies. A workgroup
+// per block would read X' once per block: 4096 -> 14336 at 16 tokens 23.0 us
+// against 12.3, gated 30.6 against 19.1; at 1 token 11.7 and 11.1, gated 17.6
+// and 18.3. The weights alone stream in 9.7 us (gated, with the launch); their
+// dequantization takes 6.5 us of vector instructions, overlapped in part. One
+// barrier per block: the sums of a block go to one of two places in LDS, and
+// wavefront (block % wavefronts) adds them while the others go on.
 constexpr int stream_waves(bool gated) { return gated ? 8 : 16; }
 
 template <int EPI, int MT, int R, bool SZV>

@@ -292,6 +292,15 @@ void w4_gemm_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
     if (kt + 1 < KT) step(kt + 1, &X1[kg][0], &W1[kg][0], &S1[kg][0], &Z1[kg][0], &X0[kg][0], &W0[kg][0], &S0[kg][0], &Z0[kg][0]);
   }
 
+  // the epilogue's second operand (read by the wavefronts of group 0), on its
+  // way while the groups' sums meet
+  u4 av[2][8];
+  if constexpr (EPI != kEpiPlain) {
+    if (kg == 0) {
+#pragma unroll
+      for (int ps = 0; ps < MT / 2; ++ps) epi_fetch<EPI, NT>(av[ps], lane, m0 + 64 * ps, n0, M, N, aux);
+    }
+  }
   if constexpr (KS > 1) {
     // the k groups add their partial sums pairwise through LDS, (0 + 1) +
     // (2 + 3): in the round of span s, group kg = r + s hands its sums to
@@ -400,8 +409,8 @@ void w4_gemm_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
 #pragma unroll
       for (int ps = 0; ps < PASSES; ++ps)
         epi_block<EPI, NT, decltype(form)::value>(
-            stage, [&](int j, int t, int e) { return acc[j][2 * ps + t][e]; }, lane, m0 + 64 * ps, n0, M, N, bias,
-            aux, act, y);
+            stage, [&](int j, int t, int e) { return acc[j][2 * ps + t][e]; }, av[ps], lane, m0 + 64 * ps, n0, M, N,
+            bias, aux, act, y);
     };
     if (erf) passes(std::true_type{});
     else passes(std::false_type{});
@@ -920,14 +929,22 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   const int n0 = nw0 + (GT ? 16 : 32) * WN * wn, mw0 = m0 + 32 * MTW * wm;
   uint8_t* stage = (uint8_t*)X0 + 8192 * w;
   if constexpr (EPI != kEpiPlain) {
+    // blocks of 64 tokens by two tiles, the second operand two blocks ahead
+    constexpr int PS = MTW / 2, BLOCKS = WN / 2 * PS;
+    u4 av[2][8];
+    auto fetch = [&](int b) {
+      epi_fetch<EPI, 2>(av[b & 1], lane, mw0 + 64 * (b % PS), n0 + (GT ? 32 : 64) * (b / PS), M, N, aux);
+    };
+    fetch(0);
+    fetch(1);
     auto passes = [&](auto form) {
 #pragma unroll
-      for (int jh = 0; jh < WN / 2; ++jh)
-#pragma unroll
-        for (int ps = 0; ps < MTW / 2; ++ps)
-          epi_block<EPI, 2, decltype(form)::value>(
-              stage, [&](int j, int t, int e) { return acc[2 * jh + j][2 * ps + t][e]; }, lane, mw0 + 64 * ps,
-              n0 + (GT ? 32 : 64) * jh, M, N, bias, aux, act, y);
+      for (int b = 0; b < BLOCKS; ++b) {
+        epi_block<EPI, 2, decltype(form)::value>(
+            stage, [&](int j, int t, int e) { return acc[2 * (b / PS) + j][2 * (b % PS) + t][e]; }, av[b & 1], lane,
+            mw0 + 64 * (b % PS), n0 + (GT ? 32 : 64) * (b / PS), M, N, bias, aux, act, y);
+        if (b + 2 < BLOCKS) fetch(b + 2);
+      }
     };
     if (erf) passes(std::true_type{});
     else passes(std::false_type{});
