@@ -489,8 +489,11 @@ int64_t paro_adamw_moments(int32_t count, const int64_t* n);
  * in fp32; p is rounded once to its type (with fp16 or bf16 parameters an
  * update below half a step of the value is lost).
  *
- * paro_adamw_create (host only, no GPU work) makes the plan of a list of
- * tensors; the caller owns the tensors and keeps them where they are.
+ * paro_adamw_create (synchronous) makes the plan of a list of tensors; the
+ * caller owns the tensors and keeps them where they are. Lists of more than
+ * 120 tensors are put into a table in the current device's memory (so not
+ * inside a stream capture), which paro_adamw_destroy frees; no enqueued step
+ * may still use it then.
  *   count, n            tensors and their values, n[i] >= 0 (0: skipped);
  *   params, grads       host arrays of device pointers, contiguous, aligned to
  *                       their element type (16 bytes: the fast accesses);
@@ -510,10 +513,11 @@ int64_t paro_adamw_moments(int32_t count, const int64_t* n);
  *                       padding between the tensors included.
  * Errors: PARO_ERR_NULL, PARO_ERR_VALUE (unknown type; parameters, moments or
  * scales that overlap each other or a gradient), PARO_ERR_UNSUPPORTED
- * (state_bits, out of host memory), PARO_ERR_SHAPE, PARO_ERR_ALIGN.
+ * (state_bits, out of host memory), PARO_ERR_SHAPE, PARO_ERR_ALIGN,
+ * PARO_ERR_HIP (the table).
  *
- * paro_adamw_step runs step t >= 1 on the current device: a launch for every
- * 120 tensors, without upload, allocation or synchronisation. A captured call
+ * paro_adamw_step runs step t >= 1 on the current device, in one launch (one
+ * for every 2^33 values), without upload, allocation or synchronisation. A captured call
  * replays the t and the rates it was captured with. Steps of one plan must
  * not run at the same time.
  * Errors: PARO_ERR_NULL, PARO_ERR_VALUE (step < 1; lr or weight_decay

@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <new>
+#include <memory>
 #include <string>
 #include <utility>
 #include <vector>
@@ -179,12 +179,25 @@ int paro_w4_gated_backward(const uint16_t* x, const uint8_t* qweight, const uint
 }  // extern "C"
 
 // The launches of one step, fixed when the plan is made; a step fills in its
-// scalars.
+// scalars. Short lists as kernel arguments (lists), long ones as parts of the
+// device table (first tensor and first chunk of each launch).
 struct paro_adamw {
-  int32_t param_type, grad_type;
-  bool eight;
-  std::vector<AdamwLaunch> launches;
-  std::vector<uint32_t> chunks;
+  int32_t param_type = 0, grad_type = 0;
+  bool eight = false;
+  void *m = nullptr, *v = nullptr;
+  float *ms = nullptr, *vs = nullptr;
+  std::vector<AdamwLaunch> lists;
+  struct Part {
+    size_t tensor0, chunk0;
+  };
+  std::vector<Part> parts;
+  std::vector<uint32_t> chunks;  // of each launch
+  AdamwTensor* d_tensors = nullptr;
+  uint32_t* d_of_chunk = nullptr;
+  ~paro_adamw() {
+    if (d_tensors) (void)hipFree(d_tensors);
+    if (d_of_chunk) (void)hipFree(d_of_chunk);
+  }
 };
 
 namespace paro {
@@ -265,48 +278,68 @@ int paro_adamw_create(int32_t count, const int64_t* n, void* const* params, int3
         return fail(PARO_ERR_VALUE, "paro_adamw_create: a gradient overlaps what the step writes");
     }
 
-    std::vector<AdamwLaunch> launches;
-    std::vector<uint32_t> chunks;
-    AdamwLaunch cur;
-    std::memset(&cur, 0, sizeof(cur));
-    cur.m = m;
-    cur.v = v;
-    cur.ms = m_scale;
-    cur.vs = v_scale;
-    uint32_t chunk = 0, block = 0;
+    // the pieces of each launch (a very large tensor takes several)
     constexpr uint32_t kMostChunks = 1u << 22;
-    auto flush = [&]() {
-      if (cur.count) {
-        launches.push_back(cur);
-        chunks.push_back(chunk);
-      }
-      cur.count = 0;
-      chunk = 0;
-    };
+    std::vector<std::vector<AdamwTensor>> launches(1);
+    std::unique_ptr<paro_adamw> h(new paro_adamw());
+    uint32_t chunk = 0, block = 0;
+    size_t pieces = 0;
     for (int32_t i = 0; i < count; ++i) {
-      // (a very large tensor takes several launches)
       for (int64_t at = 0; at < n[i];) {
-        if (cur.count == kAdamTensors || chunk == kMostChunks) flush();
-        const int64_t take = std::min(n[i] - at, (int64_t)(kMostChunks - chunk) * kAdamChunk);
-        AdamwTensor& t = cur.t[cur.count++];
+        if (chunk == kMostChunks) {
+          h->chunks.push_back(chunk);
+          launches.emplace_back();
+          chunk = 0;
+        }
+        AdamwTensor t;
         t.p = (char*)params[i] + at * type_bytes(param_type);
         t.g = (const char*)grads[i] + at * type_bytes(grad_type);
-        t.n = take;
+        t.n = std::min(n[i] - at, (int64_t)(kMostChunks - chunk) * kAdamChunk);
         t.chunk0 = chunk;
         t.block0 = block;
-        chunk += (uint32_t)((take + kAdamChunk - 1) / kAdamChunk);
-        block += (uint32_t)((take + 255) / 256);
-        at += take;
+        chunk += (uint32_t)((t.n + kAdamChunk - 1) / kAdamChunk);
+        block += (uint32_t)((t.n + 255) / 256);
+        at += t.n;
+        launches.back().push_back(t);
+        ++pieces;
       }
     }
-    flush();
-    paro_adamw* h = new paro_adamw();
+    h->chunks.push_back(chunk);
     h->param_type = param_type;
     h->grad_type = grad_type;
     h->eight = eight;
-    h->launches.swap(launches);
-    h->chunks.swap(chunks);
-    *out = h;
+    h->m = m;
+    h->v = v;
+    h->ms = m_scale;
+    h->vs = v_scale;
+    bool table = false;
+    for (const auto& l : launches) table = table || l.size() > (size_t)kAdamTensors;
+    if (!table) {
+      for (const auto& l : launches) {
+        AdamwLaunch a;
+        std::memset(&a, 0, sizeof(a));
+        a.count = (int32_t)l.size();
+        std::copy(l.begin(), l.end(), a.t);
+        h->lists.push_back(a);
+      }
+    } else {
+      std::vector<AdamwTensor> all;
+      std::vector<uint32_t> of_chunk;
+      for (const auto& l : launches) {
+        h->parts.push_back({all.size(), of_chunk.size()});
+        for (size_t k = 0; k < l.size(); ++k)
+          of_chunk.insert(of_chunk.end(), (size_t)((l[k].n + kAdamChunk - 1) / kAdamChunk), (uint32_t)k);
+        all.insert(all.end(), l.begin(), l.end());
+      }
+      hipError_t e = hipMalloc((void**)&h->d_tensors, all.size() * sizeof(AdamwTensor));
+      if (e == hipSuccess) e = hipMalloc((void**)&h->d_of_chunk, of_chunk.size() * sizeof(uint32_t));
+      if (e == hipSuccess)
+        e = hipMemcpy(h->d_tensors, all.data(), all.size() * sizeof(AdamwTensor), hipMemcpyHostToDevice);
+      if (e == hipSuccess)
+        e = hipMemcpy(h->d_of_chunk, of_chunk.data(), of_chunk.size() * sizeof(uint32_t), hipMemcpyHostToDevice);
+      if (e != hipSuccess) return hip_fail(e, "paro_adamw_create: table of tensors");
+    }
+    *out = h.release();
   } catch (const std::exception& e) {
     return fail(PARO_ERR_UNSUPPORTED, std::string("paro_adamw_create: ") + e.what());
   }
@@ -323,17 +356,29 @@ int paro_adamw_step(const paro_adamw* h, int64_t step, double lr, double beta1, 
       !((float)eps > 0 && std::isfinite((float)eps)) || !std::isfinite(weight_decay) || weight_decay < 0)
     return fail(PARO_ERR_VALUE, "paro_adamw_step: lr >= 0, 0 <= beta < 1, eps > 0, weight_decay >= 0, all finite");
   const double c1 = 1.0 - std::pow(beta1, (double)step), c2 = 1.0 - std::pow(beta2, (double)step);
-  for (size_t i = 0; i < h->launches.size(); ++i) {
-    AdamwLaunch a = h->launches[i];
-    a.b1 = (float)beta1;
-    a.c1 = (float)(1.0 - beta1);
-    a.b2 = (float)beta2;
-    a.c2 = (float)(1.0 - beta2);
-    a.keep = (float)(1.0 - lr * weight_decay);
-    a.rate = (float)(lr / c1);
-    a.root = (float)(1.0 / std::sqrt(c2));
-    a.eps = (float)eps;
-    const hipError_t e = launch_adamw(a, h->chunks[i], h->param_type, h->grad_type, h->eight, stream);
+  AdamwScalars sc;
+  sc.m = h->m;
+  sc.v = h->v;
+  sc.ms = h->ms;
+  sc.vs = h->vs;
+  sc.b1 = (float)beta1;
+  sc.c1 = (float)(1.0 - beta1);
+  sc.b2 = (float)beta2;
+  sc.c2 = (float)(1.0 - beta2);
+  sc.keep = (float)(1.0 - lr * weight_decay);
+  sc.rate = (float)(lr / c1);
+  sc.root = (float)(1.0 / std::sqrt(c2));
+  sc.eps = (float)eps;
+  for (size_t i = 0; i < h->chunks.size(); ++i) {
+    hipError_t e;
+    if (h->parts.empty()) {
+      AdamwLaunch a = h->lists[i];
+      a.s = sc;
+      e = launch_adamw(a, h->chunks[i], h->param_type, h->grad_type, h->eight, stream);
+    } else {
+      const AdamwTable a = {sc, h->d_tensors + h->parts[i].tensor0, h->d_of_chunk + h->parts[i].chunk0};
+      e = launch_adamw(a, h->chunks[i], h->param_type, h->grad_type, h->eight, stream);
+    }
     if (e != hipSuccess) return hip_fail(e, "paro_adamw_step launch");
   }
   return PARO_OK;

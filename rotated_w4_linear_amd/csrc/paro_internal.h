@@ -243,9 +243,11 @@ hipError_t launch_w4_input_grad(const uint16_t* dz, const uint8_t* qweight, cons
                                 const uint8_t* zeros, uint16_t* dx, int64_t M, int64_t P, int64_t d, int group,
                                 uint32_t* cnt, void* ws, hipStream_t stream);
 
-// One launch of the AdamW step (adamw.hip): up to kAdamTensors tensors, each
-// cut into chunks of kAdamChunk values; chunk0 is the tensor's first chunk of
-// the launch, block0 its first block of 256 moments.
+// One launch of the AdamW step (adamw.hip). Every tensor is cut into chunks of
+// kAdamChunk values; chunk0 is its first chunk of the launch, block0 its first
+// block of 256 moments. Up to kAdamTensors tensors travel as kernel arguments
+// (AdamwLaunch), more of them as a table in device memory (AdamwTable: the
+// tensors, and the tensor of each chunk).
 constexpr int kAdamTensors = 120;
 constexpr int kAdamChunk = 2048;
 struct AdamwTensor {
@@ -254,15 +256,25 @@ struct AdamwTensor {
   int64_t n;
   uint32_t chunk0, block0;
 };
-struct AdamwLaunch {
-  AdamwTensor t[kAdamTensors];
+struct AdamwScalars {
   void *m, *v;
   float *ms, *vs;
   float b1, c1, b2, c2;          // b, 1 - b
   float keep, rate, root, eps;   // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+};
+struct AdamwLaunch {
+  AdamwScalars s;
   int32_t count;
+  AdamwTensor t[kAdamTensors];
+};
+struct AdamwTable {
+  AdamwScalars s;
+  const AdamwTensor* t;
+  const uint32_t* of_chunk;
 };
 hipError_t launch_adamw(const AdamwLaunch& a, uint32_t chunks, int param_type, int grad_type, bool eight,
+                        hipStream_t stream);
+hipError_t launch_adamw(const AdamwTable& a, uint32_t chunks, int param_type, int grad_type, bool eight,
                         hipStream_t stream);
 
 // Shared by the products' entry points (api.cpp): the argument checks (N: rows
