@@ -376,18 +376,26 @@ void w4_gemm_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
     }
     __syncthreads();
     if (!s_last || kg != 0) return;
+    // (all of a split's loads before the first sum: taken one at a time, their
+    // way from L2 adds up)
+    f4 t[NF];
+    for (int k2 = 0; k2 < ksplit; ++k2) {
+      const __amdgpu_buffer_rsrc_t rk = rsrc(k2);
+      f4 v[NF];
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const int off = ((w * NF + f) * 64 + lane) * 16;
+        v[f] = __builtin_bit_cast(f4, sys ? __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxSysW)
+                                          : __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxL2R));
+      }
+#pragma unroll
+      for (int f = 0; f < NF; ++f) t[f] = k2 == 0 ? v[f] : t[f] + v[f];
+    }
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       const int j = f / (MT * 4), mm = (f / 4) % MT, q = f % 4;
-      const int off = ((w * NF + f) * 64 + lane) * 16;
-      f4 t = {0.f, 0.f, 0.f, 0.f};
-      for (int k2 = 0; k2 < ksplit; ++k2) {
-        const f4 v = __builtin_bit_cast(f4, sys ? __builtin_amdgcn_raw_buffer_load_b128(rsrc(k2), off, 0, kAuxSysW)
-                                                : __builtin_amdgcn_raw_buffer_load_b128(rsrc(k2), off, 0, kAuxL2R));
-        t = k2 == 0 ? v : t + v;
-      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][mm][4 * q + e] = t[e];
+      for (int e = 0; e < 4; ++e) acc[j][mm][4 * q + e] = t[f][e];
     }
     if (tid == 0) {
       if (sys) __hip_atomic_store(&cnt[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
