@@ -327,6 +327,8 @@ int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const 
     }
     if (epi != kEpiPlain && !fused && M <= kRowsMaxM)
       e = launch_w4_rows(epi == kEpiGated, xin, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream);
+    else if (epi != kEpiPlain && !fused)
+      e = launch_w4_tiles(epi, xin, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream);
     else if (epi == kEpiAct)
       e = launch_w4_decode_act(xin, qweight, scales, zeros, bias, y, M, N, d, group, fused, ws, ep, stream);
     else if (epi == kEpiGated)
@@ -347,7 +349,9 @@ int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const 
     const bool split = plan.partial_bytes && ws && ws_bytes >= kDecodeCounterBytes + xbytes + plan.partial_bytes;
     uint32_t* cnt = split ? (uint32_t*)ws : nullptr;
     float* part = split ? (float*)(ws + kDecodeCounterBytes + xbytes) : nullptr;
-    if (epi == kEpiAct)
+    if (epi != kEpiPlain && w4_tiles_fit(M, P, d))
+      e = launch_w4_tiles(epi, xin, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream);
+    else if (epi == kEpiAct)
       e = launch_w4_gemm_act(xin, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, ep, stream);
     else if (epi == kEpiGated)
       e = launch_w4_gemm_gated(xin, qweight, scales, zeros, bias, y, M, N, d, group, cnt, part, ep, stream);

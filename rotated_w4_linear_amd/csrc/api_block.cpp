@@ -108,7 +108,11 @@ int run_backward(const char* fn, bool gated, const uint16_t* x, const uint8_t* q
     uint32_t* cnt = split ? (uint32_t*)ws : nullptr;
     float* part = split ? (float*)(ws + kDecodeCounterBytes) : nullptr;
     auto launch = gated ? launch_w4_gemm_gated_grad : launch_w4_gemm_act_grad;
-    e = launch(x, qweight, scales, zeros, bias, dz, M, N, d, group, cnt, part, ep, stream);
+    if (w4_tiles_fit(M, P, d))
+      e = launch_w4_tiles(gated ? kEpiGatedGrad : kEpiActGrad, x, qweight, scales, zeros, bias, dz, M, N, d, group, ep,
+                          stream);
+    else
+      e = launch(x, qweight, scales, zeros, bias, dz, M, N, d, group, cnt, part, ep, stream);
     if (e != hipSuccess) return hip_fail(e, fn);
   }
   if (dx) {

@@ -47,34 +47,6 @@ constexpr int kCus = 256;
 constexpr int wave_bytes(bool gated, int mt) { return (gated ? 8192 : 4096) + 1024 * mt; }
 constexpr int max_waves(bool gated, int mt) { return mt == 1 ? (gated ? 8 : 16) : mt == 4 ? (gated ? 6 : 10) : (gated ? 6 : 7); }
 
-// From the sums z of four channels from n on (gated: z[0] the gate's, z[1] the
-// up projection's) of token m to the output.
-template <int EPI>
-__device__ __forceinline__ void finish(f4* z, int m, int n, int N, const uint16_t* bias, const uint16_t* aux,
-                                       const ActForm& act, int erf, uint16_t* y) {
-  auto add4 = [](f4& v, const uint16_t* p) {
-    const uint2 raw = *(const uint2*)p;
-    v[0] += half_lo(raw.x);
-    v[1] += half_hi(raw.x);
-    v[2] += half_lo(raw.y);
-    v[3] += half_hi(raw.y);
-  };
-  if (bias) add4(z[0], bias + n);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) z[0][e] = erf ? act_value<true>(z[0][e], act) : act_value<false>(z[0][e], act);
-  if constexpr (epi_gated(EPI)) {
-    if (bias) add4(z[1], bias + N + n);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z[0][e] *= z[1][e];
-  } else {
-    if (aux) add4(z[0], aux + (size_t)m * N + n);
-  }
-  uint2 o;
-  o.x = half_bits(z[0][0]) | (half_bits(z[0][1]) << 16);
-  o.y = half_bits(z[0][2]) | (half_bits(z[0][3]) << 16);
-  *(uint2*)(y + (size_t)m * N + n) = o;
-}
-
 // SZV: group 128 and whole chunks, so that a row's four scales and four zeros
 // of a chunk are one 8-byte and one 4-byte load.
 template <int EPI, int MT, bool SZV>
@@ -199,7 +171,7 @@ void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
   for (int k = 1; k < nw; ++k)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) z[j] += *(const f4*)(lds + k * WB + 1024 * j + 16 * lane);
-  if (token && c0 + 4 * kq < N) finish<EPI>(z, r, c0 + 4 * kq, N, bias, aux, act, erf, y);
+  if (token && c0 + 4 * kq < N) epi_lane<EPI>(z, r, c0 + 4 * kq, N, bias, aux, act, erf, y);
 }
 
 // The same for layers with more 16-channel blocks than CUs: one workgroup per
@@ -374,7 +346,7 @@ void w4_rows_stream_kernel(const uint16_t* __restrict__ x, const uint8_t* __rest
 #pragma unroll
         for (int j = 0; j < TJ; ++j) z[j] += place[(k * TJ + j) * 64 + lane];
       const int n = 16 * blk + 4 * kq;
-      if (r < M && n < N) finish<EPI>(z, r, n, N, bias, aux, act, erf, y);
+      if (r < M && n < N) epi_lane<EPI>(z, r, n, N, bias, aux, act, erf, y);
     }
     ++it;
   };

@@ -234,6 +234,13 @@ constexpr int64_t kRowsMaxM = 16;
 hipError_t launch_w4_rows(bool gated, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                           const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d,
                           int group, const W4Epilogue& ep, hipStream_t stream);
+// The products with an epilogue (any but kEpiPlain) in small tiles, k inside the
+// workgroup (w4_tiles.hip); no workspace. N: output channels, P: weight rows.
+// w4_tiles_fit: whether they are taken before the kernels of w4_gemm_kernels.h.
+bool w4_tiles_fit(int64_t M, int64_t P, int64_t d);
+hipError_t launch_w4_tiles(int epi, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+                           const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d,
+                           int group, const W4Epilogue& ep, hipStream_t stream);
 
 // Gradient of a W4 product at its input (w4_input_grad.hip): dx fp16 [M][d] =
 // dz [M][P] W_hat, P the rows of the weight block (a multiple of 16); cnt are

@@ -444,7 +444,9 @@ template <int T, int TJ, bool SZV, int TB, int EPI>
 hipError_t launch_plan(const uint16_t* x, const uint8_t* qw, const uint16_t* sc, const uint8_t* zr,
                        const uint16_t* bias, uint16_t* y, int m, int n, int k, int gsh,
                        const paro_rotation* r, void* ws, const W4Epilogue& ep, hipStream_t stream) {
-  if (!r) return launch_t<false, 0, true, true, T, TJ, SZV, TB, EPI>(x, qw, sc, zr, bias, y, m, n, k, gsh, r, ws, ep, stream);
+  if constexpr (EPI == kEpiPlain) {
+    if (!r) return launch_t<false, 0, true, true, T, TJ, SZV, TB, EPI>(x, qw, sc, zr, bias, y, m, n, k, gsh, r, ws, ep, stream);
+  }
   if (r->lay.stages == 0) return launch_t<true, 0, true, true, T, TJ, SZV, TB, EPI>(x, qw, sc, zr, bias, y, m, n, k, gsh, r, ws, ep, stream);
   if (r->lay.fast) {
     if (r->lay.stages == 8) return launch_t<true, 8, true, true, T, TJ, SZV, TB, EPI>(x, qw, sc, zr, bias, y, m, n, k, gsh, r, ws, ep, stream);
@@ -456,7 +458,8 @@ hipError_t launch_plan(const uint16_t* x, const uint8_t* qw, const uint16_t* sc,
 }  // namespace
 
 // N: output channels (rows of the weight block, half of them for the gated
-// epilogue).
+// epilogue). With an epilogue r is a plan whose transform this kernel runs, and
+// M <= 32 (other calls go to w4_rows_kernel and w4_tiles_kernel).
 template <int EPI>
 hipError_t launch_w4_decode_epi(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                                 const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M,
@@ -491,12 +494,15 @@ hipError_t launch_w4_decode_epi(const uint16_t* x, const uint8_t* qweight, const
     if (tj1) return small ? PARO_DECODE_PLAN(4, 1, false, 1) : PARO_DECODE_PLAN(16, 1, false, 1);
     return small ? PARO_DECODE_PLAN(4, 2, false, 1) : PARO_DECODE_PLAN(16, 2, false, 1);
   }
-  if (tb == 2) {
+  if (tb == 2 || EPI != kEpiPlain) {
     if (szv) return tj1 ? PARO_DECODE_PLAN(16, 1, true, 2) : PARO_DECODE_PLAN(16, 2, true, 2);
     return tj1 ? PARO_DECODE_PLAN(16, 1, false, 2) : PARO_DECODE_PLAN(16, 2, false, 2);
   }
-  if (szv) return tj1 ? PARO_DECODE_PLAN(16, 1, true, 4) : PARO_DECODE_PLAN(16, 2, true, 4);
-  return tj1 ? PARO_DECODE_PLAN(16, 1, false, 4) : PARO_DECODE_PLAN(16, 2, false, 4);
+  if constexpr (EPI == kEpiPlain) {
+    if (szv) return tj1 ? PARO_DECODE_PLAN(16, 1, true, 4) : PARO_DECODE_PLAN(16, 2, true, 4);
+    return tj1 ? PARO_DECODE_PLAN(16, 1, false, 4) : PARO_DECODE_PLAN(16, 2, false, 4);
+  }
+  return hipErrorInvalidValue;
 #undef PARO_DECODE_PLAN
 }
 

@@ -208,5 +208,51 @@ __device__ __forceinline__ void epi_block(uint8_t* stage, Get get, const u4* av,
   }
 }
 
+// Epilogue of four neighbouring channels of one token held by one lane: from
+// the sums z[0] of channels n .. n + 3 (gated: the gate's, and z[1] the up
+// projection's) to the output. y may be aux.
+template <int EPI>
+__device__ __forceinline__ void epi_lane(f4* z, int m, int n, int N, const uint16_t* bias, const uint16_t* aux,
+                                         const ActForm& act, int erf, uint16_t* y) {
+  auto read4 = [](const uint16_t* p) {
+    const uint2 raw = *(const uint2*)p;
+    return f4{half_lo(raw.x), half_hi(raw.x), half_lo(raw.y), half_hi(raw.y)};
+  };
+  auto write4 = [](uint16_t* p, const f4& v) {
+    uint2 o;
+    o.x = half_bits(v[0]) | (half_bits(v[1]) << 16);
+    o.y = half_bits(v[2]) | (half_bits(v[3]) << 16);
+    *(uint2*)p = o;
+  };
+  if (bias) {
+    z[0] += read4(bias + n);
+    if constexpr (epi_gated(EPI)) z[1] += read4(bias + N + n);
+  }
+  if constexpr (EPI == kEpiAct || EPI == kEpiGated) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[0][e] = erf ? act_value<true>(z[0][e], act) : act_value<false>(z[0][e], act);
+    if constexpr (EPI == kEpiGated) z[0] *= z[1];
+    else if (aux) z[0] += read4(aux + (size_t)m * N + n);
+    write4(y + (size_t)m * N + n, z[0]);
+  } else {
+    const f4 dy = read4(aux + (size_t)m * N + n);
+    f4 v, dv;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a, b;
+      if (erf) act_both<true>(z[0][e], act, a, b);
+      else act_both<false>(z[0][e], act, a, b);
+      v[e] = a;
+      dv[e] = b;
+    }
+    if constexpr (EPI == kEpiActGrad) {
+      write4(y + (size_t)m * N + n, dy * dv);
+    } else {
+      write4(y + (size_t)m * 2 * N + n, dy * z[1] * dv);
+      write4(y + ((size_t)m * 2 + 1) * N + n, dy * v);
+    }
+  }
+}
+
 }  // namespace w4
 }  // namespace paro

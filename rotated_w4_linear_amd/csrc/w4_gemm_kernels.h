@@ -1137,12 +1137,17 @@ hipError_t launch_w4_gemm_epi(const uint16_t* x, const uint8_t* qweight, const u
     }
     return hipGetLastError();
   }
-  if (ks4 && sg.nsplit > 1 && cnt && part) {
-    const int sys = !xcd_dispatch_is_round_robin();
-    hipLaunchKernelGGL((w4_gemm_kernel<4, 2, 1, true, EPI>), dim3(g * (unsigned)sg.nsplit), dim3(1024), 0, stream, x,
-                       qweight, scales, zeros, bias, y, (int)M, (int)N, (int)d, gsh, mblk, nblk, sg.nsplit, part,
-                       cnt, sys, mmaj, ep.aux, act_form(ep.act), ep.act == PARO_ACT_GELU);
-  } else if (ks4) launch_gemm<4, 2, 1, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
+  // (with an epilogue, tiles few enough to be split go to w4_tiles_kernel)
+  if constexpr (EPI == kEpiPlain) {
+    if (ks4 && sg.nsplit > 1 && cnt && part) {
+      const int sys = !xcd_dispatch_is_round_robin();
+      hipLaunchKernelGGL((w4_gemm_kernel<4, 2, 1, true, EPI>), dim3(g * (unsigned)sg.nsplit), dim3(1024), 0, stream, x,
+                         qweight, scales, zeros, bias, y, (int)M, (int)N, (int)d, gsh, mblk, nblk, sg.nsplit, part,
+                         cnt, sys, mmaj, ep.aux, act_form(ep.act), ep.act == PARO_ACT_GELU);
+      return hipGetLastError();
+    }
+  }
+  if (ks4) launch_gemm<4, 2, 1, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
   else if (narrow && ks2) launch_gemm<2, 2, 1, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
   else if (narrow) launch_gemm<1, 2, 1, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
   else if (half && ks2) launch_gemm<2, 2, 2, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);

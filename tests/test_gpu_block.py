@@ -126,8 +126,8 @@ def test_linear_act(paro, M, d, N, G):
     paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, residual=y, act="silu", y=y, group=G, workspace=ws)
     ref = paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, residual=dev(res), act="silu", group=G, workspace=ws)
     assert torch.equal(y, ref)
-    # no activation and no residual: paro_w4_linear's values (few tokens: sums in another order)
-    if M > 16:
+    # no activation and no residual: paro_w4_linear's values (fewer tokens: sums in another order)
+    if M > 1024:
         y = paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=c.bd, group=G, workspace=ws)
         assert torch.equal(y, paro.paro_w4_linear(None, c.xd, *c.dev, bias=c.bd, group=G, workspace=ws))
     assert ws is None or not ws[:16384].any().item(), "arrival counters not left at zero"
@@ -191,6 +191,44 @@ def test_gradients(paro, M, d, N, G, gated):
     _, full = back(c.xd, *c.dev, dev(dy), bias=c.bd, act="silu", group=G, workspace=ws)
     assert only is None and torch.equal(again, full)
     assert not ws[:16384].any().item(), "arrival counters not left at zero"
+
+
+# 17 tokens to a few hundred (the gradients from one): every tile shape, ragged in
+# tokens and channels, fewer chunks of k than wavefronts and more
+TILES = [(17, 128, 16, 64), (20, 2432, 48, 64), (33, 640, 80, 128), (48, 256, 2768, 64), (64, 1024, 2752, 256),
+         (30, 1152, 8208, 64), (31, 512, 8240, 256), (100, 2176, 4112, 128), (129, 2048, 4112, 256),
+         (250, 2304, 2080, 64), (333, 2560, 1056, 64), (65, 128, 16, 128)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,d,P,G", TILES + [(1, 256, 48, 64), (16, 640, 4112, 128)])
+def test_small_tiles(paro, M, d, P, G, gated):
+    N = P // 32 * 16 if gated else P
+    if N == 0:
+        N = 16
+    rows = 2 * N if gated else N
+    c = Case(seed_of(M, d, P, G) + 9, M, d, rows, G)
+    w, at = c.w(), c.rows_of()
+    res, dy = c.half(M, N), c.half(M, N)
+    for bias, name in [(c.b, "gelu"), (None, "silu")]:
+        log(f"small tiles M={M} d={d} N={N} G={G} gated={gated} {name}")
+        y, check = guarded(M, N)
+        if gated:
+            paro.paro_w4_gated(None, c.xd, *c.dev, bias=dev(bias), act=name, y=y, group=G)
+            want, tol = block.gated(c.x[at], w, bias, name), block.gated_tolerance(c.x[at], w, bias, name)
+        else:
+            paro.paro_w4_linear_act(None, c.xd, *c.dev, bias=dev(bias), residual=dev(res), act=name, y=y, group=G)
+            want = block.linear_act(c.x[at], w, bias, res[at], name)
+            tol = block.linear_tolerance(c.x[at], w, bias, res[at], name)
+        check()
+        within(host(y)[at], want, tol, name)
+        back = paro.paro_w4_gated_backward if gated else paro.paro_w4_linear_act_backward
+        ref = block.gated_backward if gated else block.linear_act_backward
+        dz, check = guarded(M, rows)
+        back(c.xd, *c.dev, dev(dy), bias=dev(bias), act=name, dz=dz, want_dx=False, group=G)
+        check()
+        within(host(dz)[at], ref(c.x[at], w, bias, name, dy[at])[1],
+               block.grad_tolerance(c.x[at], w, bias, name, dy[at], gated), f"{name} dz")
 
 
 @pytest.mark.parametrize("M", [1, 4, 16, 33, 64, 200])
