@@ -374,16 +374,19 @@ def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=No
     import torch
     M, d = x.shape
     N = qweight.shape[0]
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
     need = 0 if workspace is not None else paro_w4_linear_workspace_size(r, M, N, d)
     workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
+    if y is None:
+        y = x.new_empty((M, N))  # fp16 on dev as x has to be
+        y_ptr = y.data_ptr()
+    else:
+        y_ptr = _expect(y, "y", (M, N), f16, dev)
     _check(load_library().paro_w4_linear_act(
         _handle(r), _expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (N, d // 2), u8, dev),
         _expect(scales, "scales", (N, d // group), f16, dev), _expect(zeros, "zeros", (N, d // group), u8, dev),
         _expect(bias, "bias", (N,), f16, dev), _expect(residual, "residual", (M, N), f16, dev), _act(act),
-        _expect(y, "y", (M, N), f16, dev), M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
+        y_ptr, M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
     return y
 
 
@@ -403,16 +406,19 @@ def paro_w4_gated(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, a
     import torch
     M, d = x.shape
     N = qweight.shape[0] // 2
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
     need = 0 if workspace is not None else paro_w4_gated_workspace_size(r, M, N, d)
     workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
+    if y is None:
+        y = x.new_empty((M, N))  # fp16 on dev as x has to be
+        y_ptr = y.data_ptr()
+    else:
+        y_ptr = _expect(y, "y", (M, N), f16, dev)
     _check(load_library().paro_w4_gated(
         _handle(r), _expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (2 * N, d // 2), u8, dev),
         _expect(scales, "scales", (2 * N, d // group), f16, dev),
         _expect(zeros, "zeros", (2 * N, d // group), u8, dev), _expect(bias, "bias", (2 * N,), f16, dev), _act(act),
-        _expect(y, "y", (M, N), f16, dev), M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
+        y_ptr, M, N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
     return y
 
 
