@@ -6,7 +6,11 @@
 // (dequantized and transposed through LDS, fp16, p padded with zeros to a
 // multiple of 128) and the product is then a dense one of two operands whose
 // contraction index is contiguous. W_hat^T costs 2.5 P d bytes moved whatever
-// M is.
+// M is: 10.3 us for 4096 x 4096 (4.1 TB/s), 57.5 for 28672 x 4096 (5.1 TB/s, what
+// a copy reaches), 14% of the product's time at 2048 tokens. The product itself
+// is bound by the matrix cores under the power limit (busy 67% of the time at
+// 2048 x 28672 -> 4096, 393 us, 1224 TFLOP/s; a W4 operand dequantized on the
+// way, 1120).
 #include <algorithm>
 #include <type_traits>
 
@@ -372,7 +376,11 @@ size_t a256(size_t b) { return (b + 255) & ~(size_t)255; }
 int64_t pad128(int64_t n) { return (n + 127) & ~int64_t(127); }
 
 // Tile and k split of the product: the least estimated time, in k-tiles of the
-// 256 x 256 tile, over the tile heights and splits.
+// 256 x 256 tile, over the tile heights and splits: 6 for a round's start and
+// end, and for a split's meeting 5 and 4 per piece of 256 tokens (with the
+// transposition, 64 tokens x 4096 -> 4096 in 4 pieces 31.3 us, in 8 34.4; 1024
+// tokens in 256 tiles of 64 53, in 128 of 128 and two pieces 57; 1024 x 14336 ->
+// 4096 172 and 205).
 struct GradPlan {
   int bm = 256, ksplit = 1;
   int64_t mblk = 0, nblk = 0, tiles = 0;
@@ -393,7 +401,7 @@ GradPlan plan_input_grad(int64_t M, int64_t P, int64_t d) {
       if (ks > 1 && (p.tiles > (int64_t)(kDecodeCounterBytes / 4) || p.tiles * ks > 512)) break;
       const int64_t rounds = (8 * ((p.tiles + 7) / 8) * ks + 255) / 256;
       const int64_t len = 2 * ((H + ks - 1) / ks);
-      const double cost = rounds * (len * kt + 6) + (ks > 1 ? (bm / 256.0) * (5 + 2 * ks) : 0);
+      const double cost = rounds * (len * kt + 6) + (ks > 1 ? 5 + (bm / 256.0) * 4 * ks : 0);
       if (best.mblk == 0 || cost < best_cost) {
         best = p;
         best.ksplit = ks;
