@@ -393,9 +393,11 @@ int paro_layer_loss(const paro_rotation* r, const uint16_t* x, const uint16_t* w
  * The W4 linear with its bias, an activation and a residual in the epilogue:
  *   Y[m][n] = act(Z[m][n]) + R[m][n],
  *   Z[m][n] = sum_k X'[m][k] W_hat[n][k] + bias[n],
- * X', W_hat, sizes, alignment, workspace (paro_w4_linear_workspace_size) and
- * kernels as for paro_w4_linear; Z, the activation and the sum in fp32, one
- * rounding to fp16.
+ * X', W_hat, sizes, alignment and workspace (paro_w4_linear_workspace_size)
+ * as for paro_w4_linear; Z, the activation and the sum in fp32, one rounding
+ * to fp16. Up to a few hundred tokens the product runs in kernels of its own
+ * (where the transform is not fused into it), whose fp32 sums run in another
+ * order: Z may differ from paro_w4_linear's in the last places.
  *   residual  device fp16 [M][N], 16-byte aligned, or NULL; may be y itself
  *             (each value is read before it is replaced), no other overlap.
  *   act       a paro_activation.
@@ -517,9 +519,9 @@ int64_t paro_adamw_moments(int32_t count, const int64_t* n);
  * PARO_ERR_HIP (the table).
  *
  * paro_adamw_step runs step t >= 1 on the current device, in one launch (one
- * for every 2^33 values), without upload, allocation or synchronisation. A captured call
- * replays the t and the rates it was captured with. Steps of one plan must
- * not run at the same time.
+ * for every 2^33 values), without upload, allocation or synchronisation. A
+ * captured call replays the t and the rates it was captured with. Steps of one
+ * plan must not run at the same time.
  * Errors: PARO_ERR_NULL, PARO_ERR_VALUE (step < 1; lr or weight_decay
  * negative, beta outside [0, 1), eps <= 0, or one of them not finite),
  * PARO_ERR_HIP.
