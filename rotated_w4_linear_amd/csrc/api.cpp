@@ -313,6 +313,7 @@ int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const 
                   int64_t M, int64_t N, int64_t d, int32_t group, char* ws, size_t ws_bytes,
                   hipStream_t stream) {
   hipError_t e = hipSuccess;
+  ws_bytes &= ~(size_t)255;  // (X' lies at its end)
   const int64_t P = epi_gated(epi) ? 2 * N : N;  // rows of the weight block
   if (M <= kDecodeMaxM) {
     const paro_rotation* fused = r;

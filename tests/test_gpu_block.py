@@ -257,6 +257,24 @@ def test_with_transform_equals_transformed_first(paro, M, group, K):
            block.linear_tolerance(xh, w, b, host(res), "gelu_tanh"), "linear")
 
 
+@pytest.mark.parametrize("M", [40, 64])
+def test_workspace_of_odd_size(paro, M):
+    """A larger workspace of any number of bytes: X' inside it stays aligned."""
+    d, N, group = 1024, 256, 128
+    x, layer, b = synthetic.linear_case(seed=M, M=M, d=d, N=N, group=group, K=8)
+    r = paro.Rotation(layer.pairs, layer.theta, layer.alpha, group)
+    wq = paro.paro_quantize_weights(r, dev(layer.w), group)
+    xd = dev(x)
+    want = paro.paro_w4_linear_act(r, xd, *wq, act="silu", group=group)
+    plain = paro.paro_w4_linear(r, xd, *wq, group=group)
+    need = paro.paro_w4_linear_workspace_size(r, M, N, d)
+    for extra in (1, 3, 14, 255):
+        log(f"workspace M={M} extra={extra}")
+        ws = torch.zeros(need + extra, dtype=torch.uint8, device="cuda")
+        assert torch.equal(paro.paro_w4_linear_act(r, xd, *wq, act="silu", group=group, workspace=ws), want)
+        assert torch.equal(paro.paro_w4_linear(r, xd, *wq, group=group, workspace=ws), plain)
+
+
 def test_not_finite_stays_in_its_row(paro):
     """A token with an infinity or NaN spoils its own outputs only, in every direction."""
     M, d, N = 70, 512, 144   # N is no multiple of 64: the gradient's contraction is padded
