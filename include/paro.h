@@ -523,8 +523,8 @@ int64_t paro_adamw_moments(int32_t count, const int64_t* n);
  * captured call replays the t and the rates it was captured with. Steps of one
  * plan must not run at the same time.
  * Errors: PARO_ERR_NULL, PARO_ERR_VALUE (step < 1; lr or weight_decay
- * negative, beta outside [0, 1), eps <= 0, or one of them not finite),
- * PARO_ERR_HIP.
+ * negative, beta outside [0, 1), eps <= 0, or one of them, or the rates made
+ * from them, not finite in fp32), PARO_ERR_HIP.
  */
 int paro_adamw_create(int32_t count, const int64_t* n, void* const* params, int32_t param_type,
                       const void* const* grads, int32_t grad_type, int32_t state_bits, void* m,

@@ -373,6 +373,8 @@ int paro_adamw_step(const paro_adamw* h, int64_t step, double lr, double beta1, 
   sc.rate = (float)(lr / c1);
   sc.root = (float)(1.0 / std::sqrt(c2));
   sc.eps = (float)eps;
+  if (!std::isfinite(sc.keep) || !std::isfinite(sc.rate))
+    return fail(PARO_ERR_VALUE, "paro_adamw_step: lr or lr * weight_decay too large for fp32");
   for (size_t i = 0; i < h->chunks.size(); ++i) {
     hipError_t e;
     if (h->parts.empty()) {

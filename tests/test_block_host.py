@@ -144,6 +144,9 @@ def test_adamw_refusals(paro):
                 dict(eps=float("inf")), dict(wd=-1.0), dict(b1=float("nan"))):
         a = dict(step=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0) | bad
         assert lib.paro_adamw_step(h, a["step"], a["lr"], a["b1"], a["b2"], a["eps"], a["wd"], None) == -4, bad
+    # rates that fp32 does not hold: refused, not stepped to infinity
+    assert lib.paro_adamw_step(h, 1, 1e300, 0.9, 0.999, 1e-8, 0.0, None) == -4
+    assert lib.paro_adamw_step(h, 1, 1e20, 0.9, 0.999, 1e-8, 1e20, None) == -4
     assert lib.paro_adamw_step(None, 1, 1e-3, 0.9, 0.999, 1e-8, 0.0, None) == -1
     lib.paro_adamw_destroy(h)
     lib.paro_adamw_destroy(None)
