@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libparo.so")
 SOURCES = ["api.cpp", "plan.cpp", "pairs.cpp", "rotate.hip", "quantize.hip", "w4_linear.hip", "decode.hip",
            "backward.hip", "layer_loss.hip", "noalloc.hip", "dense_gemm.hip", "measure.hip",
            "w4_linear_act.hip", "w4_linear_gated.hip", "w4_linear_act_grad.hip", "w4_linear_gated_grad.hip",
-           "decode_act.hip", "decode_gated.hip", "decode_rows.hip", "w4_tiles.hip",
+           "decode_act.hip", "decode_gated.hip", "decode_rows.hip", "w4_tiles.hip", "w4_input_grad_rows.hip",
            "w4_input_grad.hip", "adamw.hip", "api_block.cpp"]
 
 COMPILE_FLAGS = [

@@ -249,6 +249,14 @@ size_t input_grad_scratch_bytes(int64_t M, int64_t P, int64_t d);
 hipError_t launch_w4_input_grad(const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
                                 const uint8_t* zeros, uint16_t* dx, int64_t M, int64_t P, int64_t d, int group,
                                 uint32_t* cnt, void* ws, hipStream_t stream);
+// The same for few tokens, straight from the codes (w4_input_grad_rows.hip);
+// scratch holds input_grad_rows_bytes. input_grad_rows_fit: whether
+// launch_w4_input_grad takes it.
+bool input_grad_rows_fit(int64_t M);
+size_t input_grad_rows_bytes(int64_t M, int64_t P, int64_t d);
+hipError_t launch_w4_input_grad_rows(const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
+                                     const uint8_t* zeros, uint16_t* dx, int64_t M, int64_t P, int64_t d, int group,
+                                     void* scratch, hipStream_t stream);
 
 // One launch of the AdamW step (adamw.hip). Every tensor is cut into chunks of
 // kAdamChunk values; chunk0 is its first chunk of the launch, block0 its first

@@ -429,6 +429,7 @@ void launch_tiles(const GradPlan& p, const uint16_t* wt, const uint16_t* dz, int
 }  // namespace
 
 size_t input_grad_scratch_bytes(int64_t M, int64_t P, int64_t d) {
+  if (input_grad_rows_fit(M)) return a256(input_grad_rows_bytes(M, P, d));
   const int64_t pp = pad128(P);
   return a256((size_t)d * pp * 2) + (pp != P ? a256((size_t)M * pp * 2) : 0) + plan_input_grad(M, P, d).partial_bytes;
 }
@@ -436,6 +437,8 @@ size_t input_grad_scratch_bytes(int64_t M, int64_t P, int64_t d) {
 hipError_t launch_w4_input_grad(const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
                                 const uint8_t* zeros, uint16_t* dx, int64_t M, int64_t P, int64_t d, int group,
                                 uint32_t* cnt, void* ws, hipStream_t stream) {
+  if (input_grad_rows_fit(M))
+    return launch_w4_input_grad_rows(dz, qweight, scales, zeros, dx, M, P, d, group, ws, stream);
   const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
   const int64_t pp = pad128(P);
   char* at = (char*)ws;

@@ -257,6 +257,35 @@ def test_with_transform_equals_transformed_first(paro, M, group, K):
            block.linear_tolerance(xh, w, b, host(res), "gelu_tanh"), "linear")
 
 
+# straight from the codes, up to 128 tokens: 1, 2 and 4 blocks of 16 tokens and
+# two of 64, one range of weight rows and up to eight, a last chunk of 16, 32 and
+# 48 rows, fewer chunks than wavefronts
+FEW = [(1, 128, 16, 64), (5, 256, 48, 128), (16, 1024, 4128, 256), (17, 384, 1072, 64), (32, 2560, 8208, 128),
+       (33, 4096, 528, 64), (64, 512, 2096, 128), (100, 768, 4112, 256), (128, 8192, 1040, 64), (3, 14336, 1024, 128)]
+
+
+@pytest.mark.parametrize("M,d,P,G", FEW)
+def test_input_gradient_of_few_tokens(paro, M, d, P, G):
+    c = Case(seed_of(M, d, P, G) + 11, M, d, P, G)
+    w, at = c.w(), c.rows_of()
+    dy = c.half(M, P)
+    log(f"few tokens M={M} d={d} P={P} G={G}")
+    ws = paro.new_linear_act_backward_workspace(M, P, d, "none")
+    dx, check = guarded(M, d)
+    for _ in range(2):
+        paro.paro_w4_linear_act_backward(None, *c.dev, dev(dy), dx=dx, group=G, workspace=ws)
+    check()
+    z = dy[at].astype(np.float64)
+    within(host(dx)[at], z @ w, block.input_grad_tolerance(z, w), "dx")
+    # a token that is not finite stays alone, the one behind it included
+    bad = dy.copy()
+    row = M // 2
+    bad[row, ::3], bad[row, 1::3] = np.nan, np.inf
+    again = paro.paro_w4_linear_act_backward(None, *c.dev, dev(bad), group=G, workspace=ws)[0]
+    keep = np.arange(M) != row
+    assert np.array_equal(host(again)[keep], host(dx)[keep]) and not np.isfinite(host(again)[row]).any()
+
+
 @pytest.mark.parametrize("M", [40, 64])
 def test_workspace_of_odd_size(paro, M):
     """A larger workspace of any number of bytes: X' inside it stays aligned."""
