@@ -333,13 +333,14 @@ def test_not_finite_stays_in_its_row(paro):
         assert not np.isnan(got).any()
 
 
-def test_streams_and_capture(paro):
+@pytest.mark.parametrize("M", [16, 100, 300, 1100])
+def test_streams_and_capture(paro, M):
     """Two streams at once, each with its workspace, and captured calls replayed
-    between eager ones."""
-    M, d, N = 16, 4096, 1024
-    c = Case(23, M, d, 2 * N, 128)
+    between eager ones, two graphs on one workspace in turn."""
+    d, N = 4096, 1024
+    c = Case(23 + M, M, d, 2 * N, 128)
     dy = dev(c.half(M, N))
-    log("streams and capture")
+    log(f"streams and capture M={M}")
 
     def all_calls(wss, stream=None):
         y = paro.paro_w4_gated(None, c.xd, *c.dev, bias=c.bd, workspace=wss[0], stream=stream)
@@ -371,13 +372,17 @@ def test_streams_and_capture(paro):
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         outs = all_calls(ws)
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2):
+        outs2 = all_calls(ws)
     for i in range(3):
-        for t in outs:
+        for t in outs + outs2:
             t.zero_()
         g.replay()
+        g2.replay()
         torch.cuda.synchronize()
-        for a, b in zip(outs, ref):
-            assert torch.equal(a, b), f"replay {i}"
+        for a, a2, b in zip(outs, outs2, ref):
+            assert torch.equal(a, b) and torch.equal(a2, b), f"replay {i}"
         for a, b in zip(all_calls(wss[0]), ref):
             assert torch.equal(a, b)
         torch.cuda.synchronize()
