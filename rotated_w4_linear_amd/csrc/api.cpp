@@ -305,6 +305,21 @@ size_t w4_linear_min_workspace(const paro_rotation* r, int64_t M, int64_t N, int
   return kDecodeCounterBytes + (((size_t)M * (size_t)d * 2 + 255) & ~(size_t)255);
 }
 
+// Small batches of a product with an epilogue, where the fused kernel could
+// transform as well: whether the stand-alone transform and the kernels for
+// transformed activations (no partial sums in memory) are the faster way, and
+// X' fits the minimum workspace (it does beyond 512 channels and 256 rows).
+// Measured, fused against transformed first: from 17 tokens on always (24
+// tokens, 4096 -> 4096 14.5 against 11.3 us, 1024 -> 256 11.1 against 7.8); to
+// 16 tokens from 2^24 weights on (1 and 16 tokens, 4096 -> 4096 9.1 against 8.0
+// and 10.9 against 10.3, 14336 -> 4096 17.7 against 13.9 and 28.3 against 18.6,
+// gated 4096 -> 14336 23.3 against 21.9 and 32.4 against 23.1; gated 4096 ->
+// 1024, 2^23, 8.8 against 9.2 and 10.0 against 11.5).
+bool transforms_first(const paro_rotation* r, int64_t M, int64_t P, int64_t d) {
+  const size_t xbytes = ((size_t)M * (size_t)d * 2 + 255) & ~(size_t)255;
+  return (M > 16 || P * d >= (int64_t(1) << 24)) && w4_linear_min_workspace(r, M, P, d) >= kDecodeCounterBytes + xbytes;
+}
+
 // The launches of a W4 product on a checked workspace ws of ws_bytes bytes
 // (at least w4_linear_min_workspace of the weight block's rows; NULL when that
 // is 0). N: output channels.
@@ -318,7 +333,7 @@ int run_w4_product(int epi, const W4Epilogue& ep, const paro_rotation* r, const 
   if (M <= kDecodeMaxM) {
     const paro_rotation* fused = r;
     const uint16_t* xin = x;
-    if (r && !decode_fuses_rotation(r, M, P, d)) {
+    if (r && (!decode_fuses_rotation(r, M, P, d) || (epi != kEpiPlain && transforms_first(r, M, P, d)))) {
       // stand-alone transform into the workspace tail, then the plain kernel
       uint16_t* xr = (uint16_t*)(ws + ws_bytes - (((size_t)M * (size_t)d * 2 + 255) & ~(size_t)255));
       e = launch_rotate(r, x, xr, M, stream);

@@ -459,7 +459,8 @@ hipError_t launch_plan(const uint16_t* x, const uint8_t* qw, const uint16_t* sc,
 
 // N: output channels (rows of the weight block, half of them for the gated
 // epilogue). With an epilogue r is a plan whose transform this kernel runs, and
-// M <= 32 (other calls go to w4_rows_kernel and w4_tiles_kernel).
+// M <= 32, beyond 16 only where the workspace has no room for X' (other calls go
+// to w4_rows_kernel and w4_tiles_kernel).
 template <int EPI>
 hipError_t launch_w4_decode_epi(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                                 const uint8_t* zeros, const uint16_t* bias, uint16_t* y, int64_t M,

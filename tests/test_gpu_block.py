@@ -257,6 +257,28 @@ def test_with_transform_equals_transformed_first(paro, M, group, K):
            block.linear_tolerance(xh, w, b, host(res), "gelu_tanh"), "linear")
 
 
+@pytest.mark.parametrize("M,d,N,group,K", [(1, 4096, 4112, 128, 8), (3, 8192, 1040, 64, 4), (16, 4096, 4112, 128, 8),
+                                           (24, 512, 32, 128, 8), (32, 512, 16, 256, 8), (20, 256, 528, 64, 8),
+                                           (17, 14336, 640, 128, 8)])
+def test_transform_inside_by_size(paro, M, d, N, group, K):
+    """A plan r in calls whose transform runs first (2^24 weights, 17 tokens) and
+    in those where the workspace leaves no room for X'."""
+    log(f"transform by size M={M} d={d} N={N} G={group}")
+    x, layer, b = synthetic.linear_case(seed=M + d, M=M, d=d, N=2 * N, group=group, K=K)
+    r = paro.Rotation(layer.pairs, layer.theta, layer.alpha, group)
+    wq = paro.paro_quantize_weights(r, dev(layer.w), group)
+    xd, bd = dev(x), dev(b)
+    w, xh = block.weights(*(host(t) for t in wq), group), host(paro.paro_rotate(r, xd))
+    wss = paro.new_workspace(r, M, 2 * N, d), paro.new_gated_workspace(r, M, N, d)
+    for _ in range(2):
+        y = paro.paro_w4_linear_act(r, xd, *wq, bias=bd, act="silu", group=group, workspace=wss[0])
+        g = paro.paro_w4_gated(r, xd, *wq, bias=bd, act="gelu", group=group, workspace=wss[1])
+        within(host(y), block.linear_act(xh, w, b, None, "silu"), block.linear_tolerance(xh, w, b, None, "silu"), "act")
+        within(host(g), block.gated(xh, w, b, "gelu"), block.gated_tolerance(xh, w, b, "gelu"), "gated")
+    for ws in wss:
+        assert not ws[:16384].any().item(), "arrival counters not left at zero"
+
+
 # straight from the codes, up to 128 tokens: 1, 2 and 4 blocks of 16 tokens and
 # two of 64, one range of weight rows and up to eight, a last chunk of 16, 32 and
 # 48 rows, fewer chunks than wavefronts
