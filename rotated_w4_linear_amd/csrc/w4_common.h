@@ -67,9 +67,12 @@ __device__ __forceinline__ uint32_t half_bits(float f) {
 // Meeting of the `pieces` workgroups that share a tile's contraction, on one
 // counter that is zero between calls. Each takes a ticket when its sums are
 // ready; all but the last to do so store their partial tile and report it, and
-// the last waits for the reports of the others. These have all taken their tickets, so they are running and wait for
-// nobody: the wait ends. Low half: tickets, high half: reports. sys: the
-// workgroups may sit on different XCDs.
+// the last waits for the reports of the others. These have all taken their
+// tickets, so they are running and wait for nobody: the wait ends. (Bounded all
+// the same, to seconds: on counters that were not zero, or shared by two calls
+// at once, the sums are wrong, but the kernel ends.) Low half: tickets, high
+// half: reports. sys: the workgroups may sit on different XCDs.
+constexpr int kMeetSpins = 1 << 22;
 __device__ __forceinline__ uint32_t meet_add(uint32_t* cnt, uint32_t v, int sys) {
   return sys ? __hip_atomic_fetch_add(cnt, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM)
              : __hip_atomic_fetch_add(cnt, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -92,10 +95,12 @@ __device__ __forceinline__ void meet_wait(uint32_t* cnt, int pieces, int sys) {
   if (threadIdx.x == 0) {
     const uint32_t all = (uint32_t)(pieces - 1);
     if (sys) {
-      while (__hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) >> 16 != all) __builtin_amdgcn_s_sleep(1);
+      for (int i = 0; i < kMeetSpins && __hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) >> 16 != all; ++i)
+        __builtin_amdgcn_s_sleep(1);
       __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     } else {
-      while (__hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >> 16 != all) __builtin_amdgcn_s_sleep(1);
+      for (int i = 0; i < kMeetSpins && __hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >> 16 != all; ++i)
+        __builtin_amdgcn_s_sleep(1);
       __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
