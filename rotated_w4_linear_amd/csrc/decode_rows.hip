@@ -146,12 +146,10 @@ void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
           const u4 v = *(const u4*)(wl + 4096 * j + 256 * r + 16 * ((4 * g + kq) ^ r));
           const h2 ss = splat2(__builtin_bit_cast(_Float16, (uint16_t)sraw[j][g]));
           const float zf = (float)zraw[j][g];
-          const h2 ss16 = ss * splat2((_Float16)0.0625f);
-          const h2 zz = splat2((_Float16)(1024.0f + zf)), zz16 = splat2((_Float16)(1024.0f + 16.0f * zf));
+          const h2 zz = splat2((_Float16)(1024.0f + zf)), zz64 = splat2((_Float16)(64.0f + zf));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(v[i], zz, ss, zz16, ss16, one), b[i], acc[j], 0,
-                                                            0, 0);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(v[i], zz, zz64, ss, one), b[i], acc[j], 0, 0, 0);
         }
       }
     }
@@ -310,12 +308,11 @@ void w4_rows_stream_kernel(const uint16_t* __restrict__ x, const uint8_t* __rest
             const u4 v = *(const u4*)(buf + 4096 * j + 256 * r + 16 * ((4 * g + kq) ^ r));
             const h2 ss = splat2(__builtin_bit_cast(_Float16, (uint16_t)s[j][g]));
             const float zf = (float)z[j][g];
-            const h2 ss16 = ss * splat2((_Float16)0.0625f);
-            const h2 zz = splat2((_Float16)(1024.0f + zf)), zz16 = splat2((_Float16)(1024.0f + 16.0f * zf));
+            const h2 zz = splat2((_Float16)(1024.0f + zf)), zz64 = splat2((_Float16)(64.0f + zf));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(v[i], zz, ss, zz16, ss16, one), xf[k][g][i],
-                                                              acc[j], 0, 0, 0);
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(v[i], zz, zz64, ss, one), xf[k][g][i], acc[j],
+                                                              0, 0, 0);
           }
         }
       }

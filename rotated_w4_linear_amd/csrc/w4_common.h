@@ -19,21 +19,26 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 // channel order (word = c0 | c2 << 4 | c4 << 8 | c6 << 12 | c1 << 16 | ...).
 // Masking one nibble of each 16-bit half and OR-ing in the fp16 pattern of
 // 1024.0 gives the pair (c_{2i}, c_{2i+1}) in channel order: with the mask
-// 0x000F000F as 1024 + q, with 0x00F000F0 as 1024 + 16 q. Then (v - (1024 +
-// z)) = q - z (or 16 (q - z)) is exact in packed fp16, and one packed multiply
-// by s (or s / 16, exact: a power of two) rounds (q - z) s once. Eight values
-// cost one shift, four and-or and eight packed fp16 operations.
+// 0x000F000F as v = 1024 + q, with 0x00F000F0 as v = 1024 + 16 q. Then v -
+// (1024 + z) or, fused, v / 16 - (64 + z) is exactly q - z in packed fp16, and
+// one packed multiply by s rounds (q - z) s once, to a subnormal too. (The
+// sixteenth is taken of v and not of s: s / 16 is not exact below s = 2^-10.)
+// Eight values cost one shift, four and-or and eight packed fp16 operations.
 //
-// zz = (1024 + z, 1024 + z), ss = (s, s), zz16 = (1024 + 16 z, ...),
-// ss16 = (s / 16, ...); `one` = 0x64006400 held in a vector register, so that
-// each (w & mask) | one is a single v_and_or_b32 (the mask is then the only
-// scalar operand, as gfx9 encodings allow).
-__device__ __forceinline__ h8 dequant8(uint32_t w, h2 zz, h2 ss, h2 zz16, h2 ss16, uint32_t one) {
+// zz = (1024 + z, 1024 + z), zz64 = (64 + z, 64 + z), ss = (s, s); `one` =
+// 0x64006400 held in a vector register, so that each (w & mask) | one is a
+// single v_and_or_b32 (the mask is then the only scalar operand, as gfx9
+// encodings allow).
+__device__ __forceinline__ h8 dequant8(uint32_t w, h2 zz, h2 zz64, h2 ss, uint32_t one) {
   const uint32_t w8 = w >> 8;
+  const h2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+  auto high = [&](uint32_t bits) {
+    return __builtin_elementwise_fma(__builtin_bit_cast(h2, bits | one), sixteenth, -zz64) * ss;
+  };
   const h2 v0 = (__builtin_bit_cast(h2, (w & 0x000F000Fu) | one) - zz) * ss;      // c0, c1
-  const h2 v1 = (__builtin_bit_cast(h2, (w & 0x00F000F0u) | one) - zz16) * ss16;  // c2, c3
+  const h2 v1 = high(w & 0x00F000F0u);                                            // c2, c3
   const h2 v2 = (__builtin_bit_cast(h2, (w8 & 0x000F000Fu) | one) - zz) * ss;     // c4, c5
-  const h2 v3 = (__builtin_bit_cast(h2, (w8 & 0x00F000F0u) | one) - zz16) * ss16; // c6, c7
+  const h2 v3 = high(w8 & 0x00F000F0u);                                           // c6, c7
   h8 out;
   out[0] = v0.x;
   out[1] = v0.y;

@@ -236,13 +236,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TB == 1 ? 4
 #pragma unroll
   for (int q = 0; q < DK_SEGS; ++q) {
     if (q < nq) {
-      h2 ss[TJ], zz[TJ], ss16[TJ], zz16[TJ];
+      h2 ss[TJ], zz[TJ], zz64[TJ];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
         ss[j] = splat2(__builtin_bit_cast(_Float16, (uint16_t)sraw[j][q]));
-        ss16[j] = ss[j] * splat2((_Float16)0.0625f);
         zz[j] = splat2((_Float16)(1024.0f + (float)zraw[j][q]));
-        zz16[j] = splat2((_Float16)(1024.0f + 16.0f * (float)zraw[j][q]));
+        zz64[j] = splat2((_Float16)(64.0f + (float)zraw[j][q]));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -254,7 +253,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TB == 1 ? 4
         }
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
-          const h8 a = dequant8(wv[j][q][i], zz[j], ss[j], zz16[j], ss16[j], one);
+          const h8 a = dequant8(wv[j][q][i], zz[j], zz64[j], ss[j], one);
 #pragma unroll
           for (int tb = 0; tb < TB; ++tb)
             acc[tb][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[tb], acc[tb][j], 0, 0, 0);

@@ -251,23 +251,22 @@ void w4_gemm_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
     dma(min(kt + 1, KT - 1), xn, wn, sn, zn);
     __builtin_amdgcn_sched_barrier(0);
     u4 wf[2];
-    h2 ss[2], zz[2], ss16[2], zz16[2];
+    h2 ss[2], zz[2], zz64[2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r = 32 * NT * w + 32 * j + l32;
       wf[j] = wl[2 * r + (g ^ ((r >> 3) & 1))];
       // (rows past N read the last row's scale, clamped by the DMA; never stored)
       ss[j] = splat2(__builtin_bit_cast(_Float16, (uint16_t)(ss_l[r] & 0xffffu)));
-      ss16[j] = ss[j] * splat2((_Float16)0.0625f);
       const float zf = (float)(zs_l[r] & 0xffu);
       zz[j] = splat2((_Float16)(1024.0f + zf));
-      zz16[j] = splat2((_Float16)(1024.0f + 16.0f * zf));
+      zz64[j] = splat2((_Float16)(64.0f + zf));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       h8 a[2], b[MT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) a[j] = dequant8(wf[j][i], zz[j], ss[j], zz16[j], ss16[j], one);
+      for (int j = 0; j < NT; ++j) a[j] = dequant8(wf[j][i], zz[j], zz64[j], ss[j], one);
 #pragma unroll
       for (int mm = 0; mm < MT; ++mm) {
         const int r = 32 * mm + l32;
@@ -657,7 +656,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // n tiles and their group's scale and zero, in the forms dequant8 takes.
   struct Params {
     u4 wf[4];
-    h2 ss[4], zz[4], ss16[4], zz16[4];
+    h2 ss[4], zz[4], zz64[4];
   };
   // the LDS reads of the operands (raw scale and zero words), then their
   // conversion
@@ -685,10 +684,9 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
     for (int j = 0; j < WN; ++j) {
       p.wf[j] = q.wf[j];
       p.ss[j] = splat2(__builtin_bit_cast(_Float16, (uint16_t)(q.s[j] & 0xffffu)));
-      p.ss16[j] = p.ss[j] * splat2((_Float16)0.0625f);
       const float zf = (float)(q.z[j] & 0xffu);
       p.zz[j] = splat2((_Float16)(1024.0f + zf));
-      p.zz16[j] = splat2((_Float16)(1024.0f + 16.0f * zf));
+      p.zz64[j] = splat2((_Float16)(64.0f + zf));
     }
   };
   auto load_params = [&](int kt, const u4* wl, const uint32_t* ss_l, const uint32_t* zs_l, Params& p) {
@@ -706,7 +704,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   };
   auto deq = [&](const Params& p, int i, h8* af) {
 #pragma unroll
-    for (int j = 0; j < WN; ++j) af[j] = dequant8(p.wf[j][i], p.zz[j], p.ss[j], p.zz16[j], p.ss16[j], one);
+    for (int j = 0; j < WN; ++j) af[j] = dequant8(p.wf[j][i], p.zz[j], p.zz64[j], p.ss[j], one);
   };
   auto mma = [&](const h8* af, const h8* bf) {
 #pragma unroll
@@ -770,12 +768,12 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
     sched_chunk<0, 3 * WN, 0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < WN / 2; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.ss[j], Pn.zz16[j], Pn.ss16[j], one);
+    for (int j = 0; j < WN / 2; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.zz64[j], Pn.ss[j], one);
     mma4(2, a, b);
     sched_chunk<0, (13 * WN / 2 + 3) / 4, 0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = WN / 2; j < WN; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.ss[j], Pn.zz16[j], Pn.ss16[j], one);
+    for (int j = WN / 2; j < WN; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.zz64[j], Pn.ss[j], one);
     mma4(3, a, b);
     sched_chunk<0, (13 * WN / 2 + 3) / 4, 0>();
     __builtin_amdgcn_sched_barrier(0);

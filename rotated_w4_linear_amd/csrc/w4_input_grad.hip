@@ -58,8 +58,7 @@ __global__ __launch_bounds__(256) void w4_transpose_kernel(const uint8_t* __rest
     const h2 ss = splat2(__builtin_bit_cast(_Float16, s));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[b][i] = dequant8(c[i], splat2((_Float16)(1024.0f + z)), ss, splat2((_Float16)(1024.0f + 16.0f * z)),
-                         ss * splat2((_Float16)0.0625f), one);
+      v[b][i] = dequant8(c[i], splat2((_Float16)(1024.0f + z)), splat2((_Float16)(64.0f + z)), ss, one);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

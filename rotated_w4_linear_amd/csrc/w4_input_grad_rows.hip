@@ -109,12 +109,12 @@ void w4_grad_rows_kernel(const uint8_t* __restrict__ qw, const uint16_t* __restr
       const uint32_t off = doff[t] + (uint32_t)(2 * p0 + 16 * piece);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void*)(zl + 1024 * t), 16, off, 0, 0, 0);
     }
-    // scale | scale / 16, 1024 + z | 1024 + 16 z (rows past P: scale zero)
+    // scale | 0, 1024 + z | 64 + z (rows past P: scale zero)
     auto form = [&](uint32_t s, uint32_t z) {
       const _Float16 ss = __builtin_bit_cast(_Float16, (uint16_t)(lane < left ? s : 0u));
       const float zf = (float)z;
-      const h2 a = {ss, ss * (_Float16)0.0625f};
-      const h2 b = {(_Float16)(1024.0f + zf), (_Float16)(1024.0f + 16.0f * zf)};
+      const h2 a = {ss, (_Float16)0.0f};
+      const h2 b = {(_Float16)(1024.0f + zf), (_Float16)(64.0f + zf)};
       return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
     };
     tab[2 * lane] = form(s0, z0);
@@ -130,7 +130,7 @@ void w4_grad_rows_kernel(const uint8_t* __restrict__ qw, const uint16_t* __restr
         const uint32_t code = *(const uint32_t*)(cl + 64 * (32 * s + 4 * i + kq) + 4 * r);
         const uint2 q = tab[2 * (32 * s + 8 * kq + i) + (gsh == 0 ? r >> 3 : 0)];
         const h2 a = __builtin_bit_cast(h2, q.x), b = __builtin_bit_cast(h2, q.y);
-        v[i] = __builtin_bit_cast(u4, dequant8(code, splat2(b[0]), splat2(a[0]), splat2(b[1]), splat2(a[1]), one));
+        v[i] = __builtin_bit_cast(u4, dequant8(code, splat2(b[0]), splat2(b[1]), splat2(a[0]), one));
       }
       h8 bf[4];
       const bool in = 32 * s + 8 * kq < left;

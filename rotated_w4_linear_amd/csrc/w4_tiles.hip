@@ -115,7 +115,7 @@ void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(xl + 1024 * t), 16, xoff[t], 256 * c, 0, 0);
     __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
     u4 v[TC];
-    h2 ss[TC], ss16[TC], zz[TC], zz16[TC];
+    h2 ss[TC], zz[TC], zz64[TC];
 #pragma unroll
     for (int j = 0; j < TC; ++j) {
       uint32_t sz = __shfl((int)sz0, 16 * j + r);
@@ -125,10 +125,9 @@ void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       }
       v[j] = *(const u4*)(wl + 1024 * j + 64 * r + 16 * (kq ^ (r >> 2)));
       ss[j] = splat2(__builtin_bit_cast(_Float16, (uint16_t)(sz & 0xffffu)));
-      ss16[j] = ss[j] * splat2((_Float16)0.0625f);
       const float zf = (float)(sz >> 16);
       zz[j] = splat2((_Float16)(1024.0f + zf));
-      zz16[j] = splat2((_Float16)(1024.0f + 16.0f * zf));
+      zz64[j] = splat2((_Float16)(64.0f + zf));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -137,7 +136,7 @@ void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       for (int t = 0; t < TT; ++t) b[t] = *(const h8*)(xl + 4096 * t + 256 * r + 16 * ((4 * kq + i) ^ r));
 #pragma unroll
       for (int j = 0; j < TC; ++j) {
-        const h8 a = dequant8(v[j][i], zz[j], ss[j], zz16[j], ss16[j], one);
+        const h8 a = dequant8(v[j][i], zz[j], zz64[j], ss[j], one);
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[t], acc[j][t], 0, 0, 0);
       }

@@ -1,0 +1,90 @@
+"""W4 products and AdamW on the GPU where values, sizes and call forms are at an edge."""
+import numpy as np
+import pytest
+
+from oracle import block
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def paro():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import rotated_w4_linear_amd as p
+    p.load_library()
+    p.paro_device_init()
+    return p
+
+
+def dev(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.cpu().numpy()
+
+
+def log(msg):
+    print(msg, flush=True)
+
+
+# ---------------------------------------------------------------------------
+# small scales
+# ---------------------------------------------------------------------------
+
+class SmallScales:
+    """Random codes with scales from 2^-16 to 2^-9: the sixteenth of a scale below 2^-10 is no fp16 number."""
+
+    def __init__(self, rows, d, group):
+        rng = np.random.default_rng(rows + d + group)
+        self.qw = rng.integers(0, 256, (rows, d // 2), dtype=np.uint8)
+        self.s = np.exp2(rng.uniform(-16, -9, (rows, d // group))).astype(np.float16)
+        self.z = rng.integers(0, 16, (rows, d // group)).astype(np.uint8)
+        self.w = block.weights(self.qw, self.s, self.z, group)
+        self.dev = [dev(a) for a in (self.qw, self.s, self.z)]
+
+
+def one_hot(M, n):
+    """[M][n] with 1024 in one column of each row (neighbouring columns: every place of a word of
+    codes), and the columns. A product with it is one weight times 2^10, which fp16 holds exactly."""
+    cols = (np.arange(M) * 37 + np.arange(M) // 5) % n
+    x = np.zeros((M, n), np.float16)
+    x[np.arange(M), cols] = 1024.0
+    return x, cols
+
+
+# few tokens (a workgroup per block, and one per CU going from block to block),
+# tiles of 16 to 64 tokens, smaller tiles of the large-batch kernels, 256 x 256 tiles
+@pytest.mark.parametrize("M,d,N,G", [(1, 512, 64, 128), (4, 1024, 4128, 128), (16, 640, 80, 64), (13, 512, 4112, 256),
+                                     (30, 640, 48, 128), (40, 512, 96, 256), (333, 2560, 1040, 64),
+                                     (500, 384, 4112, 64), (2048, 768, 16400, 128)])
+def test_products_of_small_scales(paro, M, d, N, G):
+    log(f"small scales M={M} d={d} N={N} G={G}")
+    x, cols = one_hot(M, d)
+    xd = dev(x)
+    c = SmallScales(N, d, G)
+    want = 1024.0 * c.w[:, cols].T
+    assert np.array_equal(host(paro.paro_w4_linear(None, xd, *c.dev, group=G)), want), "linear"
+    assert np.array_equal(host(paro.paro_w4_linear_act(None, xd, *c.dev, group=G)), want), "linear_act"
+    c = SmallScales(2 * N, d, G)
+    z = 1024.0 * c.w[:, cols].T
+    want = (z[:, :N] * z[:, N:]).astype(np.float16)
+    assert np.array_equal(host(paro.paro_w4_gated(None, xd, *c.dev, act="none", group=G)), want), "gated"
+    dy = torch.ones((M, N), dtype=torch.float16, device="cuda")
+    _, dz = paro.paro_w4_gated_backward(xd, *c.dev, dy, act="none", want_dx=False, group=G)
+    assert np.array_equal(host(dz), np.concatenate([z[:, N:], z[:, :N]], 1)), "gated backward"
+
+
+# straight from the codes in 1, 2 and 4 blocks of 16 tokens, and through the transposed weights
+@pytest.mark.parametrize("M,d,P,G", [(1, 512, 48, 64), (16, 256, 1040, 128), (30, 512, 272, 256), (100, 384, 4112, 64),
+                                     (300, 512, 1040, 128)])
+def test_input_gradient_of_small_scales(paro, M, d, P, G):
+    log(f"input gradient of small scales M={M} d={d} P={P} G={G}")
+    dy, rows = one_hot(M, P)
+    c = SmallScales(P, d, G)
+    dx, _ = paro.paro_w4_linear_act_backward(None, *c.dev, dev(dy), group=G)
+    assert np.array_equal(host(dx), 1024.0 * c.w[rows])
