@@ -444,8 +444,9 @@ int paro_w4_gated(const paro_rotation* r, const uint16_t* x, const uint8_t* qwei
  *   x     device fp16 [M][d]: X', the transformed activations (not needed,
  *         may be NULL, for a linear without activation);
  *   dy    device fp16 [M][N];
- *   dz    device fp16 [M][N], gated [M][2N] (gate, then up), overwritten; may
- *         be NULL for a linear without activation, where dZ is dY;
+ *   dz    device fp16 [M][N], gated [M][2N] (gate, then up), overwritten; for a
+ *         linear without activation, where dZ is dY, it may be NULL or dy (else
+ *         dY is copied there);
  *   dx    device fp16 [M][d], overwritten, or NULL (dz alone);
  *   all 16-byte aligned and not overlapping; act, bias, sizes as for the
  *   forward calls, at most 2^21 weight rows; M == 0 is a no-op.

@@ -455,7 +455,8 @@ def _backward(fn, new_workspace_, rows, cols, computes, x, qweight, scales, zero
 def paro_w4_linear_act_backward(x, qweight, scales, zeros, dy, bias=None, act: str = "none", dz=None, dx=None,
                                 want_dx: bool = True, group: int = 128, workspace=None, stream=None):
     """Gradients of paro_w4_linear_act for the transformed activations ``x`` (X'; may be None without
-    activation) and dy = dL/dY: returns (dx fp16 [M][d] or None, dz fp16 [M][N] or None where dZ is dy)."""
+    activation) and dy = dL/dY: returns (dx fp16 [M][d] or None, dz fp16 [M][N]; without activation, where dZ
+    is dy, a copy of dy if ``dz`` is given, else None)."""
     M, N = dy.shape
     return _backward(load_library().paro_w4_linear_act_backward,
                      lambda: new_linear_act_backward_workspace(M, N, 2 * qweight.shape[1], act, dy.device), N, N,

@@ -85,21 +85,27 @@ int run_backward(const char* fn, bool gated, const uint16_t* x, const uint8_t* q
   const int64_t P = gated ? 2 * N : N;
   const bool product = gated || act != PARO_ACT_NONE;  // whether dz has to be computed
   if (P > (int64_t(1) << 21)) return fail(PARO_ERR_UNSUPPORTED, f + ": at most 2^21 weight rows");
-  // (x and dz are not read when dz is dy itself: dy stands in for them in the checks)
+  // (without a product x is not read and dz may be NULL: dy stands in for them in the checks)
   bool noop = false;
   const int st = check_w4_linear(fn, nullptr, product ? x : dy, qweight, scales, zeros, product ? bias : nullptr,
                                  product ? dz : dy, M, P, d, group, &noop);
   if (st != PARO_OK || noop) return st;
   if (!dy) return fail(PARO_ERR_NULL, f + ": NULL tensor");
-  if (!aligned16(dy) || !aligned16(dx)) return fail(PARO_ERR_ALIGN, f + ": dy and dx must be 16-byte aligned");
-  if (!product && !dx) return PARO_OK;
+  if (!aligned16(dy) || !aligned16(dz) || !aligned16(dx))
+    return fail(PARO_ERR_ALIGN, f + ": dy, dz and dx must be 16-byte aligned");
+  const bool copy = !product && dz && dz != dy;  // dZ = dY, for a caller who gave a place for it
   const size_t first = product_scratch(product, M, P, d);
   const size_t need = first + (dx ? input_grad_scratch_bytes(M, P, d) : 0);
-  if (!workspace || workspace_bytes < need)
+  if ((product || dx) && (!workspace || workspace_bytes < need))
     return fail(PARO_ERR_WORKSPACE, f + ": workspace missing or smaller than the size reported for these arguments");
   if ((uintptr_t)workspace & 255) return fail(PARO_ERR_ALIGN, f + ": workspace must be 256-byte aligned");
   char* ws = (char*)workspace;
   hipError_t e = hipSuccess;
+  if (copy) {
+    const size_t bytes = (size_t)M * (size_t)N * 2;  // (N % 16 == 0)
+    e = launch_stream_copy(dy, dz, bytes, (int)std::min<size_t>(8192, (bytes + 16383) / 16384), stream);
+    if (e != hipSuccess) return hip_fail(e, fn);
+  }
   if (product) {
     W4Epilogue ep;
     ep.aux = dy;

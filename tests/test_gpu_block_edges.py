@@ -88,3 +88,28 @@ def test_input_gradient_of_small_scales(paro, M, d, P, G):
     c = SmallScales(P, d, G)
     dx, _ = paro.paro_w4_linear_act_backward(None, *c.dev, dev(dy), group=G)
     assert np.array_equal(host(dx), 1024.0 * c.w[rows])
+
+
+# ---------------------------------------------------------------------------
+# dz where it is dy
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,N", [(1, 16), (3, 80), (130, 1040), (2100, 4112)])
+@pytest.mark.parametrize("want_dx", [False, True])
+def test_dz_without_activation(paro, M, N, want_dx):
+    """Without an activation dZ is dY: a dz that is given receives it, bit for bit, and nothing beside it."""
+    log(f"dz without activation M={M} N={N} dx={want_dx}")
+    d = 256
+    c = SmallScales(N, d, 128)
+    dy = torch.from_numpy(np.random.default_rng(M).integers(0, 1 << 16, (M, N), dtype=np.uint16).view(np.int16)).cuda()
+    buf = torch.full(((M + 2) * N,), 777, dtype=torch.int16, device="cuda")
+    dz = buf[N:(M + 1) * N].view(M, N)
+    dx, got = paro.paro_w4_linear_act_backward(None, *c.dev, dy.view(torch.float16), dz=dz.view(torch.float16),
+                                               want_dx=want_dx)
+    assert (dx is None) == (not want_dx)
+    assert torch.equal(got.view(torch.int16), dy) and torch.equal(dz, dy)
+    assert (buf[:N] == 777).all() and (buf[(M + 1) * N:] == 777).all()
+    # dy itself, and no place at all
+    assert paro.paro_w4_linear_act_backward(None, *c.dev, dy.view(torch.float16), dz=dy.view(torch.float16))[1] is not None
+    assert torch.equal(dz, dy)
+    assert paro.paro_w4_linear_act_backward(None, *c.dev, dy.view(torch.float16))[1] is None
