@@ -69,12 +69,18 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
   return z < 0.0f ? q : 1.0f - q;
 }
 
+// u of act_form. The square's term is held finite: with b = 0 an infinite z
+// would make it NaN, and silu(+inf) is +inf.
+__device__ __forceinline__ float act_argument(float z, const ActForm& f) {
+  return z * (f.a + __builtin_fminf(f.b * z * z, 3.402823466e+38f));
+}
+
 // (a NaN passes through every form: the relu keeps what is not below zero)
 template <bool ERF>
 __device__ __forceinline__ float act_value(float z, const ActForm& f) {
   float e;
   if constexpr (ERF) return z * normal_cdf(z, e);
-  const float s = z * sigmoid(z * (f.a + f.b * z * z));
+  const float s = z * sigmoid(act_argument(z, f));
   const float r = z < 0.0f ? 0.0f : z;
   return f.kind == 1 ? s : f.kind == 2 ? r : z;
 }
@@ -88,7 +94,7 @@ __device__ __forceinline__ void act_both(float z, const ActForm& f, float& v, fl
     v = z * phi;
     dv = phi + z * 0.3989422804014327f * e;
   } else {
-    const float s = sigmoid(z * (f.a + f.b * z * z));
+    const float s = sigmoid(act_argument(z, f));
     const float sv = z * s;
     const float sd = s + sv * (1.0f - s) * (f.a + 3.0f * f.b * z * z);
     const float r = z < 0.0f ? 0.0f : z;

@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+import synthetic
 from oracle import block
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +114,39 @@ def test_dz_without_activation(paro, M, N, want_dx):
     assert paro.paro_w4_linear_act_backward(None, *c.dev, dy.view(torch.float16), dz=dy.view(torch.float16))[1] is not None
     assert torch.equal(dz, dy)
     assert paro.paro_w4_linear_act_backward(None, *c.dev, dy.view(torch.float16))[1] is None
+
+
+# ---------------------------------------------------------------------------
+# infinite pre-activations
+# ---------------------------------------------------------------------------
+
+# every kernel with an epilogue: few tokens (both forms), small tiles, smaller
+# tiles, 256 x 256 tiles; with a plan (K >= 0) the kernel that transforms as well
+@pytest.mark.parametrize("M,d,N,K", [(1, 512, 64, -1), (4, 1024, 4128, -1), (40, 512, 96, -1), (500, 384, 4112, -1),
+                                     (2048, 768, 16400, -1), (4, 512, 64, 8)])
+def test_infinite_preactivations(paro, M, d, N, K):
+    """Z = bias: +inf stays +inf under every activation, and times the other factor of a gated product."""
+    log(f"infinite pre-activations M={M} d={d} N={N} K={K}")
+    r = None
+    if K >= 0:
+        _, layer, _ = synthetic.linear_case(seed=K, M=M, d=d, N=N, group=128, K=K)
+        r = paro.Rotation(layer.pairs, layer.theta, layer.alpha, 128)
+    x = torch.zeros((M, d), dtype=torch.float16, device="cuda")
+    c = SmallScales(2 * N, d, 128)
+    one = [t[:N].contiguous() for t in c.dev]
+    bias = np.zeros(2 * N, np.float16)
+    bias[0:N:7], bias[3:N:7] = np.inf, 60000.0            # gate
+    bias[N:], bias[N + 1::2] = 2.0, -0.5                   # up
+    up, down = np.isposinf(bias[:N]), bias[:N] > 50000
+    want_gated = np.where(up, np.where(bias[N:] > 0, np.inf, -np.inf), 0)
+    dy = torch.ones((M, N), dtype=torch.float16, device="cuda")
+    for act in block.ACTIVATIONS:
+        y = host(paro.paro_w4_linear_act(r, x, *one, bias=dev(bias[:N]), act=act))
+        assert np.isposinf(y[:, up]).all(), act
+        assert (y[:, down & ~up] == np.float16(60000.0)).all() and (y[:, ~down] == 0).all(), act
+        g = host(paro.paro_w4_gated(r, x, *c.dev, bias=dev(bias), act=act))
+        assert np.array_equal(g[:, up], np.broadcast_to(want_gated[up], (M, up.sum()))), act
+        if r is None:  # dzu = dy act(zg)
+            _, dz = paro.paro_w4_gated_backward(x, *c.dev, dy, bias=dev(bias), act=act, want_dx=False)
+            dzu = host(dz)[:, N:]
+            assert np.isposinf(dzu[:, up]).all() and (dzu[:, ~down] == 0).all(), act
