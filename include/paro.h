@@ -452,7 +452,8 @@ int paro_w4_gated(const paro_rotation* r, const uint16_t* x, const uint8_t* qwei
  *   forward calls, at most 2^21 weight rows; M == 0 is a no-op.
  *   workspace: at least the ..._workspace_size bytes (beyond 128 tokens W_hat
  *         transposed in fp16, 2 d (2) N bytes, is the largest part; not
- *         always less for fewer tokens), 256-byte aligned,
+ *         always less for fewer tokens; 0 for sizes that the call refuses or
+ *         has nothing to do for), 256-byte aligned,
  *         zero-filled once after allocation (its first 16 KiB hold arrival
  *         counters, which every call leaves zero).
  * Arithmetic: fp32 sums and epilogues. dZ is rounded to fp16, which is what

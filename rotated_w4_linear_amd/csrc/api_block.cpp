@@ -130,7 +130,10 @@ int run_backward(const char* fn, bool gated, const uint16_t* x, const uint8_t* q
 }
 
 size_t backward_size(bool gated, int64_t M, int64_t N, int64_t d, int32_t act) {
-  if (M <= 0 || N <= 0 || d <= 0 || N > (int64_t(1) << 21) || d > (int64_t(1) << 22)) return 0;
+  // (sizes that the call refuses: 0; the plans below count whole tiles of both)
+  if (M <= 0 || N <= 0 || d <= 0 || M > (int64_t(1) << 30) || N > (int64_t(1) << 21) || d > (int64_t(1) << 22) ||
+      N % 16 || d % 128)
+    return 0;
   const int64_t P = gated ? 2 * N : N;
   return product_scratch(gated || act != PARO_ACT_NONE, M, P, d) + input_grad_scratch_bytes(M, P, d);
 }
