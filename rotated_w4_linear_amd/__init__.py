@@ -12,9 +12,14 @@ Names follow the C ABI: ``paro_device_init``, ``paro_rotation_create`` / ``Rotat
 ``paro_layer_loss_workspace_size``, ``paro_w4_linear_act``, ``paro_w4_gated``, their
 ``..._backward``, ``paro_adamw_create`` / ``AdamW``, ``paro_pairs_random``, ``paro_pairs_by_gap``,
 ``paro_sparsify_angles``.
+
+``stream``: calls that take one run on it (on the current stream without). What
+they allocate then belongs to that stream. The caller orders it behind the work
+that makes the inputs, and keeps the inputs until it has passed.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -146,6 +151,31 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _made_on(stream):
+    """Context of a call's allocations. They are filled, used and, once freed, used
+    again in the order of the stream that they are made on: the call's own."""
+    if stream is None:
+        return _HERE
+    import torch
+    return torch.cuda.stream(stream)
+
+
+def _handed_out(stream, *tensors):
+    """Tensors that a call on ``stream`` made and returns: the caller may use them on
+    the current stream as well, so they are not used again before it has passed."""
+    if stream is None:
+        return
+    import torch
+    current = torch.cuda.current_stream()
+    if current != stream:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(current)
+
+
 def _dptr(t, name, dtype=None):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -203,7 +233,9 @@ def paro_rotate(r: Rotation, x, y=None, stream=None):
     """X' = X T^-1 row by row (fp16 [M][d] -> fp16 [M][d]); ``y`` may be ``x``."""
     import torch
     if y is None:
-        y = torch.empty_like(x)
+        with _made_on(stream):
+            y = torch.empty_like(x)
+        _handed_out(stream, y)
     _check(load_library().paro_rotate(r.handle, _dptr(x, "x", torch.float16),
                                       _dptr(y, "y", torch.float16), int(x.shape[0]),
                                       _stream(stream)))
@@ -214,9 +246,11 @@ def paro_quantize_weights(r: Optional[Rotation], w, group: int = 128, stream=Non
     """Q(T W) (or Q(W) when ``r`` is None): returns (qweight u8 [N][d/2], scales fp16, zeros u8)."""
     import torch
     N, d = w.shape
-    qweight = torch.empty((N, d // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((N, d // group), dtype=torch.float16, device=w.device)
-    zeros = torch.empty((N, d // group), dtype=torch.uint8, device=w.device)
+    with _made_on(stream):
+        qweight = torch.empty((N, d // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((N, d // group), dtype=torch.float16, device=w.device)
+        zeros = torch.empty((N, d // group), dtype=torch.uint8, device=w.device)
+    _handed_out(stream, qweight, scales, zeros)
     _check(load_library().paro_quantize_weights(
         _handle(r), _dptr(w, "w", torch.float16), N, d, group, _dptr(qweight, "qweight"),
         _dptr(scales, "scales"), _dptr(zeros, "zeros"), _stream(stream)))
@@ -240,10 +274,14 @@ def paro_w4_linear(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, 
     import torch
     M, d = x.shape
     N = qweight.shape[0]
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
-    if workspace is None:
-        workspace = new_workspace(r, M, N, d, x.device)
+    made = []
+    with _made_on(stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+            made.append(y)
+        if workspace is None:
+            workspace = new_workspace(r, M, N, d, x.device)
+    _handed_out(stream, *made)
     ws_ptr = _dptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load_library().paro_w4_linear(
@@ -283,13 +321,17 @@ def paro_rotation_backward(r: Rotation, x, gy, side: str = "activation", gx=None
     import torch
     M, d = x.shape
     info_K = r.K
-    if gx is None and want_gx:
-        gx = torch.empty((M, d), dtype=torch.float32, device=x.device)
-    dtheta = torch.empty((info_K, d // 2), dtype=torch.float32, device=x.device)
-    dalpha = torch.empty((d,), dtype=torch.float32, device=x.device)
-    if workspace is None:
-        need = paro_rotation_backward_workspace_size(r, M)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    made = []
+    with _made_on(stream):
+        if gx is None and want_gx:
+            gx = torch.empty((M, d), dtype=torch.float32, device=x.device)
+            made.append(gx)
+        dtheta = torch.empty((info_K, d // 2), dtype=torch.float32, device=x.device)
+        dalpha = torch.empty((d,), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            need = paro_rotation_backward_workspace_size(r, M)
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _handed_out(stream, dtheta, dalpha, *made)
     ws_ptr = _dptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load_library().paro_rotation_backward(
@@ -308,12 +350,14 @@ def paro_layer_loss(r: Rotation, x, w, qweight, scales, zeros, gradients: bool =
     M, d = x.shape
     N = w.shape[0]
     dev_ = x.device
-    loss = torch.empty((1,), dtype=torch.float32, device=dev_)
-    dth = torch.empty((r.K, d // 2), dtype=torch.float32, device=dev_) if gradients else None
-    dal = torch.empty((d,), dtype=torch.float32, device=dev_) if gradients else None
-    if workspace is None:
-        need = int(load_library().paro_layer_loss_workspace_size(r.handle, M, N, d, int(gradients)))
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev_) if need else None
+    with _made_on(stream):
+        loss = torch.empty((1,), dtype=torch.float32, device=dev_)
+        dth = torch.empty((r.K, d // 2), dtype=torch.float32, device=dev_) if gradients else None
+        dal = torch.empty((d,), dtype=torch.float32, device=dev_) if gradients else None
+        if workspace is None:
+            need = int(load_library().paro_layer_loss_workspace_size(r.handle, M, N, d, int(gradients)))
+            workspace = torch.zeros(need, dtype=torch.uint8, device=dev_) if need else None
+    _handed_out(stream, loss, dth, dal)
     ws_ptr = _dptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load_library().paro_layer_loss(
@@ -375,13 +419,17 @@ def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=No
     M, d = x.shape
     N = qweight.shape[0]
     need = 0 if workspace is not None else paro_w4_linear_workspace_size(r, M, N, d)
-    workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
-    if y is None:
-        y = x.new_empty((M, N))  # fp16 on dev as x has to be
-        y_ptr = y.data_ptr()
-    else:
+    given = y is not None
+    with _made_on(stream):
+        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+        if not given:
+            y = x.new_empty((M, N))  # fp16 on dev as x has to be
+    if given:
         y_ptr = _expect(y, "y", (M, N), f16, dev)
+    else:
+        y_ptr = y.data_ptr()
+        _handed_out(stream, y)
     _check(load_library().paro_w4_linear_act(
         _handle(r), _expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (N, d // 2), u8, dev),
         _expect(scales, "scales", (N, d // group), f16, dev), _expect(zeros, "zeros", (N, d // group), u8, dev),
@@ -407,13 +455,17 @@ def paro_w4_gated(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, a
     M, d = x.shape
     N = qweight.shape[0] // 2
     need = 0 if workspace is not None else paro_w4_gated_workspace_size(r, M, N, d)
-    workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
-    if y is None:
-        y = x.new_empty((M, N))  # fp16 on dev as x has to be
-        y_ptr = y.data_ptr()
-    else:
+    given = y is not None
+    with _made_on(stream):
+        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+        if not given:
+            y = x.new_empty((M, N))  # fp16 on dev as x has to be
+    if given:
         y_ptr = _expect(y, "y", (M, N), f16, dev)
+    else:
+        y_ptr = y.data_ptr()
+        _handed_out(stream, y)
     _check(load_library().paro_w4_gated(
         _handle(r), _expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (2 * N, d // 2), u8, dev),
         _expect(scales, "scales", (2 * N, d // group), f16, dev),
@@ -438,11 +490,16 @@ def _backward(fn, new_workspace_, rows, cols, computes, x, qweight, scales, zero
     import torch
     M, N = dy.shape
     d = 2 * qweight.shape[1]
-    if dz is None and computes:
-        dz = torch.empty((M, cols), dtype=torch.float16, device=dy.device)
-    if dx is None and want_dx:
-        dx = torch.empty((M, d), dtype=torch.float16, device=dy.device)
-    workspace, ws_ptr, ws_bytes = _workspace(new_workspace_() if workspace is None else workspace, 0, dy.device)
+    made = []
+    with _made_on(stream):
+        if dz is None and computes:
+            dz = torch.empty((M, cols), dtype=torch.float16, device=dy.device)
+            made.append(dz)
+        if dx is None and want_dx:
+            dx = torch.empty((M, d), dtype=torch.float16, device=dy.device)
+            made.append(dx)
+        workspace, ws_ptr, ws_bytes = _workspace(new_workspace_() if workspace is None else workspace, 0, dy.device)
+    _handed_out(stream, *made)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     _check(fn(_expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (rows, d // 2), u8, dev),
               _expect(scales, "scales", (rows, d // group), f16, dev),

@@ -50,3 +50,114 @@ for M in (1 << 40, (1 << 63) - 1):
     assert res.returncode == 0, f"{res.returncode}: {res.stderr[-2000:]}"
     f = paro.load_library().paro_w4_linear_act_backward
     assert f(D, D, D, D, None, 1, D, D, D, 4, 64, 64, 64, None, 0, None) == -2
+
+
+# ---------------------------------------------------------------------------
+# calls on another stream: where their memory is made
+# ---------------------------------------------------------------------------
+
+class FakeTensor:
+    """A device tensor as far as the wrappers look at one; notes the stream it was made on."""
+    made = []
+    now = "current"
+
+    def __init__(self, shape, stream=None):
+        self.shape, self.is_cuda, self.device, self.recorded = tuple(shape), True, "cuda", []
+        self.stream = stream or FakeTensor.now
+        if stream is None:
+            FakeTensor.made.append(self)
+
+    def new_empty(self, shape):
+        return FakeTensor(shape)
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+    def data_ptr(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 30
+
+    def element_size(self):
+        return 1
+
+    def get_device(self):
+        return 0
+
+
+class FakeStream:
+    pass
+
+
+@pytest.fixture
+def faked(paro, monkeypatch):
+    """The wrappers without a GPU: allocations are noted, and no library call does anything."""
+    import contextlib
+    import torch
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 4096 if name.endswith("size") else 0
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, FakeTensor.now = FakeTensor.now, stream
+        yield
+        FakeTensor.now = before
+
+    FakeTensor.made, FakeTensor.now = [], "current"
+    make = lambda shape, *a, **k: FakeTensor((shape,) if isinstance(shape, int) else shape)  # noqa: E731
+    monkeypatch.setattr(paro, "load_library", Lib)
+    monkeypatch.setattr(paro, "_dptr", lambda *a: 0)
+    monkeypatch.setattr(paro, "_expect", lambda *a: 0)
+    monkeypatch.setattr(paro, "_stream", lambda *a: 0)
+    monkeypatch.setattr(paro, "_raw_stream", lambda *a: 0)
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, make)
+    monkeypatch.setattr(torch, "empty_like", lambda t: FakeTensor(t.shape))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return paro
+
+
+class FakePlan:
+    handle, K, group = None, 8, 128
+
+
+def fake(*shape):
+    return FakeTensor(shape, "current")
+
+
+CALLS = {
+    "rotate": lambda p, **k: p.paro_rotate(FakePlan, fake(4, 256), **k),
+    "quantize": lambda p, **k: p.paro_quantize_weights(None, fake(64, 256), **k),
+    "linear": lambda p, **k: p.paro_w4_linear(None, fake(4, 256), fake(64, 128), fake(64, 2), fake(64, 2), **k),
+    "rotation_backward": lambda p, **k: p.paro_rotation_backward(FakePlan, fake(4, 256), fake(4, 256), **k),
+    "layer_loss": lambda p, **k: p.paro_layer_loss(FakePlan, fake(4, 256), fake(64, 256), fake(64, 128), fake(64, 2),
+                                                   fake(64, 2), **k),
+    "linear_act": lambda p, **k: p.paro_w4_linear_act(None, fake(4, 256), fake(64, 128), fake(64, 2), fake(64, 2), **k),
+    "gated": lambda p, **k: p.paro_w4_gated(None, fake(4, 256), fake(64, 128), fake(64, 2), fake(64, 2), **k),
+    "linear_act_backward": lambda p, **k: p.paro_w4_linear_act_backward(
+        fake(4, 256), fake(64, 128), fake(64, 2), fake(64, 2), fake(4, 64), act="silu", **k),
+    "gated_backward": lambda p, **k: p.paro_w4_gated_backward(
+        fake(4, 256), fake(64, 128), fake(64, 2), fake(64, 2), fake(4, 32), **k),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_memory_belongs_to_the_calls_stream(faked, name):
+    """Zero-filled counters, scratch and outputs are made on the stream that the kernels run on."""
+    s = FakeStream()
+    out = CALLS[name](faked, stream=s)
+    assert FakeTensor.made and all(t.stream is s for t in FakeTensor.made)
+    # what is handed out may be used on the current stream as well
+    for t in out if isinstance(out, tuple) else (out,):
+        assert t is None or t.recorded == ["current"]
+    FakeTensor.made.clear()
+    CALLS[name](faked)
+    assert FakeTensor.made and all(t.stream == "current" and not t.recorded for t in FakeTensor.made)

@@ -150,3 +150,59 @@ def test_infinite_preactivations(paro, M, d, N, K):
             _, dz = paro.paro_w4_gated_backward(x, *c.dev, dy, bias=dev(bias), act=act, want_dx=False)
             dzu = host(dz)[:, N:]
             assert np.isposinf(dzu[:, up]).all() and (dzu[:, ~down] == 0).all(), act
+
+
+# ---------------------------------------------------------------------------
+# calls on another stream than the current one
+# ---------------------------------------------------------------------------
+
+def spoil(nbytes):
+    """Memory of this size on the current stream, full of ones, and freed again."""
+    torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("M", [4, 100, 300, 1100])
+def test_calls_on_another_stream(paro, M):
+    """stream= without a workspace or outputs, while the current stream is busy and hands out memory."""
+    d, N = 4096, 1024
+    log(f"another stream M={M}")
+    x, layer, b = synthetic.linear_case(seed=M, M=M, d=d, N=2 * N, group=128, K=8)
+    r = paro.Rotation(layer.pairs, layer.theta, layer.alpha, 128)
+    wq = paro.paro_quantize_weights(r, dev(layer.w), 128)
+    xd, bd = dev(x), dev(b)
+    dy, dy2 = (torch.randn((M, n), device="cuda").half() for n in (N, 2 * N))
+    gy = torch.randn((M, d), device="cuda")
+    wd = dev(layer.w)
+
+    def calls(**k):
+        yield "rotate", lambda: [paro.paro_rotate(r, xd, **k)]
+        yield "quantize", lambda: paro.paro_quantize_weights(r, wd, 128, **k)
+        yield "linear", lambda: [paro.paro_w4_linear(r, xd, *wq, bias=bd, **k)]
+        yield "linear_act", lambda: [paro.paro_w4_linear_act(r, xd, *wq, bias=bd, act="gelu", **k)]
+        yield "gated", lambda: [paro.paro_w4_gated(r, xd, *wq, bias=bd, **k)]
+        yield "linear_act without a plan", lambda: [paro.paro_w4_linear_act(None, xd, *wq, act="silu", **k)]
+        yield "linear_act_backward", lambda: paro.paro_w4_linear_act_backward(xd, *wq, dy2, bias=bd, act="silu", **k)
+        yield "gated_backward", lambda: paro.paro_w4_gated_backward(xd, *wq, dy, bias=bd, **k)
+        yield "rotation_backward", lambda: paro.paro_rotation_backward(r, xd, gy, **k)
+        yield "layer_loss", lambda: paro.paro_layer_loss(r, xd, wd, *wq, **k)
+
+    want = {}
+    for name, call in calls():
+        want[name] = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for name, call in calls(stream=s):
+        log(f"  {name}")
+        for n in (1 << 16, 1 << 22, 1 << 26):
+            spoil(n)
+        for _ in range(20):   # (some work that is still running when the call is made)
+            gy @ gy.T
+        out = call()
+        for n in (1 << 16, 1 << 22, 1 << 26):
+            spoil(n)          # not into what the call still uses
+        s.synchronize()
+        for a, w in zip(out, want[name]):
+            assert torch.equal(a, w), name
+        del out, a
+        spoil(1 << 22)
+    torch.cuda.synchronize()
