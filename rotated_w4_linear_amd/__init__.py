@@ -546,8 +546,8 @@ class AdamW:
     ``params`` and ``grads``: contiguous device tensors, one type each (fp32,
     fp16 or bf16), stepped in place and read where they are; ``m``, ``v`` (and
     for 8-bit moments ``m_scale``, ``v_scale``): the moments, zero-filled ones
-    are made when they are not given: fp32, or with ``state_bits=8`` e4m3 with
-    fp32 scales (``v`` then holds sqrt(v)).
+    are made (and waited for) when they are not given: fp32, or with
+    ``state_bits=8`` e4m3 with fp32 scales (``v`` then holds sqrt(v)).
     """
 
     def __init__(self, params, grads, m=None, v=None, m_scale=None, v_scale=None, state_bits: int = 32):
@@ -565,8 +565,15 @@ class AdamW:
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
         state = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
-        new = lambda n, t: torch.zeros(n, dtype=torch.uint8 if t != torch.float32 else t,  # noqa: E731
-                                       device=params[0].device).view(t)
+        self._made = []
+
+        def new(n, t):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("moments made inside a capture would be zero-filled by every replay: pass them")
+            made = torch.zeros(n, dtype=torch.uint8 if t != torch.float32 else t, device=params[0].device).view(t)
+            self._made.append(made)
+            return made
+
         self.m = new(total, state) if m is None else m
         self.v = new(total, state) if v is None else v
         self.m_scale, self.v_scale = m_scale, v_scale
@@ -588,6 +595,9 @@ class AdamW:
             _expect(self.m, "m", (total,), state, dev), _expect(self.v, "v", (total,), state, dev), *scales,
             ctypes.byref(h)))
         self._h = h
+        self._made_on = torch.cuda.current_stream()
+        if self._made:  # zero before the first step, whatever stream that runs on
+            self._made_on.synchronize()
 
     def step(self, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
              stream=None):
@@ -595,8 +605,11 @@ class AdamW:
         import torch
         if self._device != torch.cuda.current_device():
             raise ValueError("the tensors must be on the current device")
-        _check(load_library().paro_adamw_step(self._h, step, lr, betas[0], betas[1], eps, weight_decay,
-                                              _raw_stream(stream, self._device)))
+        at = _raw_stream(stream, self._device)
+        _check(load_library().paro_adamw_step(self._h, step, lr, betas[0], betas[1], eps, weight_decay, at))
+        if at != self._made_on.cuda_stream:  # the moments made here stay until the step has passed
+            for t in self._made:
+                t.record_stream(stream if stream is not None else torch.cuda.current_stream())
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:

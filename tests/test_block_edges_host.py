@@ -161,3 +161,41 @@ def test_memory_belongs_to_the_calls_stream(faked, name):
     FakeTensor.made.clear()
     CALLS[name](faked)
     assert FakeTensor.made and all(t.stream == "current" and not t.recorded for t in FakeTensor.made)
+
+
+def test_adamw_moments_are_zero_before_any_step(faked, monkeypatch):
+    """Moments made for a plan are waited for, since its steps may run on any stream; not inside a capture."""
+    import torch
+    log = []
+
+    class Current:
+        cuda_stream = 5
+
+        def synchronize(self):
+            log.append(("wait", len(FakeTensor.made)))
+
+    current, capturing = Current(), [False]
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(faked, "_raw_stream", lambda s, d: s.cuda_stream if s else 5)
+    monkeypatch.setattr(FakeTensor, "view", lambda self, t: self, raising=False)
+    monkeypatch.setattr(FakeTensor, "dtype", torch.float32, raising=False)
+    p, g = [fake(8)], [fake(8)]
+    opt = faked.AdamW(p, g, state_bits=8)
+    assert log == [("wait", 4)]
+    other = FakeStream()
+    other.cuda_stream = 6
+    opt.step(1)
+    assert not any(t.recorded for t in FakeTensor.made)
+    opt.step(2, stream=other)
+    assert all(t.recorded == [other] for t in FakeTensor.made)
+    # moments of the caller's: their order is the caller's
+    m, v = fake(256), fake(256)
+    monkeypatch.setattr(FakeTensor, "element_size", lambda self: 4)
+    opt = faked.AdamW(p, g, m, v)
+    opt.step(1, stream=other)
+    assert len(log) == 1 and not m.recorded
+    capturing[0] = True
+    with pytest.raises(ValueError, match="capture"):
+        faked.AdamW(p, g)
+    faked.AdamW(p, g, m, v)

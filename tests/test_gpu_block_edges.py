@@ -206,3 +206,34 @@ def test_calls_on_another_stream(paro, M):
         del out, a
         spoil(1 << 22)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_made_and_stepped_on_two_streams(paro, bits):
+    """A plan made while the current stream is busy, stepped on another one at once, and dropped."""
+    log(f"adamw on two streams {bits}")
+    n = [100_000] * 3
+    rng = np.random.default_rng(bits)
+    p0 = [dev(rng.standard_normal(k).astype(np.float32)) for k in n]
+    g = [dev(rng.standard_normal(k).astype(np.float32)) for k in n]
+    want = [t.clone() for t in p0]
+    paro.AdamW(want, g, state_bits=bits).step(1)
+    a = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        p = [t.clone() for t in p0]
+        torch.cuda.synchronize()
+        for k in (1 << 18, 1 << 20, 1 << 21):
+            spoil(k)
+        for _ in range(10):
+            a @ a
+        opt = paro.AdamW(p, g, state_bits=bits)
+        opt.step(1, stream=s)
+        del opt
+        for k in (1 << 18, 1 << 20, 1 << 21):
+            spoil(k)
+        s.synchronize()
+        for x, w in zip(p, want):
+            assert torch.equal(x, w)
+    torch.cuda.synchronize()
