@@ -70,46 +70,25 @@ __device__ __forceinline__ uint32_t half_bits(float f) {
 }
 
 // Meeting of the `pieces` workgroups that share a tile's contraction, on one
-// counter that is zero between calls. Each takes a ticket when its sums are
-// ready; all but the last to do so store their partial tile and report it, and
-// the last waits for the reports of the others. These have all taken their
-// tickets, so they are running and wait for nobody: the wait ends. (Bounded all
-// the same, to seconds: on counters that were not zero, or shared by two calls
-// at once, the sums are wrong, but the kernel ends.) Low half: tickets, high
-// half: reports. sys: the workgroups may sit on different XCDs.
-constexpr int kMeetSpins = 1 << 22;
-__device__ __forceinline__ uint32_t meet_add(uint32_t* cnt, uint32_t v, int sys) {
-  return sys ? __hip_atomic_fetch_add(cnt, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM)
-             : __hip_atomic_fetch_add(cnt, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// whether this workgroup is the last (every thread; slot: a word of LDS)
-__device__ __forceinline__ bool meet_last(uint32_t* cnt, int pieces, int sys, volatile uint32_t* slot) {
-  __syncthreads();
-  if (threadIdx.x == 0) *slot = (meet_add(cnt, 1u, sys) & 0xffffu) == (uint32_t)(pieces - 1);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane((int)*slot) != 0;
-}
-// not the last, after its stores
-__device__ __forceinline__ void meet_report(uint32_t* cnt, int sys) {
+// counter that is zero between calls: each stores its partial tile, then counts
+// itself in here, and the last one to do so (true, in every thread) finds all
+// of them stored and adds them. Nobody waits for another workgroup. sys: the
+// workgroups may sit on different XCDs; slot: a word of LDS.
+__device__ __forceinline__ bool arrive_last(uint32_t* cnt, int pieces, int sys, volatile uint32_t* slot) {
   __builtin_amdgcn_s_waitcnt(0);  // this wavefront's stores have reached L2 / memory
   __syncthreads();
-  if (threadIdx.x == 0) meet_add(cnt, 0x10000u, sys);
-}
-// the last, before it reads the others' partial tiles; leaves the counter zero
-__device__ __forceinline__ void meet_wait(uint32_t* cnt, int pieces, int sys) {
   if (threadIdx.x == 0) {
-    const uint32_t all = (uint32_t)(pieces - 1);
-    if (sys) {
-      for (int i = 0; i < kMeetSpins && __hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) >> 16 != all; ++i)
-        __builtin_amdgcn_s_sleep(1);
-      __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-    } else {
-      for (int i = 0; i < kMeetSpins && __hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >> 16 != all; ++i)
-        __builtin_amdgcn_s_sleep(1);
-      __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before = sys ? __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM)
+                                : __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = before == (uint32_t)(pieces - 1);
+    if (last) {  // (all have counted themselves in)
+      if (sys) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      else __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    *slot = last;
   }
   __syncthreads();
+  return __builtin_amdgcn_readfirstlane((int)*slot) != 0;
 }
 
 }  // namespace w4

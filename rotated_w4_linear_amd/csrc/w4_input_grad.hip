@@ -273,30 +273,21 @@ void input_grad_kernel(const uint16_t* __restrict__ wt, const uint16_t* __restri
       return __builtin_amdgcn_make_buffer_rsrc((void*)(part + ((size_t)tile * ksplit + k2) * (size_t)(IG_N * BM)),
                                                (short)0, IG_N * BM * 4, kRsrcWord3);
     };
-    // (the stages take all of LDS; the epilogue uses A0)
-    // With two pieces the last keeps its own sums in registers (1024 x 4096 ->
-    // 4096: 127 -> 119 us with the product before it); the 256 x 256 tile's 256
-    // accumulators would spill for it (1001 -> 1013 us)
-    constexpr bool kKeep = NF < 16;
-    const bool last = meet_last(&cnt[tile], ksplit, sys, (uint32_t*)B0);
-    if (!last || !kKeep || ksplit > 2) {
-      const __amdgpu_buffer_rsrc_t rmine = rsrc(ks);
+    const __amdgpu_buffer_rsrc_t rmine = rsrc(ks);
 #pragma unroll
-      for (int f = 0; f < 4 * NF; ++f) {
-        const int j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
-        const u4 v = __builtin_bit_cast(u4, f4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
-                                               acc[j][i][4 * q + 3]});
-        const int off = ((w * 4 * NF + f) * 64 + lane) * 16;
-        if (sys) __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, kAuxSys);
-        else __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, 0);
-      }
+    for (int f = 0; f < 4 * NF; ++f) {
+      const int j = f / (4 * TM), i = f / 4 % TM, q = f % 4;
+      const u4 v = __builtin_bit_cast(u4, f4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2],
+                                             acc[j][i][4 * q + 3]});
+      const int off = ((w * 4 * NF + f) * 64 + lane) * 16;
+      if (sys) __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, kAuxSys);
+      else __builtin_amdgcn_raw_buffer_store_b128(v, rmine, off, 0, 0);
     }
-    if (!last) {
-      meet_report(&cnt[tile], sys);
-      return;
-    }
-    __builtin_amdgcn_s_waitcnt(0);  // (its own partial tile, if it stored one)
-    meet_wait(&cnt[tile], ksplit, sys);
+    // (the stages take all of LDS; the epilogue uses A0)
+    if (!arrive_last(&cnt[tile], ksplit, sys, (uint32_t*)B0)) return;
+    // With two pieces the last keeps its own sums in registers and reads the
+    // other's; the 256 x 256 tile's 256 accumulators would spill for it
+    constexpr bool kKeep = NF < 16;
     auto load4 = [&](const __amdgpu_buffer_rsrc_t rk, int f) {
       const int off = ((w * 4 * NF + f) * 64 + lane) * 16;
       return __builtin_bit_cast(f4, sys ? __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, kAuxSys)

@@ -199,3 +199,14 @@ def test_adamw_moments_are_zero_before_any_step(faked, monkeypatch):
     with pytest.raises(ValueError, match="capture"):
         faked.AdamW(p, g)
     faked.AdamW(p, g, m, v)
+
+
+def test_no_workgroup_waits_for_another(paro):
+    """Workgroups that share a sum meet by counting themselves in, the last one adds: no kernel polls memory, so none
+    can stay, or go on with half a sum, whatever the counters hold."""
+    csrc = os.path.join(ROOT, "rotated_w4_linear_amd", "csrc")
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for word in ("s_sleep", "__hip_atomic_load", "__nanosleep"):
+            assert word not in text, f"{name}: {word}"
