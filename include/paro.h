@@ -206,7 +206,8 @@ size_t paro_w4_linear_workspace_size(const paro_rotation* r, int64_t M, int64_t 
  *   y        device fp16 [M][N] (must not overlap x).
  *   group    G = 64, 128 or 256; other values return PARO_ERR_UNSUPPORTED.
  *            A plan r must have the same d and group (the pairs stay inside
- *            quantization groups), else PARO_ERR_SHAPE.
+ *            quantization groups), else PARO_ERR_SHAPE, and belong to the
+ *            current device, else PARO_ERR_VALUE.
  *   N % 16 == 0, d % 128 == 0, d % G == 0, M >= 0 (M == 0 is a no-op); N <= 2^30,
  *   d <= 2^22, M < 2^30, else PARO_ERR_UNSUPPORTED.
  *   workspace, workspace_bytes: device memory of
@@ -241,8 +242,8 @@ size_t paro_w4_linear_workspace_size(const paro_rotation* r, int64_t M, int64_t 
  * (q - z) * s, in an order that depends on the sizes (and for M > 64 on
  * whether the workspace holds the stream-K partial tiles) but not on timing;
  * fp16 output.
- * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_ALIGN, PARO_ERR_UNSUPPORTED,
- * PARO_ERR_WORKSPACE, PARO_ERR_HIP.
+ * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE, PARO_ERR_ALIGN,
+ * PARO_ERR_UNSUPPORTED, PARO_ERR_WORKSPACE, PARO_ERR_HIP.
  */
 int paro_w4_linear(const paro_rotation* r, const uint16_t* x, const uint8_t* qweight,
                    const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias,

@@ -160,7 +160,13 @@ def _made_on(stream):
     if stream is None:
         return _HERE
     import torch
+    _same_device(stream, torch.cuda.current_device())
     return torch.cuda.stream(stream)
+
+
+def _same_device(stream, device):
+    if stream.device_index != device:
+        raise ValueError("stream must belong to the current device")
 
 
 def _handed_out(stream, *tensors):
@@ -394,13 +400,15 @@ def _expect(t, name, shape, dtype, device):
 def _raw_stream(stream, device):
     """Handle of ``stream``, or of the device's current stream."""
     if stream is not None:
+        _same_device(stream, device)
         return stream.cuda_stream
     import torch
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _workspace(workspace, need, device):
-    """(workspace, its address, its bytes); a zero-filled one of ``need`` bytes where none is given."""
+def _workspace(workspace, need, device, current=None):
+    """(workspace, its address, its bytes); a zero-filled one of ``need`` bytes where none is given.
+    One that is given has to be on the ``current`` device."""
     import torch
     if workspace is None:
         if not need:
@@ -408,6 +416,8 @@ def _workspace(workspace, need, device):
         workspace = torch.zeros(need, dtype=torch.uint8, device=device)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous device tensor")
+    if current is not None and workspace.get_device() != current:
+        raise ValueError("workspace must be on the current device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -422,7 +432,7 @@ def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=No
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     given = y is not None
     with _made_on(stream):
-        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device, dev)
         if not given:
             y = x.new_empty((M, N))  # fp16 on dev as x has to be
     if given:
@@ -458,7 +468,7 @@ def paro_w4_gated(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, a
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     given = y is not None
     with _made_on(stream):
-        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device)
+        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device, dev)
         if not given:
             y = x.new_empty((M, N))  # fp16 on dev as x has to be
     if given:
@@ -490,6 +500,7 @@ def _backward(fn, new_workspace_, rows, cols, computes, x, qweight, scales, zero
     import torch
     M, N = dy.shape
     d = 2 * qweight.shape[1]
+    dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     made = []
     with _made_on(stream):
         if dz is None and computes:
@@ -498,9 +509,8 @@ def _backward(fn, new_workspace_, rows, cols, computes, x, qweight, scales, zero
         if dx is None and want_dx:
             dx = torch.empty((M, d), dtype=torch.float16, device=dy.device)
             made.append(dx)
-        workspace, ws_ptr, ws_bytes = _workspace(new_workspace_() if workspace is None else workspace, 0, dy.device)
+        workspace, ws_ptr, ws_bytes = _workspace(new_workspace_() if workspace is None else workspace, 0, dy.device, dev)
     _handed_out(stream, *made)
-    dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     _check(fn(_expect(x, "x", (M, d), f16, dev), _expect(qweight, "qweight", (rows, d // 2), u8, dev),
               _expect(scales, "scales", (rows, d // group), f16, dev),
               _expect(zeros, "zeros", (rows, d // group), u8, dev), _expect(bias, "bias", (rows,), f16, dev),

@@ -289,6 +289,15 @@ int check_w4_linear(const char* fn, const paro_rotation* r, const uint16_t* x,
     set_error(f + ": x, qweight, y must be 16-byte aligned (bias 8-byte)");
     return PARO_ERR_ALIGN;
   }
+  if (r) {  // (its tables are in the memory of the device it was made on)
+    int dev = 0;
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, fn);
+    if (dev != r->device) {
+      set_error(f + ": the rotation plan belongs to another device than the current one");
+      return PARO_ERR_VALUE;
+    }
+  }
   if (M <= kDecodeMaxM && (uint64_t)((d / 128 + 3) / 4) * (uint64_t)M * (uint64_t)N * 4 >= (1ull << 31)) {
     set_error(f + ": ceil(d / 512) * M * N * 4 must be below 2^31 for M <= 64");
     return PARO_ERR_UNSUPPORTED;

@@ -90,7 +90,7 @@ class FakeTensor:
 
 
 class FakeStream:
-    pass
+    device_index = 0
 
 
 @pytest.fixture
@@ -210,3 +210,18 @@ def test_no_workgroup_waits_for_another(paro):
             text = f.read()
         for word in ("s_sleep", "__hip_atomic_load", "__nanosleep"):
             assert word not in text, f"{name}: {word}"
+
+
+def test_streams_and_workspaces_of_another_device(faked, monkeypatch):
+    """Refused before anything is allocated or launched."""
+    other = FakeStream()
+    other.device_index = 1
+    for name, call in CALLS.items():
+        with pytest.raises(ValueError, match="current device"):
+            call(faked, stream=other)
+        assert not FakeTensor.made, name
+    monkeypatch.undo()
+    with pytest.raises(ValueError, match="current device"):
+        faked._workspace(fake(1), 0, "cuda", 1)   # a tensor on device 0
+    with pytest.raises(ValueError, match="current device"):
+        faked._raw_stream(FakeStream(), 1)

@@ -1,4 +1,6 @@
 """W4 products and AdamW on the GPU where values, sizes and call forms are at an edge."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -236,4 +238,39 @@ def test_adamw_made_and_stepped_on_two_streams(paro, bits):
         s.synchronize()
         for x, w in zip(p, want):
             assert torch.equal(x, w)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# a plan of another device
+# ---------------------------------------------------------------------------
+
+class Plan(ctypes.Structure):
+    """The start of a plan as the library keeps it."""
+    _fields_ = [("d", ctypes.c_int64), ("group", ctypes.c_int32), ("K", ctypes.c_int32), ("device", ctypes.c_int32),
+                ("rest", ctypes.c_int64 * 64)]
+
+
+def test_plan_of_another_device(paro):
+    """Refused with its own error by every product, before anything is enqueued."""
+    log("plan of another device")
+    d, N = 512, 64
+    c = SmallScales(2 * N, d, 128)
+    one = [t[:N].contiguous() for t in c.dev]
+    y = torch.empty((100, N), dtype=torch.float16, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    plan = Plan(d, 128, 8, torch.cuda.current_device() + 1)
+
+    class Other:
+        handle = ctypes.cast(ctypes.pointer(plan), ctypes.c_void_p)
+
+    for M in (4, 100):
+        x = torch.zeros((M, d), dtype=torch.float16, device="cuda")
+        for call in (lambda: paro.paro_w4_linear(Other, x, *one, y=y[:M], workspace=ws),
+                     lambda: paro.paro_w4_linear_noalloc(Other, x, *one, y[:M]),
+                     lambda: paro.paro_w4_linear_act(Other, x, *one, y=y[:M], workspace=ws),
+                     lambda: paro.paro_w4_gated(Other, x, *c.dev, y=y[:M], workspace=ws)):
+            with pytest.raises(paro.ParoError, match="another device") as e:
+                call()
+            assert e.value.status == -4
     torch.cuda.synchronize()
