@@ -182,6 +182,17 @@ def _handed_out(stream, *tensors):
                 t.record_stream(current)
 
 
+def _given(t, name, shape, device, made):
+    """The fp32 output ``t``, of this shape, or a new one (noted in ``made``)."""
+    if t is None:
+        import torch
+        t = torch.empty(shape, dtype=torch.float32, device=device)
+        made.append(t)
+    elif tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t
+
+
 def _dptr(t, name, dtype=None):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -321,9 +332,11 @@ def paro_rotation_backward_workspace_size(r: Rotation, M: int) -> int:
 
 
 def paro_rotation_backward(r: Rotation, x, gy, side: str = "activation", gx=None,
-                           want_gx: bool = True, workspace=None, stream=None):
+                           want_gx: bool = True, workspace=None, stream=None, dtheta=None, dalpha=None):
     """Gradients of the transform: returns (gx fp32 [M][d] or None, dtheta fp32
-    [K][d/2], dalpha fp32 [d]) for x fp16 [M][d] and gy = dL/d(output) fp32."""
+    [K][d/2], dalpha fp32 [d]) for x fp16 [M][d] and gy = dL/d(output) fp32.
+    ``gx``, ``dtheta``, ``dalpha`` that are given are overwritten: an ``AdamW``
+    reads its gradients where they were when it was made."""
     import torch
     M, d = x.shape
     info_K = r.K
@@ -332,12 +345,12 @@ def paro_rotation_backward(r: Rotation, x, gy, side: str = "activation", gx=None
         if gx is None and want_gx:
             gx = torch.empty((M, d), dtype=torch.float32, device=x.device)
             made.append(gx)
-        dtheta = torch.empty((info_K, d // 2), dtype=torch.float32, device=x.device)
-        dalpha = torch.empty((d,), dtype=torch.float32, device=x.device)
+        dtheta = _given(dtheta, "dtheta", (info_K, d // 2), x.device, made)
+        dalpha = _given(dalpha, "dalpha", (d,), x.device, made)
         if workspace is None:
             need = paro_rotation_backward_workspace_size(r, M)
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    _handed_out(stream, dtheta, dalpha, *made)
+    _handed_out(stream, *made)
     ws_ptr = _dptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load_library().paro_rotation_backward(
@@ -349,21 +362,24 @@ def paro_rotation_backward(r: Rotation, x, gy, side: str = "activation", gx=None
 
 
 def paro_layer_loss(r: Rotation, x, w, qweight, scales, zeros, gradients: bool = True,
-                    workspace=None, stream=None):
+                    workspace=None, stream=None, loss=None, dtheta=None, dalpha=None):
     """Layer-wise output loss sum (Y_q - X W^T)^2 (fp32 device scalar) and, with
-    ``gradients``, its straight-through dtheta [K][d/2] and dalpha [d]."""
+    ``gradients``, its straight-through dtheta [K][d/2] and dalpha [d]. ``loss``
+    [1], ``dtheta``, ``dalpha`` that are given are overwritten: an ``AdamW`` reads
+    its gradients where they were when it was made."""
     import torch
     M, d = x.shape
     N = w.shape[0]
     dev_ = x.device
+    made = []
     with _made_on(stream):
-        loss = torch.empty((1,), dtype=torch.float32, device=dev_)
-        dth = torch.empty((r.K, d // 2), dtype=torch.float32, device=dev_) if gradients else None
-        dal = torch.empty((d,), dtype=torch.float32, device=dev_) if gradients else None
+        loss = _given(loss, "loss", (1,), dev_, made)
+        dth = _given(dtheta, "dtheta", (r.K, d // 2), dev_, made) if gradients else None
+        dal = _given(dalpha, "dalpha", (d,), dev_, made) if gradients else None
         if workspace is None:
             need = int(load_library().paro_layer_loss_workspace_size(r.handle, M, N, d, int(gradients)))
             workspace = torch.zeros(need, dtype=torch.uint8, device=dev_) if need else None
-    _handed_out(stream, loss, dth, dal)
+    _handed_out(stream, *made)
     ws_ptr = _dptr(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load_library().paro_layer_loss(

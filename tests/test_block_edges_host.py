@@ -225,3 +225,20 @@ def test_streams_and_workspaces_of_another_device(faked, monkeypatch):
         faked._workspace(fake(1), 0, "cuda", 1)   # a tensor on device 0
     with pytest.raises(ValueError, match="current device"):
         faked._raw_stream(FakeStream(), 1)
+
+
+def test_gradients_go_where_they_are_wanted(faked):
+    """Outputs that are given are the ones returned: a plan of AdamW steps reads its gradients at fixed places."""
+    loss, dth, dal, gx = fake(1), fake(8, 128), fake(256), fake(4, 256)
+    got = faked.paro_rotation_backward(FakePlan, fake(4, 256), fake(4, 256), gx=gx, dtheta=dth, dalpha=dal,
+                                       workspace=fake(1), stream=FakeStream())
+    assert got[0] is gx and got[1] is dth and got[2] is dal and not FakeTensor.made
+    args = [fake(*s) for s in ((4, 256), (64, 256), (64, 128), (64, 2), (64, 2))]
+    got = faked.paro_layer_loss(FakePlan, *args, loss=loss, dtheta=dth, dalpha=dal, workspace=fake(1))
+    assert got[0] is loss and got[1] is dth and got[2] is dal and not FakeTensor.made
+    with pytest.raises(ValueError, match="dtheta"):
+        faked.paro_rotation_backward(FakePlan, fake(4, 256), fake(4, 256), dtheta=fake(8, 64))
+    with pytest.raises(ValueError, match="dalpha"):
+        faked.paro_layer_loss(FakePlan, *args, dalpha=fake(128))
+    with pytest.raises(ValueError, match="loss"):
+        faked.paro_layer_loss(FakePlan, *args, loss=fake(2))

@@ -1,5 +1,6 @@
 """W4 products and AdamW on the GPU where values, sizes and call forms are at an edge."""
 import ctypes
+import gc
 
 import numpy as np
 import pytest
@@ -274,3 +275,64 @@ def test_plan_of_another_device(paro):
                 call()
             assert e.value.status == -4
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# one plan of steps over the gradients that the library makes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_learning_with_one_plan(paro, captured):
+    """Angles and scales of two layers, three steps of one AdamW plan: the gradients of each step are written where
+    the plan reads them, eager and replayed."""
+    log(f"learning with one plan captured={captured}")
+    M, G, K = 96, 128, 4
+    layers = []
+    for d, N in ((512, 256), (384, 64)):
+        x, layer, _ = synthetic.linear_case(seed=d, M=M, d=d, N=N, group=G, K=K)
+        r = paro.Rotation(layer.pairs, layer.theta, layer.alpha, G)
+        w = dev(layer.w)
+        layers.append((r, dev(x), w, paro.paro_quantize_weights(r, w, G), layer))
+    theta = [dev(la[4].theta.astype(np.float32)) for la in layers]
+    alpha = [dev(la[4].alpha.astype(np.float32)) for la in layers]
+    want = [t.clone() for t in theta + alpha]
+    dth, dal = [torch.full_like(t, 7) for t in theta], [torch.full_like(t, 7) for t in alpha]
+    loss = torch.zeros(1, device="cuda")
+    hyper = dict(lr=1e-2, weight_decay=0.0)
+    spaces = [torch.zeros(1 << 25, dtype=torch.uint8, device="cuda") for _ in layers]
+    gys = [[torch.randn((M, la[4].theta.shape[1] * 2), device="cuda") for la in layers] for _ in range(3)]
+    gy = [t.clone() for t in gys[0]]
+
+    def gradients():
+        paro.paro_layer_loss(*layers[0][:3], *layers[0][3], loss=loss, dtheta=dth[0], dalpha=dal[0],
+                             workspace=spaces[0])
+        for a, (r, x, _, _, _), b, c, s in zip(gy[1:], layers[1:], dth[1:], dal[1:], spaces[1:]):
+            paro.paro_rotation_backward(r, x, a, dtheta=b, dalpha=c, want_gx=False, workspace=s)
+
+    opt = paro.AdamW(theta + alpha, dth + dal)
+    ref = paro.AdamW(want, [torch.zeros_like(t) for t in want])
+    graph = None
+    if captured:
+        gc.collect()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gradients()
+    for step in (1, 2, 3):
+        for a, b in zip(gy, gys[step - 1]):
+            a.copy_(b)
+        if graph is not None:
+            graph.replay()
+        else:
+            gradients()
+        opt.step(step, **hyper)
+        # the same with the gradients made anew and copied
+        l0, t0, a0 = paro.paro_layer_loss(*layers[0][:3], *layers[0][3])
+        _, t1, a1 = paro.paro_rotation_backward(layers[1][0], layers[1][1], gys[step - 1][1], want_gx=False)
+        for to, g in zip(ref.grads, (t0, t1, a0, a1)):
+            to.copy_(g)
+        ref.step(step, **hyper)
+        torch.cuda.synchronize()
+        assert torch.equal(loss, l0)
+        for got, w in zip(theta + alpha, want):
+            assert torch.equal(got, w), step
