@@ -1,6 +1,9 @@
 """W4 products and AdamW on the GPU where values, sizes and call forms are at an edge."""
 import ctypes
 import gc
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,8 @@ from oracle import block
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -336,3 +341,59 @@ def test_learning_with_one_plan(paro, captured):
         assert torch.equal(loss, l0)
         for got, w in zip(theta + alpha, want):
             assert torch.equal(got, w), step
+
+
+# ---------------------------------------------------------------------------
+# a device that was never set up
+# ---------------------------------------------------------------------------
+
+CHILD = r"""
+import sys
+import torch
+sys.path.insert(0, ROOT)
+import rotated_w4_linear_amd as paro
+
+gen = torch.Generator(device="cuda").manual_seed(11)
+# products over ranges of k in one tile and across tiles; gradients in two and four pieces of 64, 128 and 256 tokens
+SHAPES = [(300, 2560, 1040, 64), (1300, 8192, 4096, 64), (2048, 8192, 2048, 128), (192, 4096, 4096, 128),
+          (256, 4096, 4096, 128), (1024, 4096, 14336, 128), (2048, 4096, 14336, 128)]
+cases = []
+for M, d, N, G in SHAPES:
+    half = lambda *s: torch.randn(s, generator=gen, device="cuda").half()
+    w = [torch.randint(0, 256, (2 * N, d // 2), generator=gen, device="cuda").to(torch.uint8),
+         (torch.rand((2 * N, d // G), generator=gen, device="cuda") * 0.01 + 0.002).half(),
+         torch.randint(0, 16, (2 * N, d // G), generator=gen, device="cuda").to(torch.uint8)]
+    cases.append((M, d, N, G, half(M, d), w, [t[:N].contiguous() for t in w], half(M, N), half(2 * N)))
+
+
+def results():
+    for M, d, N, G, x, w, one, dy, bias in cases:
+        print(f"child: M={M} d={d} N={N}", flush=True)
+        spaces = (paro.new_workspace(None, M, N, d), paro.new_gated_workspace(None, M, N, d),
+                  paro.new_linear_act_backward_workspace(M, N, d, "gelu"), paro.new_gated_backward_workspace(M, N, d))
+        y = paro.paro_w4_linear_act(None, x, *one, bias=bias[:N], residual=dy, act="silu", group=G,
+                                    workspace=spaces[0])
+        g = paro.paro_w4_gated(None, x, *w, bias=bias, group=G, workspace=spaces[1])
+        a = paro.paro_w4_linear_act_backward(x, *one, dy, bias=bias[:N], act="gelu", group=G, workspace=spaces[2])
+        b = paro.paro_w4_gated_backward(x, *w, dy, bias=bias, group=G, workspace=spaces[3])
+        torch.cuda.synchronize()
+        for s in spaces:
+            assert s is None or not s[:16384].any().item(), "arrival counters not left at zero"
+        yield y, g, *a, *b
+
+
+before = list(results())
+paro.paro_device_init()
+for i, after in enumerate(results()):
+    for p, q in zip(before[i], after):
+        assert torch.equal(p, q), SHAPES[i]
+print("child: ok", flush=True)
+"""
+
+
+def test_device_that_was_never_set_up():
+    """Without paro_device_init the pieces of a split product meet through memory: the same bits as in one XCD's L2."""
+    res = subprocess.run([sys.executable, "-c", CHILD.replace("ROOT", repr(ROOT), 1)], capture_output=True, text=True,
+                         timeout=100, cwd=ROOT)
+    print(res.stdout, flush=True)
+    assert res.returncode == 0, f"child failed ({res.returncode}):\n{res.stdout}\n{res.stderr[-4000:]}"
