@@ -51,9 +51,12 @@ __device__ __forceinline__ float sigmoid(float u) {
 // The normal distribution function Phi(z) = erfc(-z / sqrt 2) / 2 of the erf
 // gelu, and e = exp(-z^2 / 2): for x = |z| / sqrt 2, erfc(x) = exp(-x^2) t P(t)
 // with t = 1 / (1 + 0.425 x) and P a polynomial of degree 7 fitted in relative
-// terms over x in [0, 12] (error 5.4e-7 evaluated in fp32, a thousandth of an
-// fp16 rounding, also far out on the negative side where Phi is small). The
-// math library's erfc took 2.3 us more of a 333 x 2560 -> 1040 call.
+// terms. The fit is off by at most 4.5e-7 of Phi for |z| <= 8 (1.8e-6 to |z| =
+// 17); evaluated in fp32, where the rounding of exp2's argument adds about
+// 2^-24 z^2, Phi(-|z|) is off by 5.8e-7 to |z| = 1, 7.4e-7 to 3, 1.5e-6 to 5
+// and 3.0e-6 to 8: less than a hundredth of an fp16 rounding (4.9e-4) down to
+// where z Phi(z) is no fp16 number any more (z = -5.7). The math library's
+// erfc took 2.3 us more of a 333 x 2560 -> 1040 call.
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
   const float t = __builtin_amdgcn_rcpf(1.0f + 0.425f * 0.7071067811865476f * __builtin_fabsf(z));
   float p = 0.0688890740275383f;

@@ -1,6 +1,7 @@
 """W4 products and AdamW on the GPU where values, sizes and call forms are at an edge."""
 import ctypes
 import gc
+import math
 import os
 import subprocess
 import sys
@@ -397,3 +398,55 @@ def test_device_that_was_never_set_up():
                          timeout=100, cwd=ROOT)
     print(res.stdout, flush=True)
     assert res.returncode == 0, f"child failed ({res.returncode}):\n{res.stdout}\n{res.stderr[-4000:]}"
+
+
+# ---------------------------------------------------------------------------
+# activations value by value
+# ---------------------------------------------------------------------------
+
+def act_exactly(name, z):
+    """(act, act', a bound of the fp32 evaluation's error of each) in fp64.
+
+    U = 2^-24. The value is z times a factor built from products of positive terms: its relative error is that of
+    exp2's argument (2 roundings and a rounded constant: 3 U of the argument, so of 1.44 |u| or 0.72 z^2, times ln 2),
+    and at most 64 U for the two ulps of exp2 and rcp each, the polynomial (fit 8 U; eight fused steps over
+    coefficients whose magnitudes sum to 1.8 times its value) and the products. The slope is a sum of two such terms,
+    the second of which holds 1 - s, off by 2 U of 1.
+    """
+    U = 2.0 ** -24
+    if name == "gelu":
+        phi = np.array([0.5 * math.erfc(-v / math.sqrt(2)) for v in z])
+        second = z * np.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+        rel = (64 + 3 * z * z) * U
+        return z * phi, phi + second, rel * np.abs(z * phi), rel * (phi + np.abs(second))
+    if name == "relu":
+        return np.maximum(z, 0), (z > 0) * 1.0, 0 * z, 0 * z
+    a, b = (1.0, 0.0) if name == "silu" else (2 * math.sqrt(2 / math.pi), 2 * math.sqrt(2 / math.pi) * 0.044715)
+    u = z * (a + b * z * z)
+    s, rest, du = 1 / (1 + np.exp(-u)), 1 / (1 + np.exp(u)), a + 3 * b * z * z
+    second = z * s * rest * du
+    rel = (64 + 8 * np.abs(u)) * U   # (u itself: 4 roundings and two constants)
+    return z * s, s + second, rel * np.abs(z * s), rel * (s + np.abs(second)) + 2 * U * np.abs(z * s * du)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_activations_value_by_value(paro, M, name):
+    """Every fp16 number in [-6.5, 6.5] as a pre-activation (the bias; x = 0, so there is no sum to be off): value and
+    slope to fp16's own rounding, far out in the tails too."""
+    log(f"activation {name} M={M}")
+    z = np.arange(1 << 16, dtype=np.uint16).view(np.float16)
+    z = z[np.isfinite(z) & (np.abs(z.astype(np.float64)) <= 6.5)]
+    N = len(z) // 16 * 16
+    z = np.sort(z)[:N]
+    d = 128
+    w = [dev(a) for a in (np.zeros((N, d // 2), np.uint8), np.ones((N, 1), np.float16), np.zeros((N, 1), np.uint8))]
+    x = torch.zeros((M, d), dtype=torch.float16, device="cuda")
+    v, dv, ev, edv = act_exactly(name, z.astype(np.float64))
+    y = host(paro.paro_w4_linear_act(None, x, *w, bias=dev(z), act=name))
+    dy = torch.ones((M, N), dtype=torch.float16, device="cuda")
+    _, dz = paro.paro_w4_linear_act_backward(x, *w, dy, bias=dev(z), act=name, want_dx=False)
+    for got, ref, err, what in ((y, v, ev, "value"), (host(dz), dv, edv, "slope")):
+        tol = 2.0 ** -11 * (np.abs(ref) + err) + 2.0 ** -25 + err
+        off = np.abs(got.astype(np.float64) - ref) - tol
+        assert (off <= 0).all(), f"{what} at z = {z[np.argmax(off.max(0))]}: {off.max()} beyond the bound"
