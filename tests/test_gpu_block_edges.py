@@ -450,3 +450,128 @@ def test_activations_value_by_value(paro, M, name):
         tol = 2.0 ** -11 * (np.abs(ref) + err) + 2.0 ** -25 + err
         off = np.abs(got.astype(np.float64) - ref) - tol
         assert (off <= 0).all(), f"{what} at z = {z[np.argmax(off.max(0))]}: {off.max()} beyond the bound"
+
+
+# ---------------------------------------------------------------------------
+# the smallest workspace, plans under capture, the largest sizes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,d,N,G", [(65, 1024, 272, 128), (300, 2560, 1040, 64), (2048, 8192, 2048, 128),
+                                     (1300, 8192, 4096, 64)])
+def test_products_without_room_for_partial_tiles(paro, M, d, N, G):
+    """Beyond 64 tokens without a plan no workspace is needed: k is then not split across workgroups."""
+    log(f"no workspace M={M} d={d} N={N}")
+    c = SmallScales(2 * N, d, G)
+    one = [t[:N].contiguous() for t in c.dev]
+    x, cols = one_hot(M, d)
+    xd = dev(x)
+    z = 1024.0 * c.w[:, cols].T
+    ws = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert np.array_equal(host(paro.paro_w4_linear_act(None, xd, *one, act="relu", group=G, workspace=ws)),
+                          np.maximum(z[:, :N], 0))
+    assert np.array_equal(host(paro.paro_w4_gated(None, xd, *c.dev, act="none", group=G, workspace=ws)),
+                          (z[:, :N] * z[:, N:]).astype(np.float16))
+    assert (ws == 0xFF).all()
+
+
+@pytest.mark.parametrize("M", [1, 16, 24, 64, 300])
+@pytest.mark.parametrize("d,N", [(512, 64), (4096, 2064)])
+def test_plans_under_capture(paro, M, d, N):
+    """The transform inside the activated and gated products, captured and replayed between eager calls."""
+    log(f"plan under capture M={M} d={d} N={N}")
+    x, layer, b = synthetic.linear_case(seed=M + d, M=M, d=d, N=2 * N, group=128, K=8)
+    r = paro.Rotation(layer.pairs, layer.theta, layer.alpha, 128)
+    wq = paro.paro_quantize_weights(r, dev(layer.w), 128)
+    xd, bd = dev(x), dev(b)
+    spaces = paro.new_workspace(r, M, 2 * N, d), paro.new_gated_workspace(r, M, N, d)
+
+    def calls():
+        return (paro.paro_w4_linear_act(r, xd, *wq, bias=bd, act="gelu", workspace=spaces[0]),
+                paro.paro_w4_gated(r, xd, *wq, bias=bd, workspace=spaces[1]))
+
+    want = [t.clone() for t in calls()]
+    gc.collect()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls()
+    for i in range(3):
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, w in zip(outs, want):
+            assert torch.equal(a, w), f"replay {i}"
+        for a, w in zip(calls(), want):
+            assert torch.equal(a, w)
+        torch.cuda.synchronize()
+
+
+def test_largest_sizes(paro):
+    """Offsets beyond 32 bits: N d just below 2^31 in a gated block, more than 2^31 outputs, 2^21 weight rows."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def weights(rows, d):
+        return [torch.randint(0, 256, (rows, d // 2), generator=gen, device="cuda", dtype=torch.uint8),
+                torch.randint(1, 64, (rows, d // 128), generator=gen, device="cuda").half() * 2.0 ** -12,
+                torch.randint(0, 16, (rows, d // 128), generator=gen, device="cuda", dtype=torch.uint8)]
+
+    def some(w, rows):  # (q - z) s of these rows
+        return block.weights(*(host(t[rows].contiguous()) for t in w), 128)
+
+    d, N = 16256, 1 << 17
+    w = weights(2 * N, d)
+    at = torch.tensor([0, 1, N // 2 + 5, N - 16, N - 1], device="cuda")
+    gate, up = some(w, at), some(w, at + N)
+    for M in (1, 40, 200, 600):
+        log(f"gated {M} x {d} -> {N}")
+        x, cols = one_hot(M, d)
+        cols[-1], x[-1] = d - 1, 0
+        x[-1, d - 1] = 1024.0
+        y = paro.paro_w4_gated(None, dev(x), *w, act="none")
+        want = (1024.0 * gate[:, cols] * (1024.0 * up[:, cols])).T.astype(np.float16)
+        assert np.array_equal(host(y[:, at]), want)
+    del w, y
+
+    M, d, N = 70001, 128, 32768
+    log(f"linear_act {M} x {d} -> {N}")
+    w = weights(N, d)
+    x, cols = one_hot(M, d)
+    y = torch.full((M, N), 0.5, dtype=torch.float16, device="cuda")
+    paro.paro_w4_linear_act(None, dev(x), *w, residual=y, y=y)
+    at = torch.tensor([0, 1, N // 2, N - 1], device="cuda")
+    rows = np.array([0, 65535, 65536, M - 2, M - 1])
+    want = (1024.0 * some(w, at)[:, cols[rows]] + 0.5).T.astype(np.float16)
+    assert np.array_equal(host(y[torch.from_numpy(rows).cuda()][:, at]), want)
+    del w, y
+
+    P, d = 1 << 21, 128
+    w = weights(P, d)
+    for M in (3, 130):
+        log(f"input gradient {M} x {P} -> {d}")
+        dy = torch.zeros((M, P), dtype=torch.float16, device="cuda")
+        rows = torch.arange(M, device="cuda") * 15991 + 5
+        rows[-1] = P - 1
+        dy[torch.arange(M, device="cuda"), rows] = 1024.0
+        dx, _ = paro.paro_w4_linear_act_backward(None, *w, dy)
+        assert np.array_equal(host(dx), 1024.0 * some(w, rows))
+
+
+def test_adamw_of_more_than_2_31_values(paro):
+    log("adamw of 2^31 + 1003 values")
+    n, tail = (1 << 31) + 1003, 1003 + 2048
+    p = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.full((n,), 0.25, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    g[-tail:] = torch.randn(tail, generator=gen, device="cuda").bfloat16()
+    p[-tail:] = torch.randn(tail, generator=gen, device="cuda").bfloat16()
+    end, gend = p[-tail:].clone(), g[-tail:].clone()
+    one, two = paro.AdamW([p], [g], state_bits=8), paro.AdamW([end], [gend], state_bits=8)
+    for step in (1, 2):
+        one.step(step, lr=0.1)
+        two.step(step, lr=0.1)
+    torch.cuda.synchronize()
+    assert torch.equal(p[-tail:], end)
+    assert torch.equal(one.m.view(torch.uint8)[-two.m.numel():], two.m.view(torch.uint8))
+    assert torch.equal(one.v_scale[-two.v_scale.numel():], two.v_scale)
+    assert (p[:-tail] == p[0]).all()
