@@ -394,8 +394,9 @@ int paro_layer_loss(const paro_rotation* r, const uint16_t* x, const uint16_t* w
  * The W4 linear with its bias, an activation and a residual in the epilogue:
  *   Y[m][n] = act(Z[m][n]) + R[m][n],
  *   Z[m][n] = sum_k X'[m][k] W_hat[n][k] + bias[n],
- * X', W_hat, sizes, alignment and workspace (paro_w4_linear_workspace_size)
- * as for paro_w4_linear; Z, the activation and the sum in fp32, one rounding
+ * X', W_hat, sizes, alignment and workspace (paro_w4_linear_workspace_size;
+ * without a plan and with M <= 64 its first 16 KiB are enough) as for
+ * paro_w4_linear; Z, the activation and the sum in fp32, one rounding
  * to fp16. Up to a few hundred tokens the product runs in kernels of its own
  * (where the transform is not fused into it), whose fp32 sums run in another
  * order: Z may differ from paro_w4_linear's in the last places.

@@ -392,6 +392,7 @@ def paro_layer_loss(r: Rotation, x, w, qweight, scales, zeros, gradients: bool =
     return loss, dth, dal
 
 
+_COUNTERS = 16384  # bytes of the arrival counters that a workspace starts with
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 
 
@@ -440,11 +441,13 @@ def _workspace(workspace, need, device, current=None):
 def paro_w4_linear_act(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, residual=None,
                        act: str = "none", y=None, group: int = 128, workspace=None, stream=None):
     """Y = act(rot(X) dequant(W)^T + b) + residual (fp16 [M][N]); ``y`` may be ``residual``.
-    The workspace is paro_w4_linear's (``new_workspace``)."""
+    The workspace is paro_w4_linear's (``new_workspace``); without a plan 16 KiB do up to 64 tokens."""
     import torch
     M, d = x.shape
     N = qweight.shape[0]
-    need = 0 if workspace is not None else paro_w4_linear_workspace_size(r, M, N, d)
+    need = 0
+    if workspace is None:
+        need = _COUNTERS if r is None and 0 < M <= 64 else paro_w4_linear_workspace_size(r, M, N, d)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     given = y is not None
     with _made_on(stream):
@@ -480,7 +483,9 @@ def paro_w4_gated(r: Optional[Rotation], x, qweight, scales, zeros, bias=None, a
     import torch
     M, d = x.shape
     N = qweight.shape[0] // 2
-    need = 0 if workspace is not None else paro_w4_gated_workspace_size(r, M, N, d)
+    need = 0
+    if workspace is None:
+        need = _COUNTERS if r is None and 0 < M <= 64 else paro_w4_gated_workspace_size(r, M, N, d)
     dev, f16, u8 = torch.cuda.current_device(), torch.float16, torch.uint8
     given = y is not None
     with _made_on(stream):

@@ -53,7 +53,8 @@ int run_forward(const char* fn, int epi, const paro_rotation* r, const uint16_t*
   const int st = check_w4_linear(fn, r, x, qweight, scales, zeros, bias, y, M, P, d, group, &noop);
   if (st != PARO_OK || noop) return st;
   if (!aligned16(residual)) return fail(PARO_ERR_ALIGN, f + ": residual must be 16-byte aligned");
-  const size_t need = w4_linear_min_workspace(r, M, P, d);
+  // (X' given and few tokens: kernels without partial sums in memory)
+  const size_t need = !r && M <= kDecodeMaxM ? kDecodeCounterBytes : w4_linear_min_workspace(r, M, P, d);
   if (need && (!workspace || workspace_bytes < need))
     return fail(PARO_ERR_WORKSPACE, f + ": workspace missing or smaller than the minimum");
   if ((uintptr_t)workspace & 255) return fail(PARO_ERR_ALIGN, f + ": workspace must be 256-byte aligned");

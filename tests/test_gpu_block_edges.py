@@ -474,6 +474,29 @@ def test_products_without_room_for_partial_tiles(paro, M, d, N, G):
     assert (ws == 0xFF).all()
 
 
+@pytest.mark.parametrize("M,d,N,G", [(1, 4096, 4128, 128), (16, 2048, 48, 64), (40, 2560, 1040, 64),
+                                     (64, 512, 4112, 256)])
+def test_products_of_few_tokens_on_the_counters_alone(paro, M, d, N, G):
+    """Up to 64 tokens without a plan nothing of a workspace is used, and its first 16 KiB do."""
+    log(f"16 KiB workspace M={M} d={d} N={N}")
+    c = SmallScales(2 * N, d, G)
+    one = [t[:N].contiguous() for t in c.dev]
+    x, cols = one_hot(M, d)
+    xd = dev(x)
+    z = 1024.0 * c.w[:, cols].T
+    buf = torch.zeros(2 * 16384, dtype=torch.uint8, device="cuda")
+    buf[16384:] = 0xFF
+    ws = buf[:16384]
+    for _ in range(2):
+        assert np.array_equal(host(paro.paro_w4_linear_act(None, xd, *one, act="relu", group=G, workspace=ws)),
+                              np.maximum(z[:, :N], 0))
+        assert np.array_equal(host(paro.paro_w4_gated(None, xd, *c.dev, act="none", group=G, workspace=ws)),
+                              (z[:, :N] * z[:, N:]).astype(np.float16))
+    assert not ws.any() and (buf[16384:] == 0xFF).all()
+    with pytest.raises(paro.ParoError):
+        paro.paro_w4_gated(None, xd, *c.dev, group=G, workspace=ws[:16128])
+
+
 @pytest.mark.parametrize("M", [1, 16, 24, 64, 300])
 @pytest.mark.parametrize("d,N", [(512, 64), (4096, 2064)])
 def test_plans_under_capture(paro, M, d, N):
