@@ -297,7 +297,6 @@ int paro_adamw_create(int32_t count, const int64_t* n, void* const* params, int3
     std::vector<std::vector<AdamwTensor>> launches(1);
     std::unique_ptr<paro_adamw> h(new paro_adamw());
     uint32_t chunk = 0, block = 0;
-    size_t pieces = 0;
     for (int32_t i = 0; i < count; ++i) {
       for (int64_t at = 0; at < n[i];) {
         if (chunk == kMostChunks) {
@@ -315,7 +314,6 @@ int paro_adamw_create(int32_t count, const int64_t* n, void* const* params, int3
         block += (uint32_t)((t.n + 255) / 256);
         at += t.n;
         launches.back().push_back(t);
-        ++pieces;
       }
     }
     h->chunks.push_back(chunk);
