@@ -6,11 +6,14 @@
 // (dequantized and transposed through LDS, fp16, p padded with zeros to a
 // multiple of 128) and the product is then a dense one of two operands whose
 // contraction index is contiguous. W_hat^T costs 2.5 P d bytes moved whatever
-// M is: 10.3 us for 4096 x 4096 (4.1 TB/s), 57.5 for 28672 x 4096 (5.1 TB/s, what
-// a copy reaches), 14% of the product's time at 2048 tokens. The product itself
+// M is: 10.1 us for 4096 x 4096 (4.1 TB/s), 57 for 28672 x 4096 (5.2 TB/s, what
+// a copy reaches), 15% of the product's time at 2048 tokens. The product itself
 // is bound by the matrix cores under the power limit (busy 67% of the time at
-// 2048 x 28672 -> 4096, 393 us, 1224 TFLOP/s; a W4 operand dequantized on the
-// way, 1120).
+// 2048 x 28672 -> 4096; 385 us at least, 400 on average over 20 calls from a
+// cold clock, 1250 and 1200 TFLOP/s; a W4 operand dequantized on the way, 1120).
+// dZ is the matrix cores' fp16 operand, as the caller gets it: dX' is off by
+// 2.9e-4 of its norm against 64 bits, 2.1e-4 of which is its own rounding. The
+// fp32 dZ as a sum of two fp16 terms would take the product twice.
 #include <algorithm>
 #include <type_traits>
 
@@ -368,9 +371,8 @@ int64_t pad128(int64_t n) { return (n + 127) & ~int64_t(127); }
 // Tile and k split of the product: the least estimated time, in k-tiles of the
 // 256 x 256 tile, over the tile heights and splits: 6 for a round's start and
 // end, and for a split's meeting 5 and 4 per piece of 256 tokens (with the
-// transposition, 64 tokens x 4096 -> 4096 in 4 pieces 31.3 us, in 8 34.4; 1024
-// tokens in 256 tiles of 64 53, in 128 of 128 and two pieces 57; 1024 x 14336 ->
-// 4096 172 and 205).
+// transposition, 1024 tokens x 4096 -> 4096 in 256 tiles of 64 53 us, in 128 of
+// 128 and two pieces 57; 1024 x 14336 -> 4096 172 and 205).
 struct GradPlan {
   int bm = 256, ksplit = 1;
   int64_t mblk = 0, nblk = 0, tiles = 0;
