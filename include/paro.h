@@ -423,7 +423,8 @@ int paro_w4_linear_act(const paro_rotation* r, const uint16_t* x, const uint8_t*
  * shared by them.
  *   qweight [2N][d/2], scales and zeros [2N][d/group], bias [2N] or NULL,
  *   y fp16 [M][N]; N % 16 == 0 and N d < 2^31, else as paro_w4_linear with
- *   2 N rows, the workspace (paro_w4_gated_workspace_size) included.
+ *   2 N rows, the workspace (paro_w4_gated_workspace_size; without a plan and
+ *   with M <= 64 its first 16 KiB are enough) included.
  * Errors: those of paro_w4_linear, PARO_ERR_VALUE (unknown activation).
  */
 size_t paro_w4_gated_workspace_size(const paro_rotation* r, int64_t M, int64_t N, int64_t d);

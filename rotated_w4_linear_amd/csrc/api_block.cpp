@@ -95,6 +95,7 @@ int run_backward(const char* fn, bool gated, const uint16_t* x, const uint8_t* q
   if (!aligned16(dy) || !aligned16(dz) || !aligned16(dx))
     return fail(PARO_ERR_ALIGN, f + ": dy, dz and dx must be 16-byte aligned");
   const bool copy = !product && dz && dz != dy;  // dZ = dY, for a caller who gave a place for it
+  if (!product && !dx && !copy) return PARO_OK;
   const size_t first = product_scratch(product, M, P, d);
   const size_t need = first + (dx ? input_grad_scratch_bytes(M, P, d) : 0);
   if ((product || dx) && (!workspace || workspace_bytes < need))

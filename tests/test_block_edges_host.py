@@ -25,6 +25,8 @@ def test_dz_without_activation_is_checked(paro):
     assert f(None, D, D, D, None, 0, D, ODD, None, 4, 64, 256, 128, None, 0, None) == -5
     assert f(None, D, D, D, None, 0, D, D, None, 4, 64, 256, 128, None, 0, None) == 0   # dz is dy: nothing to do
     assert f(None, D, D, D, None, 0, D, D, D, 4, 64, 256, 128, None, 0, None) == -7
+    # nothing asked for: no workspace is looked at
+    assert f(None, D, D, D, None, 0, D, None, None, 4, 64, 256, 128, ODD, 0, None) == 0
 
 
 def test_backward_workspace_of_refused_sizes(paro):
