@@ -288,6 +288,9 @@ typedef enum {
   PARO_ACT_RELU = 4       /* max(z, 0) */
 } paro_activation;
 
+/* Element types of tensors that are not fp16 alone. */
+typedef enum { PARO_TYPE_F32 = 0, PARO_TYPE_F16 = 1, PARO_TYPE_BF16 = 2 } paro_type;
+
 /* Which transform paro_rotation_backward differentiates. */
 typedef enum {
   PARO_SIDE_ACTIVATION = 0, /* X' = X T^-1, as paro_rotate computes it */
@@ -477,8 +480,176 @@ int paro_w4_gated_backward(const uint16_t* x, const uint8_t* qweight, const uint
                            uint16_t* dz, uint16_t* dx, int64_t M, int64_t N, int64_t d, int32_t group,
                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* Element types of the AdamW step's tensors. */
-typedef enum { PARO_TYPE_F32 = 0, PARO_TYPE_F16 = 1, PARO_TYPE_BF16 = 2 } paro_type;
+/*
+ * Mixture of experts: every token goes through k of E experts. A routing says
+ * which: M tokens, R = M k pairs p = m k + s of a token m and its slot s. The
+ * rows of the experts' products are the pairs in expert order: first those of
+ * expert 0 in the order of their numbers, then those of expert 1, and so on; the
+ * pairs without an expert come last and have no row.
+ *   ids      device int32 [M][k]: the expert of each pair; one outside 0 .. E - 1
+ *            (-1) means none.
+ *   offsets  device int32 [E + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ *   order    device int32 [R]: the pair of each row; -1 from offsets[E] on.
+ *   place    device int32 [R]: the row of each pair; -1 without an expert.
+ *   weights  device fp32 [R]: the pairs' weights (read by the combining calls).
+ * The tables are those of paro_experts_route or paro_experts_sort: tables that
+ * contradict each other give wrong results, but no access outside the tensors.
+ */
+typedef struct paro_routing {
+  int64_t M;
+  int32_t E, k;
+  const int32_t *ids, *offsets, *order, *place;
+  const float* weights;
+} paro_routing;
+
+/*
+ * The router: for every token the k largest of its E logits l, the lower expert
+ * first where two are equal, with p = softmax(l) and
+ *   w_s = p_s / (sum of p over the k)  (normalize != 0),  else  w_s = p_s;
+ * and the tables of the routing. An expert with logit -inf or NaN is never
+ * taken: a token with fewer than k others has pairs without an expert (id -1,
+ * weight 0), and a token whose mask leaves none has no expert at all. A NaN
+ * among a token's logits makes its weights NaN. fp32 arithmetic; the logits'
+ * order is exact.
+ *   logits   device [M][E] of a paro_type, aligned to it.
+ *   ids, weights, offsets, order, place: outputs, as above (M == 0: offsets = 0).
+ *   1 <= k <= E <= 1024, k <= 16, R <= 2^30.
+ *   workspace: paro_experts_route_workspace_size(M, E, k) bytes (0 up to 64
+ *            tokens), 256-byte aligned; scratch, not shared by calls that may
+ *            run at the same time.
+ * paro_experts_sort makes the tables of given ids (a router of the caller's, or
+ * the experts e0 .. e0 + E - 1 that one device holds, from ids - e0).
+ * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE (unknown type),
+ * PARO_ERR_ALIGN, PARO_ERR_UNSUPPORTED (limits), PARO_ERR_WORKSPACE, PARO_ERR_HIP.
+ */
+size_t paro_experts_route_workspace_size(int64_t M, int32_t E, int32_t k);
+int paro_experts_route(const void* logits, int32_t type, int64_t M, int32_t E, int32_t k, int32_t normalize,
+                       int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+int paro_experts_sort(const int32_t* ids, int64_t M, int32_t E, int32_t k, int32_t* offsets, int32_t* order,
+                      int32_t* place, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient of the router at its logits, for dw = dL/dw (the choice of the experts
+ * is constant): with normalize dl_i = w_i (dw_i - sum_s w_s dw_s) for the token's
+ * experts and 0 for the others (logits may be NULL), else
+ * dl_j = p_j (dw_j [j is one of them] - sum_s p_s dw_s). Pairs without an expert
+ * take no part, and a token without experts has a gradient of 0.
+ *   ids, weights, normalize: the forward call's; dweights device fp32 [M][k];
+ *   dlogits device [M][E], of the logits' type, overwritten (may be logits).
+ * Errors: as paro_experts_route, without a workspace.
+ */
+int paro_experts_route_backward(const void* logits, int32_t type, int64_t M, int32_t E, int32_t k, int32_t normalize,
+                                const int32_t* ids, const float* weights, const float* dweights, void* dlogits,
+                                hipStream_t stream);
+
+/*
+ * The experts' products on 4-bit weights, each row by its expert's:
+ *
+ * paro_w4_experts_gated, for row r of expert e and its token m:
+ *   H[r][n] = act(Zg) Zu,  Zg = sum_k X'[m][k] W_hat[e][n][k] + bias[e][n],
+ *   Zu the same with row N + n: the weights of an expert are a block of 2 N rows
+ *   as for paro_w4_gated.
+ * paro_w4_experts_combine, over the slots s of a token with row r_s, expert e_s:
+ *   Y[m][n] = residual[m][n]
+ *             + sum_s w[m][s] (sum_k H[r_s][k] W_hat[e_s][n][k] + bias[e_s][n]).
+ *
+ *   x        device fp16 [M][d]: X', transformed activations (paro_rotate; the
+ *            experts of a layer share the transform);
+ *   h        device fp16 [R][N] (gated's output; rows from offsets[E] on are left
+ *            as they were) and [R][d] (combine's input, transformed if its
+ *            weights are);
+ *   qweight  device uint8 [E][P][d/2], scales [E][P][d/group], zeros likewise,
+ *            bias fp16 [E][P] or NULL, with P = 2 N (gated) or N (combine): what
+ *            paro_quantize_weights makes of the E [P][d] weights, one after the
+ *            other;
+ *   residual device fp16 [M][N] or NULL; may be y itself, no other overlap;
+ *   y        device fp16 [M][N]; tokens without an expert get the residual, or 0.
+ *   N % 16 == 0, d % 128 == 0, d % group == 0, P and d <= 2^21, P d < 2^31; the
+ *   tokens times their channels (gated d, combine N) < 2^30, R max(P, d) < 2^38;
+ *   tensors 16-byte aligned. M == 0 is a no-op.
+ *   workspace: at least the ..._workspace_size bytes (combine: its rows in fp32,
+ *   4 R N bytes, so that a token's sum is rounded once), 256-byte aligned;
+ *   scratch, not shared by calls that may run at the same time.
+ * Arithmetic: fp32 sums of exact fp16 products, one rounding to fp16; results do
+ * not depend on timing, nor a row's on the other rows' values.
+ * The calls read the numbers of rows on the device: they do not synchronise, and
+ * a captured call follows the routing that its replay finds.
+ * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE (unknown activation),
+ * PARO_ERR_ALIGN, PARO_ERR_UNSUPPORTED, PARO_ERR_WORKSPACE, PARO_ERR_HIP.
+ */
+size_t paro_w4_experts_gated_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d);
+int paro_w4_experts_gated(const paro_routing* routing, const uint16_t* x, const uint8_t* qweight,
+                          const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, int32_t act,
+                          uint16_t* h, int64_t N, int64_t d, int32_t group, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+size_t paro_w4_experts_combine_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d);
+int paro_w4_experts_combine(const paro_routing* routing, const uint16_t* h, const uint8_t* qweight,
+                            const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias,
+                            const uint16_t* residual, uint16_t* y, int64_t N, int64_t d, int32_t group,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Their gradients (the 4-bit weights are constants):
+ * paro_w4_experts_gated_backward, for dH = dL/dH (fp16 [R][N], by row):
+ *   dZg = dH Zu act'(Zg), dZu = dH act(Zg) (dz fp16 [R][2N], rows from offsets[E]
+ *   on left as they were), Z computed again, and
+ *   dX'[m] = sum over the token's rows r of dZ[r] W_hat[e] (dx fp16 [M][d], 0 for a
+ *   token without an expert; NULL: not computed).
+ * paro_w4_experts_combine_backward, for dY = dL/dY (fp16 [M][N]), with
+ * U[r] = dY[m] W_hat[e] (fp32):
+ *   dH[r] = w U[r] (dh fp16 [R][d], rows from offsets[E] on left as they were),
+ *   dw[m][s] = U[r] . H[r] + dY[m] . bias[e] (dweights fp32 [M][k], 0 without an
+ *   expert); the residual's gradient is dY itself.
+ * Arguments, limits and errors as for the forward calls. dX' is summed from dZ
+ * rounded to fp16, as it is returned; a bias gradient is the sum of an expert's
+ * rows of dZ, or of w dY.
+ */
+size_t paro_w4_experts_gated_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d);
+int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* x, const uint8_t* qweight,
+                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, int32_t act,
+                                   const uint16_t* dh, uint16_t* dz, uint16_t* dx, int64_t N, int64_t d,
+                                   int32_t group, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t paro_w4_experts_combine_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d);
+int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t* h, const uint8_t* qweight,
+                                     const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias,
+                                     const uint16_t* dy, uint16_t* dh, float* dweights, int64_t N, int64_t d,
+                                     int32_t group, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Distillation loss from a teacher's top logits, the objective of learning through
+ * a whole model (the layer-wise one is paro_layer_loss). Per row, with
+ * q = softmax(z / T) over the V logits of the student and the teacher's entries i
+ * (logit t_i at index j_i):
+ *   lse NULL: p_i = exp(t_i / T) / sum over the entries,  P = 0;
+ *   else:     p_i = exp(t_i / T - lse), lse the log of the sum of exp(t / T) over
+ *             all the teacher's logits, and P = max(0, 1 - sum p): the rest of its
+ *             mass, compared with the student's outside the entries, Q, as one
+ *             more class;
+ *   L = w T^2 [sum_i p_i (log p_i - log q_ji) + P (log P - log Q)],
+ *   dL/dz_j = w T (A q_j - sum of p_i with j_i = j), outside the entries with a
+ *   rest w T q_j (A - P / Q); A = sum p + P.
+ *   z        device [M][V] of a paro_type, 16-byte aligned; student logits of
+ *            -inf are classes that it cannot take.
+ *   values   device [M][K] of a paro_type (t), index device int32 [M][K] (j): an
+ *            index outside 0 .. V - 1 (-1) means no entry, a value of -inf an
+ *            entry of mass 0; an index that comes twice adds its masses.
+ *   lse, row_weight  device fp32 [M] or NULL (w = 1). A row with w = 0 is left
+ *            out whatever it holds, and so is (lse NULL) one without an entry
+ *            above -inf: loss 0, gradient 0. With a rest and no student mass
+ *            outside the entries, those logits have no gradient.
+ *   loss     device fp32 [M].
+ *   dz       device [M][V] of z's type, 16-byte aligned: grad_scale dL/dz (the
+ *            scale keeps fp16 gradients normal), or NULL; may be z itself.
+ *   M < 2^31, 1 <= V <= 2^20, 1 <= K <= 1024; T > 0.
+ * Arithmetic: exponentials and their sums over the row in fp32, the entries in
+ * fp64; results do not depend on timing. One launch, no workspace.
+ * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE, PARO_ERR_ALIGN,
+ * PARO_ERR_UNSUPPORTED, PARO_ERR_HIP.
+ */
+int paro_distill_loss(const void* z, int32_t z_type, const void* values, int32_t value_type, const int32_t* index,
+                      const float* lse, const float* row_weight, int64_t M, int64_t V, int64_t K, double temperature,
+                      double grad_scale, float* loss, void* dz, hipStream_t stream);
 
 /* Plan of an AdamW step over a fixed list of tensors. Immutable after creation. */
 typedef struct paro_adamw paro_adamw;

@@ -10,8 +10,10 @@ Names follow the C ABI: ``paro_device_init``, ``paro_rotation_create`` / ``Rotat
 ``paro_w4_linear_workspace_size``, ``paro_w4_linear_noalloc``, ``paro_rotation_backward``,
 ``paro_rotation_backward_workspace_size``, ``paro_layer_loss``,
 ``paro_layer_loss_workspace_size``, ``paro_w4_linear_act``, ``paro_w4_gated``, their
-``..._backward``, ``paro_adamw_create`` / ``AdamW``, ``paro_pairs_random``, ``paro_pairs_by_gap``,
-``paro_sparsify_angles``.
+``..._backward``, ``paro_experts_route`` / ``paro_experts_sort`` / ``Routing``,
+``paro_w4_experts_gated``, ``paro_w4_experts_combine``, their ``..._backward``,
+``paro_distill_loss``, ``paro_adamw_create`` / ``AdamW``, ``paro_pairs_random``,
+``paro_pairs_by_gap``, ``paro_sparsify_angles``.
 
 ``stream``: calls that take one run on it (on the current stream without). What
 they allocate then belongs to that stream. The caller orders it behind the work
@@ -43,6 +45,12 @@ class ParoError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
         self.status = status
+
+
+class _Routing(ctypes.Structure):
+    """``paro_routing``"""
+    _fields_ = [("M", ctypes.c_int64), ("E", ctypes.c_int32), ("k", ctypes.c_int32)] + [
+        (name, ctypes.c_void_p) for name in ("ids", "offsets", "order", "place", "weights")]
 
 
 def load_library() -> ctypes.CDLL:
@@ -103,6 +111,31 @@ def load_library() -> ctypes.CDLL:
     for fn in (lib.paro_w4_linear_act_backward, lib.paro_w4_gated_backward):
         fn.restype = ctypes.c_int
         fn.argtypes = [vp, vp, vp, vp, vp, c_i32, vp, vp, vp, c_i64, c_i64, c_i64, c_i32, vp, c_size, vp]
+    rt = ctypes.POINTER(_Routing)
+    lib.paro_experts_route_workspace_size.restype = c_size
+    lib.paro_experts_route_workspace_size.argtypes = [c_i64, c_i32, c_i32]
+    lib.paro_experts_route.restype = ctypes.c_int
+    lib.paro_experts_route.argtypes = [vp, c_i32, c_i64, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp, vp, c_size, vp]
+    lib.paro_experts_sort.restype = ctypes.c_int
+    lib.paro_experts_sort.argtypes = [vp, c_i64, c_i32, c_i32, vp, vp, vp, vp, c_size, vp]
+    lib.paro_experts_route_backward.restype = ctypes.c_int
+    lib.paro_experts_route_backward.argtypes = [vp, c_i32, c_i64, c_i32, c_i32, c_i32, vp, vp, vp, vp, vp]
+    for name in ("gated", "combine", "gated_backward", "combine_backward"):
+        size = getattr(lib, f"paro_w4_experts_{name}_workspace_size")
+        size.restype = c_size
+        size.argtypes = [c_i64, c_i32, c_i32, c_i64, c_i64]
+    lib.paro_w4_experts_gated.restype = ctypes.c_int
+    lib.paro_w4_experts_gated.argtypes = [rt, vp, vp, vp, vp, vp, c_i32, vp, c_i64, c_i64, c_i32, vp, c_size, vp]
+    lib.paro_w4_experts_combine.restype = ctypes.c_int
+    lib.paro_w4_experts_combine.argtypes = [rt, vp, vp, vp, vp, vp, vp, vp, c_i64, c_i64, c_i32, vp, c_size, vp]
+    lib.paro_w4_experts_gated_backward.restype = ctypes.c_int
+    lib.paro_w4_experts_gated_backward.argtypes = [rt, vp, vp, vp, vp, vp, c_i32, vp, vp, vp, c_i64, c_i64, c_i32, vp,
+                                                   c_size, vp]
+    lib.paro_w4_experts_combine_backward.restype = ctypes.c_int
+    lib.paro_w4_experts_combine_backward.argtypes = [rt, vp, vp, vp, vp, vp, vp, vp, vp, c_i64, c_i64, c_i32, vp,
+                                                     c_size, vp]
+    lib.paro_distill_loss.restype = ctypes.c_int
+    lib.paro_distill_loss.argtypes = [vp, c_i32, vp, c_i32, vp, vp, vp, c_i64, c_i64, c_i64, c_f64, c_f64, vp, vp, vp]
     lib.paro_adamw_moments.restype = c_i64
     lib.paro_adamw_moments.argtypes = [c_i32, vp]
     lib.paro_adamw_create.restype = ctypes.c_int
@@ -560,6 +593,286 @@ def paro_w4_gated_backward(x, qweight, scales, zeros, dy, bias=None, act: str = 
     return _backward(load_library().paro_w4_gated_backward,
                      lambda: new_gated_backward_workspace(M, N, 2 * qweight.shape[1], dy.device), 2 * N, 2 * N,
                      True, x, qweight, scales, zeros, dy, bias, act, dz, dx, want_dx, group, workspace, stream)
+
+
+def _types():
+    import torch
+    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _type(t, name) -> int:
+    """paro_type of a tensor."""
+    types = _types()
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
+    return types[t.dtype]
+
+
+class Routing:
+    """Which experts every token goes to, and the tables that the experts' products read
+    (``paro_routing``): ``ids`` int32 and ``weights`` fp32 [M][k], ``offsets`` int32 [E + 1],
+    ``order`` and ``place`` int32 [M k]. ``paro_experts_route`` and ``paro_experts_sort`` make it;
+    ``weights`` may be None where only paro_w4_experts_gated and its gradient are called."""
+
+    def __init__(self, ids, weights, offsets, order, place):
+        import torch
+        self.M, self.k = ids.shape
+        self.E = offsets.shape[0] - 1
+        self.ids, self.weights, self.offsets, self.order, self.place = ids, weights, offsets, order, place
+        self.device, i32, R = ids.get_device(), torch.int32, self.M * self.k
+        at = self.device
+        self._c = _Routing(self.M, self.E, self.k, _expect(ids, "ids", (self.M, self.k), i32, at),
+                           _expect(offsets, "offsets", (self.E + 1,), i32, at), _expect(order, "order", (R,), i32, at),
+                           _expect(place, "place", (R,), i32, at),
+                           _expect(weights, "weights", (self.M, self.k), torch.float32, at))
+
+    def _on(self, device):
+        if self.device != device:
+            raise ValueError("routing must be on the current device")
+        return ctypes.byref(self._c)
+
+
+def _route_workspace(M, E, k, workspace, device, current):
+    need = int(load_library().paro_experts_route_workspace_size(M, E, k)) if workspace is None else 0
+    if need:
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)  # (scratch: nothing has to be zero)
+    return _workspace(workspace, 0, device, current)
+
+
+def new_experts_route_workspace(M: int, E: int, k: int, device="cuda"):
+    """A workspace for paro_experts_route and paro_experts_sort (None when none is needed)."""
+    return _workspace(None, int(load_library().paro_experts_route_workspace_size(M, E, k)), device)[0]
+
+
+def _tables(M, k, E, device):
+    """offsets, order and place of a routing, not yet written."""
+    import torch
+    t = torch.empty(2 * M * k + E + 1, dtype=torch.int32, device=device)
+    return t[2 * M * k:], t[:M * k], t[M * k:2 * M * k]
+
+
+def paro_experts_route(logits, k: int, normalize: bool = True, workspace=None, stream=None) -> Routing:
+    """The ``k`` experts of every token with the largest logits ([M][E], fp32, fp16 or bf16), their softmax
+    weights (``normalize``: divided by their sum) and the tables of the routing."""
+    import torch
+    M, E = logits.shape
+    dev = torch.cuda.current_device()
+    with _made_on(stream):
+        ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+        offsets, order, place = _tables(M, k, E, logits.device)
+        workspace, ws_ptr, ws_bytes = _route_workspace(M, E, k, workspace, logits.device, dev)
+    _handed_out(stream, ids, weights, offsets)
+    _check(load_library().paro_experts_route(
+        _expect(logits, "logits", (M, E), logits.dtype, dev), _type(logits, "logits"), M, E, k, int(normalize),
+        ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), ws_ptr, ws_bytes,
+        _raw_stream(stream, dev)))
+    return Routing(ids, weights, offsets, order, place)
+
+
+def paro_experts_sort(ids, E: int, weights=None, workspace=None, stream=None) -> Routing:
+    """The routing of given ``ids`` (int32 [M][k]; outside 0 .. E - 1: no expert) and ``weights``."""
+    import torch
+    M, k = ids.shape
+    dev = torch.cuda.current_device()
+    with _made_on(stream):
+        offsets, order, place = _tables(M, k, E, ids.device)
+        workspace, ws_ptr, ws_bytes = _route_workspace(M, E, k, workspace, ids.device, dev)
+    _handed_out(stream, offsets)
+    _check(load_library().paro_experts_sort(
+        _expect(ids, "ids", (M, k), torch.int32, dev), M, E, k, offsets.data_ptr(), order.data_ptr(),
+        place.data_ptr(), ws_ptr, ws_bytes, _raw_stream(stream, dev)))
+    return Routing(ids, weights, offsets, order, place)
+
+
+def paro_experts_route_backward(logits, ids, weights, dweights, normalize: bool = True, dlogits=None, stream=None):
+    """Gradient at the logits of paro_experts_route ([M][E], their type) for dweights = dL/dweights (fp32 [M][k]);
+    ``ids`` and ``weights`` are the forward call's."""
+    import torch
+    M, E = logits.shape
+    k = ids.shape[1]
+    dev, f32 = torch.cuda.current_device(), torch.float32
+    if dlogits is None:
+        with _made_on(stream):
+            dlogits = torch.empty_like(logits)
+        _handed_out(stream, dlogits)
+    _check(load_library().paro_experts_route_backward(
+        _expect(logits, "logits", (M, E), logits.dtype, dev), _type(logits, "logits"), M, E, k, int(normalize),
+        _expect(ids, "ids", (M, k), torch.int32, dev), _expect(weights, "weights", (M, k), f32, dev),
+        _expect(dweights, "dweights", (M, k), f32, dev), _expect(dlogits, "dlogits", (M, E), logits.dtype, dev),
+        _raw_stream(stream, dev)))
+    return dlogits
+
+
+def _experts_size(call, M, E, k, N, d) -> int:
+    return int(getattr(load_library(), f"paro_w4_experts_{call}_workspace_size")(M, E, k, N, d))
+
+
+def new_experts_gated_workspace(M: int, E: int, k: int, N: int, d: int, device="cuda"):
+    """A workspace for paro_w4_experts_gated (None when none is needed)."""
+    return _workspace(None, _experts_size("gated", M, E, k, N, d), device)[0]
+
+
+def new_experts_combine_workspace(M: int, E: int, k: int, N: int, d: int, device="cuda"):
+    """A workspace for paro_w4_experts_combine (None when none is needed)."""
+    return _workspace(None, _experts_size("combine", M, E, k, N, d), device)[0]
+
+
+def new_experts_gated_backward_workspace(M: int, E: int, k: int, N: int, d: int, device="cuda"):
+    """A workspace for paro_w4_experts_gated_backward (None when none is needed)."""
+    return _workspace(None, _experts_size("gated_backward", M, E, k, N, d), device)[0]
+
+
+def new_experts_combine_backward_workspace(M: int, E: int, k: int, N: int, d: int, device="cuda"):
+    """A workspace for paro_w4_experts_combine_backward (None when none is needed)."""
+    return _workspace(None, _experts_size("combine_backward", M, E, k, N, d), device)[0]
+
+
+def _experts_weights(r, qweight, scales, zeros, bias, P, d, group, dev):
+    """Addresses of the weight stack of a routing's experts."""
+    import torch
+    f16, u8, E = torch.float16, torch.uint8, r.E
+    return (_expect(qweight, "qweight", (E, P, d // 2), u8, dev), _expect(scales, "scales", (E, P, d // group), f16, dev),
+            _expect(zeros, "zeros", (E, P, d // group), u8, dev), _expect(bias, "bias", (E, P), f16, dev))
+
+
+def paro_w4_experts_gated(routing: Routing, x, qweight, scales, zeros, bias=None, act: str = "silu", h=None,
+                          group: int = 128, workspace=None, stream=None):
+    """H = act(x Wg^T + bg) * (x Wu^T + bu) of every (token, expert) pair (fp16 [M k][N], rows in expert order; those
+    behind the last pair with an expert are left as they were) for the transformed activations ``x`` [M][d] and the
+    experts' weight blocks [E][2 N][d / 2] (gate, then up)."""
+    import torch
+    M, d = routing.M, x.shape[1]
+    N = qweight.shape[1] // 2
+    dev, f16 = torch.cuda.current_device(), torch.float16
+    need = _experts_size("gated", M, routing.E, routing.k, N, d) if workspace is None else 0
+    made = []
+    with _made_on(stream):
+        if h is None:
+            h = x.new_empty((M * routing.k, N))
+            made.append(h)
+        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device, dev)
+    _handed_out(stream, *made)
+    _check(load_library().paro_w4_experts_gated(
+        routing._on(dev), _expect(x, "x", (M, d), f16, dev),
+        *_experts_weights(routing, qweight, scales, zeros, bias, 2 * N, d, group, dev), _act(act),
+        _expect(h, "h", (M * routing.k, N), f16, dev), N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
+    return h
+
+
+def _scratch(call, r, N, d, workspace, device, current):
+    """A call's workspace, given or made (scratch: nothing has to be zero)."""
+    if workspace is None:
+        need = _experts_size(call, r.M, r.E, r.k, N, d)
+        if need:
+            import torch
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return _workspace(workspace, 0, device, current)
+
+
+def paro_w4_experts_combine(routing: Routing, h, qweight, scales, zeros, bias=None, residual=None, y=None,
+                            group: int = 128, workspace=None, stream=None):
+    """Y = residual + sum over a token's experts of weight (H W^T + b) (fp16 [M][N]) for rows ``h`` [M k][d] in expert
+    order and the experts' weights [E][N][d / 2]; ``y`` may be ``residual``."""
+    import torch
+    M, d = routing.M, h.shape[1]
+    N = qweight.shape[1]
+    dev, f16 = torch.cuda.current_device(), torch.float16
+    made = []
+    with _made_on(stream):
+        if y is None:
+            y = h.new_empty((M, N))
+            made.append(y)
+        workspace, ws_ptr, ws_bytes = _scratch("combine", routing, N, d, workspace, h.device, dev)
+    _handed_out(stream, *made)
+    _check(load_library().paro_w4_experts_combine(
+        routing._on(dev), _expect(h, "h", (M * routing.k, d), f16, dev),
+        *_experts_weights(routing, qweight, scales, zeros, bias, N, d, group, dev),
+        _expect(residual, "residual", (M, N), f16, dev), _expect(y, "y", (M, N), f16, dev), N, d, group, ws_ptr,
+        ws_bytes, _raw_stream(stream, dev)))
+    return y
+
+
+def paro_w4_experts_gated_backward(routing: Routing, x, qweight, scales, zeros, dh, bias=None, act: str = "silu",
+                                   dz=None, dx=None, want_dx: bool = True, group: int = 128, workspace=None,
+                                   stream=None):
+    """Gradients of paro_w4_experts_gated for dh = dL/dH ([M k][N], by row): returns (dx fp16 [M][d] or None, dz fp16
+    [M k][2 N]: the gate's columns, then the up projection's; rows behind the last pair are left as they were)."""
+    import torch
+    M, d = routing.M, x.shape[1]
+    N = qweight.shape[1] // 2
+    R = M * routing.k
+    dev, f16 = torch.cuda.current_device(), torch.float16
+    made = []
+    with _made_on(stream):
+        if dz is None:
+            dz = x.new_empty((R, 2 * N))
+            made.append(dz)
+        if dx is None and want_dx:
+            dx = x.new_empty((M, d))
+            made.append(dx)
+        workspace, ws_ptr, ws_bytes = _scratch("gated_backward", routing, N, d, workspace, x.device, dev) \
+            if dx is not None or workspace is not None else (None, None, 0)
+    _handed_out(stream, *made)
+    _check(load_library().paro_w4_experts_gated_backward(
+        routing._on(dev), _expect(x, "x", (M, d), f16, dev),
+        *_experts_weights(routing, qweight, scales, zeros, bias, 2 * N, d, group, dev), _act(act),
+        _expect(dh, "dh", (R, N), f16, dev), _expect(dz, "dz", (R, 2 * N), f16, dev),
+        _expect(dx, "dx", (M, d), f16, dev), N, d, group, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
+    return dx, dz
+
+
+def paro_w4_experts_combine_backward(routing: Routing, h, qweight, scales, zeros, dy, bias=None, dh=None,
+                                     dweights=None, group: int = 128, workspace=None, stream=None):
+    """Gradients of paro_w4_experts_combine for dy = dL/dY ([M][N]): returns (dh fp16 [M k][d], rows in expert order,
+    those behind the last pair left as they were; dweights fp32 [M][k])."""
+    import torch
+    M, d = routing.M, h.shape[1]
+    N = qweight.shape[1]
+    R = M * routing.k
+    dev, f16 = torch.cuda.current_device(), torch.float16
+    made = []
+    with _made_on(stream):
+        if dh is None:
+            dh = h.new_empty((R, d))
+            made.append(dh)
+        dweights = _given(dweights, "dweights", (M, routing.k), h.device, made)
+        workspace, ws_ptr, ws_bytes = _scratch("combine_backward", routing, N, d, workspace, h.device, dev)
+    _handed_out(stream, *made)
+    _check(load_library().paro_w4_experts_combine_backward(
+        routing._on(dev), _expect(h, "h", (R, d), f16, dev),
+        *_experts_weights(routing, qweight, scales, zeros, bias, N, d, group, dev),
+        _expect(dy, "dy", (M, N), f16, dev), _expect(dh, "dh", (R, d), f16, dev),
+        _expect(dweights, "dweights", (M, routing.k), torch.float32, dev), N, d, group, ws_ptr, ws_bytes,
+        _raw_stream(stream, dev)))
+    return dh, dweights
+
+
+def paro_distill_loss(z, values, index, lse=None, row_weight=None, temperature: float = 1.0, grad_scale: float = 1.0,
+                      gradients: bool = True, loss=None, dz=None, stream=None):
+    """T^2 KL(teacher || student) of each row, from the teacher's top logits ``values`` [M][K] at ``index`` int32 [M][K]
+    (-1: no entry) and the student's logits ``z`` [M][V]: returns (loss fp32 [M], grad_scale dL/dz of z's type or None).
+    ``lse`` fp32 [M]: log-sum-exp of all the teacher's logits / T, with which the rest of its mass is one more class.
+    ``row_weight`` fp32 [M]: rows of weight 0 are left out. ``dz`` may be ``z``."""
+    import torch
+    M, V = z.shape
+    K = values.shape[1]
+    dev, f32 = torch.cuda.current_device(), torch.float32
+    made = []
+    with _made_on(stream):
+        loss = _given(loss, "loss", (M,), z.device, made)
+        if dz is None and gradients:
+            dz = torch.empty_like(z)
+            made.append(dz)
+    _handed_out(stream, *made)
+    _check(load_library().paro_distill_loss(
+        _expect(z, "z", (M, V), z.dtype, dev), _type(z, "z"), _expect(values, "values", (M, K), values.dtype, dev),
+        _type(values, "values"), _expect(index, "index", (M, K), torch.int32, dev),
+        _expect(lse, "lse", (M,), f32, dev), _expect(row_weight, "row_weight", (M,), f32, dev), M, V, K, temperature,
+        grad_scale, _expect(loss, "loss", (M,), f32, dev), _expect(dz, "dz", (M, V), z.dtype, dev),
+        _raw_stream(stream, dev)))
+    return loss, dz
 
 
 def paro_adamw_moments(sizes) -> int:

@@ -292,6 +292,63 @@ hipError_t launch_adamw(const AdamwLaunch& a, uint32_t chunks, int param_type, i
 hipError_t launch_adamw(const AdamwTable& a, uint32_t chunks, int param_type, int grad_type, bool eight,
                         hipStream_t stream);
 
+// Mixture of experts. The limits of a routing, and its tables as the kernels take
+// them: R = M k pairs, rows in expert order.
+constexpr int kExpertsMax = 1024, kExpertsMaxK = 16;
+struct ExpertRouting {
+  int M, E, k, R;
+  const int *ids, *offsets, *order, *place;
+  const float* weights;
+};
+// Most blocks of at most bm rows of one expert that R rows in E experts make.
+inline int64_t expert_blocks(const ExpertRouting& t, int bm) {
+  const int64_t full = t.R / bm, used = t.E < t.R ? t.E : t.R;
+  return full + used < t.R ? full + used : t.R;
+}
+// The router (logits NULL: the tables of given ids) and its gradient
+// (experts_route.hip); scratch holds experts_route_scratch(M, E) bytes.
+size_t experts_route_scratch(int64_t M, int E);
+hipError_t launch_experts_route(const void* logits, int type, int64_t M, int E, int k, int normalize, int* ids,
+                                float* weights, int* offsets, int* order, int* place, void* scratch,
+                                hipStream_t stream);
+hipError_t launch_experts_route_backward(const void* logits, int type, int64_t M, int E, int k, int normalize,
+                                         const int* ids, const float* weights, const float* dweights, void* dlogits,
+                                         hipStream_t stream);
+// The experts' products in small tiles (w4_tiles.hip): epi kEpiGated and
+// kEpiGatedGrad on tokens x, kEpiShare on rows x in expert order; y by row.
+hipError_t launch_w4_experts_tiles(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
+                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
+// part [splits][R][d] = dz W_hat of each row's expert, in pieces of the
+// contraction (w4_input_grad_rows.hip); gather: dz by token, else by row.
+int experts_grad_rows_splits(const ExpertRouting& t, int64_t P, int64_t d);
+hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, const uint16_t* dz,
+                                       const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                                       float* part, int64_t P, int64_t d, int group, hipStream_t stream);
+// Sums over a token's experts and the weights' gradients (experts_sum.hip):
+//   y[m] = residual[m] + sum_s sum_p part[p][place[m][s]]  (fp16 [M][N]);
+//   dh[r] = w U[r], dw[p] = U[r] . h[r] + dy[m] . bias[e], U = sum_p part[p].
+hipError_t launch_experts_sum(const ExpertRouting& t, const float* part, int splits, const uint16_t* residual,
+                              uint16_t* y, int64_t N, hipStream_t stream);
+hipError_t launch_experts_share_grad(const ExpertRouting& t, const float* part, int splits, const uint16_t* h,
+                                     const uint16_t* dy, const uint16_t* bias, uint16_t* dh, float* dweights,
+                                     int64_t N, int64_t d, hipStream_t stream);
+
+// Distillation from a teacher's top logits (distill.hip).
+struct DistillArgs {
+  const void* z;          // [M][V]
+  const void* values;     // [M][K]
+  const int* index;       // [M][K]
+  const float* lse;       // [M] or NULL
+  const float* weight;    // [M] or NULL
+  float* loss;            // [M]
+  void* dz;               // [M][V] or NULL
+  int64_t M;
+  int V, K;
+  float temperature, grad_scale;
+};
+hipError_t launch_distill(const DistillArgs& a, int z_type, int value_type, hipStream_t stream);
+
 // Shared by the products' entry points (api.cpp): the argument checks (N: rows
 // of the weight block; *noop set when M == 0), the smallest workspace, and the
 // launches of the product with epilogue epi on a checked workspace.

@@ -6,7 +6,9 @@
 //                  second N rows of the weight block
 //   kEpiActGrad    dz = dy act'(Z + b)
 //   kEpiGatedGrad  dzg = dy (Zu + bu) act'(Zg + bg), dzu = dy act(Zg + bg)
-// All in fp32 with one rounding to fp16 at the store.
+//   kEpiShare      y = w (Z + b), w a row's own weight, fp32 (a token's experts
+//                  are summed from these)
+// All in fp32 with one rounding to fp16 at the store (kEpiShare: none).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,7 +20,7 @@
 
 namespace paro {
 
-enum { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2, kEpiActGrad = 3, kEpiGatedGrad = 4 };
+enum { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2, kEpiActGrad = 3, kEpiGatedGrad = 4, kEpiShare = 5 };
 constexpr bool epi_gated(int epi) { return epi == kEpiGated || epi == kEpiGatedGrad; }
 
 // The activation as the kernels take it: silu and gelu_tanh are both
@@ -261,6 +263,15 @@ __device__ __forceinline__ void epi_lane(f4* z, int m, int n, int N, const uint1
       write4(y + ((size_t)m * 2 + 1) * N + n, dy * v);
     }
   }
+}
+
+// kEpiShare of four neighbouring channels of one row held by one lane.
+__device__ __forceinline__ void epi_share(f4 z, float weight, int m, int n, int N, const uint16_t* bias, float* y) {
+  if (bias) {
+    const uint2 raw = *(const uint2*)(bias + n);
+    z += f4{half_lo(raw.x), half_hi(raw.x), half_lo(raw.y), half_hi(raw.y)};
+  }
+  *(f4*)(y + (size_t)m * N + n) = z * weight;
 }
 
 }  // namespace w4

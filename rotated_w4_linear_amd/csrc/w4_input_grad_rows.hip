@@ -28,6 +28,7 @@
 // codes are 360 vector instructions of a wavefront.
 #include <algorithm>
 
+#include "expert_rows.h"
 #include "paro_internal.h"
 #include "w4_common.h"
 
@@ -48,12 +49,14 @@ constexpr int row_waves(int tt) { return tt == 1 ? 16 : 8; }
 // codes, scales and zeros (two groups a row), dz; and room for a token block's sums
 constexpr int row_bytes(int tt) { return std::max(8192, 4096 + 1024 + 2048 * tt); }
 
-template <int TT>
+// ROWS: the tokens, or the experts' rows (a block then is one of an expert's rows
+// and contracts that expert's weights; the sums always go to `part`, by row).
+template <class ROWS, int TT>
 __global__ __launch_bounds__(64 * row_waves(TT))
 void w4_grad_rows_kernel(const uint8_t* __restrict__ qw, const uint16_t* __restrict__ sc,
                          const uint8_t* __restrict__ zr, const uint16_t* __restrict__ dz, int M, int P, int d,
                          int gsh, int mblk, int kblk, int splits, uint16_t* __restrict__ dx,
-                         float* __restrict__ part) {
+                         float* __restrict__ part, ROWS rows_of) {
   constexpr int WB = row_bytes(TT);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[row_waves(TT) * WB];
   const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
@@ -61,21 +64,33 @@ void w4_grad_rows_kernel(const uint8_t* __restrict__ qw, const uint16_t* __restr
   // token blocks fastest: they share the weights
   const int blk = blockIdx.x;
   const int mb = blk % mblk, kb = blk / mblk % kblk, sp = blk / (mblk * kblk);
-  const int m0 = 16 * TT * mb, k0 = 128 * kb;
+  int m0 = 16 * TT * mb;
+  const int k0 = 128 * kb, all = M;
   const int chunks = (P + kChunk - 1) / kChunk;
   const int c0 = (int)((int64_t)chunks * sp / splits), c1 = (int)((int64_t)chunks * (sp + 1) / splits);
   const int sgr = d >> (6 + gsh), gi = k0 >> (6 + gsh);
   uint8_t* cl = lds + w * WB;
   uint2* tab = (uint2*)(cl + 4096);  // [64 rows][2 groups]
   uint8_t* zl = cl + 5120;
+  if constexpr (ROWS::kExperts) {
+    ExpertTile tile;
+    if (!rows_of.find(mb, 16 * TT, tile)) return;
+    m0 = tile.first;
+    M = tile.end;
+    const size_t first = (size_t)tile.expert * P;
+    qw += first * (size_t)(d >> 1);
+    sc += first * sgr;
+    zr += first * sgr;
+  }
   const int tokens = min(16 * TT, M - m0);
-  const __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc((void*)(dz + (size_t)m0 * P), (short)0,
-                                                                      tokens * P * 2, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(dz + (ROWS::kGather ? 0 : (size_t)m0 * P)), (short)0,
+      (ROWS::kGather ? rows_tokens(rows_of) : tokens) * P * 2, kRsrcWord3);
   uint32_t doff[8];  // (tokens past M repeat the last one and are never stored)
 #pragma unroll
   for (int t = 0; t < 2 * TT; ++t) {
     const int row = 8 * t + (lane >> 3);
-    doff[t] = (uint32_t)(min(row, tokens - 1) * P * 2);
+    doff[t] = (uint32_t)(source_row(rows_of, m0, min(row, tokens - 1)) * P * 2);
   }
   const int dpiece = lane & 7;
   const uint32_t one = fp16_1024_pair();
@@ -173,8 +188,8 @@ void w4_grad_rows_kernel(const uint8_t* __restrict__ qw, const uint16_t* __restr
       for (int k = 1; k < nw; ++k) sum += *(const f4*)(p + k * WB);
       const int m = m0 + 16 * t + r, k = k0 + 8 * (4 * kq + (jh >> 1)) + 4 * (jh & 1);
       if (m < M) {
-        if (splits > 1) {
-          *(f4*)(part + ((size_t)sp * M + m) * d + k) = sum;
+        if (ROWS::kExperts || splits > 1) {
+          *(f4*)(part + ((size_t)sp * all + m) * d + k) = sum;
         } else {
           uint2 o;
           o.x = half_bits(sum[0]) | (half_bits(sum[1]) << 16);
@@ -238,16 +253,55 @@ hipError_t launch_w4_input_grad_rows(const uint16_t* dz, const uint8_t* qweight,
   auto go = [&](auto kernel, int waves) {
     const int nw = (int)std::min<int64_t>(waves, most);
     hipLaunchKernelGGL(kernel, dim3((unsigned)(mblk * kblk * splits)), dim3(64 * nw), 0, stream, qweight, scales,
-                       zeros, dz, (int)M, (int)P, (int)d, gsh, mblk, kblk, splits, dx, (float*)scratch);
+                       zeros, dz, (int)M, (int)P, (int)d, gsh, mblk, kblk, splits, dx, (float*)scratch, AllRows{});
   };
-  if (tt == 1) go(w4_grad_rows_kernel<1>, row_waves(1));
-  else if (tt == 2) go(w4_grad_rows_kernel<2>, row_waves(2));
-  else go(w4_grad_rows_kernel<4>, row_waves(4));
+  if (tt == 1) go(w4_grad_rows_kernel<AllRows, 1>, row_waves(1));
+  else if (tt == 2) go(w4_grad_rows_kernel<AllRows, 2>, row_waves(2));
+  else go(w4_grad_rows_kernel<AllRows, 4>, row_waves(4));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const int64_t n4 = M * d / 4;
   hipLaunchKernelGGL(add_splits_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, stream, (const f4*)scratch,
                      splits, n4, (uint2*)dx);
+  return hipGetLastError();
+}
+
+// Rows of an expert per block, and ranges of p: as for tokens, by the experts'
+// mean number of rows and the blocks that they are expected to make.
+namespace {
+int expert_rows_per_block(const ExpertRouting& t) {
+  const int64_t mean = t.R / std::min<int64_t>(t.E, t.R);
+  return mean <= 8 ? 1 : mean <= 24 ? 2 : 4;
+}
+}  // namespace
+
+int experts_grad_rows_splits(const ExpertRouting& t, int64_t P, int64_t d) {
+  const int tt = expert_rows_per_block(t);
+  const int64_t blocks = std::max<int64_t>(std::min<int64_t>(t.E, t.R), t.R / (16 * tt)) * (d / 128);
+  const int64_t chunks = (P + kChunk - 1) / kChunk;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kCus / blocks, chunks / 8, 8}));
+}
+
+hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, const uint16_t* dz,
+                                       const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                                       float* part, int64_t P, int64_t d, int group, hipStream_t stream) {
+  const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
+  const int tt = expert_rows_per_block(t), splits = experts_grad_rows_splits(t, P, d);
+  const int kblk = (int)(d / 128);
+  const int64_t mblk = expert_blocks(t, 16 * tt), most = (P + kChunk - 1) / kChunk / splits + 1;
+  auto go = [&](auto kernel, int waves, auto rows) {
+    const int nw = (int)std::min<int64_t>(waves, most);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(mblk * kblk * splits)), dim3(64 * nw), 0, stream, qweight, scales,
+                       zeros, dz, t.R, (int)P, (int)d, gsh, (int)mblk, kblk, splits, nullptr, part, rows);
+  };
+  auto shape = [&](auto rows) {
+    typedef decltype(rows) Rows;
+    if (tt == 1) go(w4_grad_rows_kernel<Rows, 1>, row_waves(1), rows);
+    else if (tt == 2) go(w4_grad_rows_kernel<Rows, 2>, row_waves(2), rows);
+    else go(w4_grad_rows_kernel<Rows, 4>, row_waves(4), rows);
+  };
+  if (gather) shape(ExpertRows<true>{t});
+  else shape(ExpertRows<false>{t});
   return hipGetLastError();
 }
 
