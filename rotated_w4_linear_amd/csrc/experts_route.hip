@@ -1,16 +1,20 @@
 // gfx950 kernels of the experts' router:
 //   p = softmax(l) over the E experts of a token, S its k largest logits (the
 //   lower expert first where they are equal), w_s = p_s, or p_s / sum_S p;
-// then the (token, slot) pairs in expert order, by counting: chunks of 64
-// tokens count their pairs per expert, one workgroup turns the counts into each
-// chunk's first row of every expert, and the chunks place their pairs, in pair
-// order inside an expert. Up to 64 tokens one workgroup does all of it in one
-// launch.
+// then the (token, slot) pairs in expert order, by counting: chunks of 256
+// tokens count their pairs per expert, and each chunk then adds up the counts of
+// the chunks before it and of the experts before each one, and places its pairs,
+// in pair order inside an expert. Up to 256 tokens one launch does all of it.
+// (Chunks of 64 tokens with a third kernel that turned the counts into first
+// rows, one workgroup walking over the chunks: 16384 tokens, 8 of 256 experts,
+// 234 us.)
 //
 // A wavefront takes a token, 64 experts at a time in a register per lane, and
 // picks the largest of (logit, -expert) k times with a reduction over the
 // lanes. What bounds it: at a few tokens the launch and the k reductions one
 // after the other; at many their instructions (the logits are read once).
+#include <algorithm>
+
 #include "paro_internal.h"
 #include "paro_types.h"
 
@@ -19,8 +23,8 @@
 namespace paro {
 namespace {
 
-constexpr int kChunkTokens = 64;
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kChunkTokens = 256;
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
 
 // Order of the floats as unsigned numbers, never 0 for an expert that can be
 // taken; -inf and NaN: 0.
@@ -133,45 +137,89 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* total) {
   return before + s - v;
 }
 
-// Places a chunk's pairs (ids in LDS, -1 and others outside [0, E): bucket E).
-// pre[b][e] becomes the first row of batch b's (64 pairs) pairs of expert e:
-// base(e) for batch 0. order has -1 in the rows of bucket E.
-template <class Base>
-__device__ __forceinline__ void place_chunk(const int* ids, int pairs, int pair0, int E, int* pre, Base base,
-                                            int* __restrict__ order, int* __restrict__ place) {
+// LDS of a chunk: its pairs' experts (those without one: bucket E), for each
+// batch of 64 pairs the rows of every bucket before it in the chunk, and each
+// bucket's first row.
+struct ChunkLds {
+  int* ids;       // [pairs]
+  int* first;     // [E + 1]
+  int* red;       // [kWaves]
+  uint16_t* pre;  // [batches][E + 1]
+};
+__device__ __forceinline__ ChunkLds chunk_lds(uint8_t* at, int pairs, int E) {
+  ChunkLds l;
+  l.ids = (int*)at;
+  l.first = l.ids + pairs;
+  l.red = l.first + E + 1;
+  l.pre = (uint16_t*)(l.red + kWaves);
+  return l;
+}
+size_t chunk_lds_bytes(int64_t pairs, int E) {
+  return (size_t)(pairs + E + 1 + kWaves) * 4 + (size_t)((pairs + 63) / 64) * (E + 1) * 2;
+}
+
+// Places a chunk's pairs behind the rows that first holds: a row is first[e], the
+// expert's pairs in the batches before, and those before it in its batch. order
+// has -1 in the rows of bucket E.
+__device__ __forceinline__ void place_chunk(const ChunkLds& l, int pairs, int pair0, int E, int* __restrict__ order,
+                                            int* __restrict__ place) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int batches = (pairs + 63) >> 6, EB = E + 1;
-  for (int i = tid; i < batches * EB; i += kThreads) pre[i] = 0;
+  for (int i = tid; i < batches * EB; i += kThreads) l.pre[i] = 0;
   __syncthreads();
-  for (int b = w; b < batches; b += kWaves) {
+  auto batch = [&](int b, bool& in, uint32_t& e, uint64_t& m) {
     const int p = 64 * b + lane;
-    const bool in = p < pairs;
-    const uint32_t e = in ? (uint32_t)ids[p] : 2047u;  // (lanes past the end: a bucket of their own)
-    const uint64_t m = same_lanes(e);
-    if (in && (m & ((uint64_t(1) << lane) - 1)) == 0) pre[b * EB + e] = __popcll(m);
+    in = p < pairs;
+    e = in ? (uint32_t)l.ids[p] : 2047u;  // (lanes past the end: a bucket of their own)
+    m = same_lanes(e);
+  };
+  bool in;
+  uint32_t e;
+  uint64_t m;
+  for (int b = w; b < batches; b += kWaves) {
+    batch(b, in, e, m);
+    if (in && (m & ((uint64_t(1) << lane) - 1)) == 0) l.pre[b * EB + e] = (uint16_t)__popcll(m);
   }
   __syncthreads();
-  for (int e = tid; e < EB; e += kThreads) {
-    int at = base(e);
-    for (int b = 0; b < batches; ++b) {
-      const int n = pre[b * EB + e];
-      pre[b * EB + e] = at;
-      at += n;
+  if (batches > 1) {
+    for (int x = tid; x < EB; x += kThreads) {
+      int at = 0;
+      for (int b = 0; b < batches; ++b) {
+        const int n = l.pre[b * EB + x];
+        l.pre[b * EB + x] = (uint16_t)at;
+        at += n;
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
   for (int b = w; b < batches; b += kWaves) {
-    const int p = 64 * b + lane;
-    const bool in = p < pairs;
-    const uint32_t e = in ? (uint32_t)ids[p] : 2047u;
-    const uint64_t m = same_lanes(e);
+    batch(b, in, e, m);
     if (in) {
-      const int row = pre[b * EB + e] + __popcll(m & ((uint64_t(1) << lane) - 1));
+      const int before = batches > 1 ? l.pre[b * EB + e] : 0;
+      const int row = l.first[e] + before + __popcll(m & ((uint64_t(1) << lane) - 1));
       const bool live = e < (uint32_t)E;
-      order[row] = live ? pair0 + p : -1;
-      place[pair0 + p] = live ? row : -1;
+      order[row] = live ? pair0 + 64 * b + lane : -1;
+      place[pair0 + 64 * b + lane] = live ? row : -1;
     }
   }
+}
+
+// first[e], e's pairs, to the first row of e: the rows of the experts before it
+// (and offsets, if given; offsets[E] is that of bucket E). more[e] is added.
+template <class More>
+__device__ __forceinline__ void scan_first(const ChunkLds& l, int E, int* offsets, More more) {
+  int carry = 0;
+  for (int e0 = 0; e0 < E + 1; e0 += kThreads) {
+    const int e = e0 + (int)threadIdx.x;
+    int total;
+    const int at = carry + block_scan(e <= E ? l.first[e] : 0, l.red, &total);
+    if (e <= E) {
+      if (offsets) offsets[e] = at;
+      l.first[e] = at + more(e);
+    }
+    carry += total;
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ int bucket(int id, int E) { return (uint32_t)id < (uint32_t)E ? id : E; }
@@ -184,14 +232,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const typename T::raw* 
                                                          int* ids, float* __restrict__ weights,
                                                          int* __restrict__ counts, int* __restrict__ offsets,
                                                          int* __restrict__ order, int* __restrict__ place) {
-  __shared__ int lids[kChunkTokens * kExpertsMaxK];
-  __shared__ int hist[kExpertsMax + 1];
-  __shared__ int red[kWaves];
-  extern __shared__ int pre[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int t0 = kChunkTokens * blockIdx.x, tokens = min(kChunkTokens, M - t0);
-  const int pairs = tokens * k, EB = E + 1;
-  for (int i = tid; i < EB; i += kThreads) hist[i] = 0;
+  const int pairs = tokens * k;
+  const ChunkLds l = chunk_lds(dyn, min(kChunkTokens, M) * k, E);
+  for (int i = tid; i <= E; i += kThreads) l.first[i] = 0;
   __syncthreads();
   if constexpr (ROUTE) {
     for (int t = w; t < tokens; t += kWaves) {
@@ -202,85 +248,70 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const typename T::raw* 
         const size_t p = (size_t)(t0 + t) * k + lane;
         ids[p] = id;
         weights[p] = weight;
-        lids[t * k + lane] = bucket(id, E);
-        atomicAdd(&hist[bucket(id, E)], 1);
+        l.ids[t * k + lane] = bucket(id, E);
+        atomicAdd(&l.first[bucket(id, E)], 1);
       }
     }
   } else {
     for (int p = tid; p < pairs; p += kThreads) {
       const int e = bucket(given[(size_t)t0 * k + p], E);
-      lids[p] = e;
-      atomicAdd(&hist[e], 1);
+      l.ids[p] = e;
+      atomicAdd(&l.first[e], 1);
     }
   }
   __syncthreads();
   if (gridDim.x > 1) {
-    for (int i = tid; i < EB; i += kThreads) counts[(size_t)blockIdx.x * EB + i] = hist[i];
+    for (int i = tid; i <= E; i += kThreads) counts[(size_t)blockIdx.x * (E + 1) + i] = l.first[i];
     return;
   }
-  int carry = 0;
-  for (int e0 = 0; e0 < EB; e0 += kThreads) {
-    const int e = e0 + tid, n = e < EB ? hist[e] : 0;
-    int total;
-    const int at = carry + block_scan(n, red, &total);
-    if (e < EB) {
-      offsets[e] = at;  // (offsets[E]: the first row of bucket E, the pairs without an expert)
-      hist[e] = at;
-    }
-    carry += total;
-  }
-  __syncthreads();
-  place_chunk(lids, pairs, 0, E, pre, [&](int e) { return hist[e]; }, order, place);
+  scan_first(l, E, offsets, [](int) { return 0; });
+  place_chunk(l, pairs, 0, E, order, place);
 }
 
-// counts [chunks][E + 1] to each chunk's first row of every expert, and the offsets
-__global__ __launch_bounds__(kThreads) void scan_kernel(int* counts, int chunks, int E, int* __restrict__ offsets) {
-  __shared__ int red[kWaves];
-  const int EB = E + 1;
-  int carry = 0;
-  for (int e0 = 0; e0 < EB; e0 += kThreads) {
-    const int e = e0 + (int)threadIdx.x;
-    int n = 0;
-    if (e < EB)
-      for (int c = 0; c < chunks; ++c) n += counts[(size_t)c * EB + e];
-    int total;
-    int at = carry + block_scan(n, red, &total);
-    if (e < EB) {
-      offsets[e] = at;
-      for (int c = 0; c < chunks; ++c) {
-        const int m = counts[(size_t)c * EB + e];
-        counts[(size_t)c * EB + e] = at;
-        at += m;
-      }
-    }
-    carry += total;
-  }
-}
-
+// The tables of one chunk, from all chunks' counts [chunks][E + 1]. (Every
+// workgroup reads them all: 66 KB at 16384 tokens and 256 experts, from L2.)
 __global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__ ids, int M, int E, int k,
-                                                         const int* __restrict__ base, int* __restrict__ order,
+                                                         const int* __restrict__ counts, int chunks,
+                                                         int* __restrict__ offsets, int* __restrict__ order,
                                                          int* __restrict__ place) {
-  __shared__ int lids[kChunkTokens * kExpertsMaxK];
-  extern __shared__ int pre[];
-  const int t0 = kChunkTokens * blockIdx.x, pairs = min(kChunkTokens, M - t0) * k;
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ int before[kExpertsMax + 1];
+  const int tid = threadIdx.x, mine = blockIdx.x;
+  const int t0 = kChunkTokens * mine, pairs = min(kChunkTokens, M - t0) * k;
   const int pair0 = t0 * k;
-  for (int p = threadIdx.x; p < pairs; p += kThreads) lids[p] = bucket(ids[pair0 + p], E);
+  const ChunkLds l = chunk_lds(dyn, kChunkTokens * k, E);
+  for (int i = tid; i <= E; i += kThreads) l.first[i] = before[i] = 0;
   __syncthreads();
-  const int* mine = base + (size_t)blockIdx.x * (E + 1);
-  place_chunk(lids, pairs, pair0, E, pre, [&](int e) { return mine[e]; }, order, place);
+  for (int p = tid; p < pairs; p += kThreads) l.ids[p] = bucket(ids[pair0 + p], E);
+  // parts of the chunks side by side, as many as there are threads for
+  const int EB = E + 1, parts = max(1, kThreads / EB), part = tid / EB;
+  for (int e = tid - part * EB; part < parts && e < EB; e += kThreads) {
+    int sum = 0, all = 0;
+#pragma unroll 8
+    for (int c = part; c < chunks; c += parts) {
+      const int n = counts[(size_t)c * EB + e];
+      all += n;
+      sum += c < mine ? n : 0;
+    }
+    atomicAdd(&l.first[e], all);  // (whole numbers: the same in any order)
+    atomicAdd(&before[e], sum);
+  }
+  __syncthreads();
+  scan_first(l, E, mine == 0 ? offsets : nullptr, [&](int e) { return before[e]; });
+  place_chunk(l, pairs, pair0, E, order, place);
 }
 
 // Gradient at the logits, a wavefront per token. Normalised weights:
 //   dl_i = w_i (dw_i - sum_S w dw) for i in S, else 0;
 // p itself: dl_j = [j in S] p_j dw_j - p_j sum_S p dw.
 template <class T>
-__global__ __launch_bounds__(kThreads) void route_backward_kernel(const typename T::raw* __restrict__ logits,
+__global__ __launch_bounds__(256) void route_backward_kernel(const typename T::raw* __restrict__ logits,
                                                                   const int* __restrict__ ids,
                                                                   const float* __restrict__ weights,
                                                                   const float* __restrict__ dweights, int M, int E,
                                                                   int k, int normalize,
                                                                   typename T::raw* __restrict__ dlogits) {
-  const int lane = threadIdx.x & 63, m = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (m >= M) return;
   int id = -1;
   float w = 0.0f, dw = 0.0f;
@@ -321,14 +352,25 @@ int experts_per_lane(int E) {
   while (64 * n < E) n *= 2;
   return n;
 }
-unsigned place_lds(int64_t tokens, int E, int k) { return (unsigned)((tokens * k + 63) / 64 * (E + 1) * 4); }
+
+// (dynamic LDS beyond what a launch takes by itself)
+template <class K>
+hipError_t allow_lds(K kernel, size_t bytes) {
+  if (bytes <= 65536) return hipSuccess;
+  return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 
 template <class T, bool ROUTE>
-void launch_route(int chunks, unsigned lds, hipStream_t stream, const void* logits, const int* given, int M, int E,
-                  int k, int normalize, int* ids, float* weights, int* counts, int* offsets, int* order, int* place) {
+hipError_t launch_route(int chunks, hipStream_t stream, const void* logits, const int* given, int M, int E, int k,
+                        int normalize, int* ids, float* weights, int* counts, int* offsets, int* order, int* place) {
+  const size_t lds = chunk_lds_bytes((int64_t)std::min(kChunkTokens, M) * k, E);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)chunks), dim3(kThreads), lds, stream, (const typename T::raw*)logits,
-                       given, M, E, k, normalize, ids, weights, counts, offsets, order, place);
+    const hipError_t e = allow_lds(kernel, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)chunks), dim3(kThreads), (unsigned)lds, stream,
+                       (const typename T::raw*)logits, given, M, E, k, normalize, ids, weights, counts, offsets, order,
+                       place);
+    return hipGetLastError();
   };
   switch (ROUTE ? experts_per_lane(E) : 1) {
     case 1: return go(route_kernel<T, 1, ROUTE>);
@@ -350,32 +392,31 @@ hipError_t launch_experts_route(const void* logits, int type, int64_t M, int E, 
                                 float* weights, int* offsets, int* order, int* place, void* scratch,
                                 hipStream_t stream) {
   const int chunks = (int)((M + kChunkTokens - 1) / kChunkTokens);
-  const unsigned lds = chunks == 1 ? place_lds(M, E, k) : 0;
   int* counts = (int*)scratch;
+  hipError_t e = hipSuccess;
   if (!logits)
-    launch_route<F32, false>(chunks, lds, stream, nullptr, ids, (int)M, E, k, 0, nullptr, nullptr, counts, offsets,
-                             order, place);
+    e = launch_route<F32, false>(chunks, stream, nullptr, ids, (int)M, E, k, 0, nullptr, nullptr, counts, offsets,
+                                 order, place);
   else
     with_type(type, [&](auto t) {
-      launch_route<decltype(t), true>(chunks, lds, stream, logits, nullptr, (int)M, E, k, normalize, ids, weights,
-                                      counts, offsets, order, place);
+      e = launch_route<decltype(t), true>(chunks, stream, logits, nullptr, (int)M, E, k, normalize, ids, weights,
+                                          counts, offsets, order, place);
     });
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks == 1) return e;
-  hipLaunchKernelGGL(scan_kernel, dim3(1), dim3(kThreads), 0, stream, counts, chunks, E, offsets);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(place_kernel, dim3((unsigned)chunks), dim3(kThreads), place_lds(kChunkTokens, E, k), stream, ids,
-                     (int)M, E, k, counts, order, place);
+  const size_t lds = chunk_lds_bytes((int64_t)kChunkTokens * k, E);
+  if ((e = allow_lds(place_kernel, lds)) != hipSuccess) return e;
+  hipLaunchKernelGGL(place_kernel, dim3((unsigned)chunks), dim3(kThreads), (unsigned)lds, stream, ids, (int)M, E, k,
+                     counts, chunks, offsets, order, place);
   return hipGetLastError();
 }
 
 hipError_t launch_experts_route_backward(const void* logits, int type, int64_t M, int E, int k, int normalize,
                                          const int* ids, const float* weights, const float* dweights, void* dlogits,
                                          hipStream_t stream) {
-  const unsigned blocks = (unsigned)((M + kWaves - 1) / kWaves);
+  const unsigned blocks = (unsigned)((M + 3) / 4);
   with_type(type, [&](auto t) {
     typedef decltype(t) T;
-    hipLaunchKernelGGL(route_backward_kernel<T>, dim3(blocks), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL(route_backward_kernel<T>, dim3(blocks), dim3(256), 0, stream,
                        (const typename T::raw*)logits, ids, weights, dweights, (int)M, E, k, normalize,
                        (typename T::raw*)dlogits);
   });

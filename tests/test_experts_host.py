@@ -130,7 +130,7 @@ def refused(paro, fn, args, status):
 def test_route_refusals(paro):
     lib = paro.load_library()
 
-    def args(logits=A, type=0, M=100, E=8, k=2, normalize=1, ids=A, weights=A, offsets=A, order=A, place=A, ws=A,
+    def args(logits=A, type=0, M=1000, E=8, k=2, normalize=1, ids=A, weights=A, offsets=A, order=A, place=A, ws=A,
              ws_bytes=1 << 20):
         return logits, type, M, E, k, normalize, ids, weights, offsets, order, place, ws, ws_bytes, None
     fn = lib.paro_experts_route
@@ -142,13 +142,13 @@ def test_route_refusals(paro):
                         ({"logits": A + 2}, ALIGN), ({"ids": A + 2}, ALIGN), ({"ws": None}, WORKSPACE),
                         ({"ws_bytes": 17}, WORKSPACE), ({"ws": A + 128}, ALIGN)]:
         refused(paro, fn, args(**bad), status)
-    assert lib.paro_experts_route_workspace_size(64, 8, 2) == 0
-    assert lib.paro_experts_route_workspace_size(65, 8, 2) == 2 * 9 * 4
+    assert lib.paro_experts_route_workspace_size(256, 8, 2) == 0
+    assert lib.paro_experts_route_workspace_size(257, 8, 2) == 2 * 9 * 4
     for M, E, k in [(-1, 8, 2), (10, 0, 1), (10, 8, 9), (100, 2000, 2), (1 << 30, 8, 2)]:
         assert lib.paro_experts_route_workspace_size(M, E, k) == 0
 
     sort = lib.paro_experts_sort
-    ok = [A, 100, 8, 2, A, A, A, A, 1 << 20, None]
+    ok = [A, 1000, 8, 2, A, A, A, A, 1 << 20, None]
     for i, v, status in [(0, None, NULL), (4, None, NULL), (5, None, NULL), (6, None, NULL), (1, -1, SHAPE),
                          (2, 0, SHAPE), (3, 17, SHAPE), (7, None, WORKSPACE), (0, A + 2, ALIGN)]:
         refused(paro, sort, ok[:i] + [v] + ok[i + 1:], status)
