@@ -88,8 +88,9 @@ ExpertRouting sizes_only(int64_t M, int32_t E, int32_t k) {
   return {(int)M, E, k, (int)(M * k), nullptr, nullptr, nullptr, nullptr, nullptr};
 }
 
-size_t grad_bytes(const ExpertRouting& t, int64_t P, int64_t d) {
-  return a256((size_t)experts_grad_rows_splits(t, P, d) * t.R * d * 4);
+size_t grad_bytes(const ExpertRouting& t, int64_t P, int64_t d, bool share) {
+  if (!experts_grad_wide_fit(t, P)) return a256((size_t)experts_grad_rows_splits(t, P, d) * t.R * d * 4);
+  return a256(share ? experts_grad_dots(t, d) : (size_t)t.R * d * 4);
 }
 
 bool known_act(int32_t act) { return act >= PARO_ACT_NONE && act <= PARO_ACT_RELU; }
@@ -180,7 +181,7 @@ int paro_w4_experts_gated(const paro_routing* routing, const uint16_t* x, const 
   if ((st = check_workspace(f, 0, workspace, workspace_bytes)) != PARO_OK) return st;
   W4Epilogue ep;
   ep.act = act;
-  const hipError_t e = launch_w4_experts_tiles(kEpiGated, t, x, qweight, scales, zeros, bias, h, N, d, group, ep, stream);
+  const hipError_t e = launch_w4_experts(kEpiGated, t, x, qweight, scales, zeros, bias, h, N, d, group, ep, stream);
   return e == hipSuccess ? PARO_OK : hip_fail(e, "paro_w4_experts_gated");
 }
 
@@ -200,7 +201,7 @@ int paro_w4_experts_combine(const paro_routing* routing, const uint16_t* h, cons
   if (!aligned(residual, 16)) return fail(PARO_ERR_ALIGN, f + ": residual must be 16-byte aligned");
   const size_t need = paro_w4_experts_combine_workspace_size(t.M, t.E, t.k, N, d);
   if ((st = check_workspace(f, need, workspace, workspace_bytes)) != PARO_OK) return st;
-  hipError_t e = launch_w4_experts_tiles(kEpiShare, t, h, qweight, scales, zeros, bias, workspace, N, d, group,
+  hipError_t e = launch_w4_experts(kEpiShare, t, h, qweight, scales, zeros, bias, workspace, N, d, group,
                                          W4Epilogue{}, stream);
   if (e == hipSuccess) e = launch_experts_sum(t, (const float*)workspace, 1, residual, y, N, stream);
   return e == hipSuccess ? PARO_OK : hip_fail(e, "paro_w4_experts_combine");
@@ -208,7 +209,7 @@ int paro_w4_experts_combine(const paro_routing* routing, const uint16_t* h, cons
 
 size_t paro_w4_experts_gated_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d) {
   if (N > (int64_t(1) << 20) || !good_sizes(M, E, k, 2 * N, d) || N % 16) return 0;
-  return grad_bytes(sizes_only(M, E, k), 2 * N, d);
+  return grad_bytes(sizes_only(M, E, k), 2 * N, d, false);
 }
 
 int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* x, const uint8_t* qweight,
@@ -230,17 +231,20 @@ int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* 
   W4Epilogue ep;
   ep.aux = dh;
   ep.act = act;
-  hipError_t e = launch_w4_experts_tiles(kEpiGatedGrad, t, x, qweight, scales, zeros, bias, dz, N, d, group, ep, stream);
+  hipError_t e = launch_w4_experts(kEpiGatedGrad, t, x, qweight, scales, zeros, bias, dz, N, d, group, ep, stream);
   if (e == hipSuccess && dx) {
-    const int splits = experts_grad_rows_splits(t, 2 * N, d);
-    e = launch_w4_experts_grad_rows(t, false, dz, qweight, scales, zeros, (float*)workspace, 2 * N, d, group, stream);
+    const bool wide = experts_grad_wide_fit(t, 2 * N);
+    const int splits = wide ? 1 : experts_grad_rows_splits(t, 2 * N, d);
+    float* part = (float*)workspace;
+    e = wide ? launch_w4_experts_grad_part(t, dz, qweight, scales, zeros, part, 2 * N, d, group, stream)
+             : launch_w4_experts_grad_rows(t, false, dz, qweight, scales, zeros, part, 2 * N, d, group, stream);
     if (e == hipSuccess) e = launch_experts_sum(t, (const float*)workspace, splits, nullptr, dx, d, stream);
   }
   return e == hipSuccess ? PARO_OK : hip_fail(e, "paro_w4_experts_gated_backward");
 }
 
 size_t paro_w4_experts_combine_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d) {
-  return good_sizes(M, E, k, N, d) ? grad_bytes(sizes_only(M, E, k), N, d) : 0;
+  return good_sizes(M, E, k, N, d) ? grad_bytes(sizes_only(M, E, k), N, d, true) : 0;
 }
 
 int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t* h, const uint8_t* qweight,
@@ -257,10 +261,17 @@ int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t
     return fail(PARO_ERR_ALIGN, f + ": dy must be 16-byte aligned, dweights 4-byte");
   const size_t need = paro_w4_experts_combine_backward_workspace_size(t.M, t.E, t.k, N, d);
   if ((st = check_workspace(f, need, workspace, workspace_bytes)) != PARO_OK) return st;
-  const int splits = experts_grad_rows_splits(t, N, d);
-  hipError_t e = launch_w4_experts_grad_rows(t, true, dy, qweight, scales, zeros, (float*)workspace, N, d, group, stream);
-  if (e == hipSuccess)
-    e = launch_experts_share_grad(t, (const float*)workspace, splits, h, dy, bias, dh, dweights, N, d, stream);
+  float* part = (float*)workspace;
+  hipError_t e;
+  if (experts_grad_wide_fit(t, N)) {
+    e = launch_w4_experts_grad_share(t, dy, qweight, scales, zeros, part, h, dh, N, d, group, stream);
+    if (e == hipSuccess)
+      e = launch_experts_dots(t, part, (int)(experts_grad_dots(t, d) / 4 / t.R), dy, bias, dweights, N, stream);
+  } else {
+    e = launch_w4_experts_grad_rows(t, true, dy, qweight, scales, zeros, part, N, d, group, stream);
+    if (e == hipSuccess)
+      e = launch_experts_share_grad(t, part, experts_grad_rows_splits(t, N, d), h, dy, bias, dh, dweights, N, d, stream);
+  }
   return e == hipSuccess ? PARO_OK : hip_fail(e, "paro_w4_experts_combine_backward");
 }
 

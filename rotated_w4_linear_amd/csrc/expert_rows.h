@@ -58,6 +58,61 @@ struct ExpertRows {
     return false;
   }
 
+  // Blocks of bm rows that the experts make.
+  __device__ __forceinline__ int blocks(int bm) const {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int e0 = 0; e0 < t.E; e0 += 64) {
+      const int e = e0 + lane;
+      const int a = min(max(t.offsets[min(e, t.E)], 0), t.R), b = min(max(t.offsets[min(e + 1, t.E)], 0), t.R);
+      n += b > a ? (b - a + bm - 1) / bm : 0;
+    }
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) n += __shfl_xor(n, x);
+    return __builtin_amdgcn_readfirstlane(n);
+  }
+
+  // The tile of workgroup b, of all blocks of at most bm rows by nblk column
+  // blocks; false where there is none. The tiles, walked expert by expert, eight
+  // column blocks at a time, over the expert's rows, are cut into eight equal
+  // runs, one for each XCD (workgroup b runs on XCD b % 8): an XCD's workgroups
+  // then share few experts' weights and few rows, whatever the numbers of rows
+  // and columns. (Column blocks dealt out to the XCDs instead, as for one weight
+  // block, leave XCDs idle where there are few of them.)
+  __device__ __forceinline__ bool find_tile(int b, int bm, int nblk, ExpertTile& out, int& nb) const {
+    const int lane = threadIdx.x & 63;
+    const int all = blocks(bm) * nblk, per = (all + 7) >> 3;
+    const int idx = b >> 3, tile = (b & 7) * per + idx;
+    if (idx >= per || tile >= all) return false;
+    int before = 0;  // tiles of the experts before e0
+    for (int e0 = 0; e0 < t.E; e0 += 64) {
+      const int e = e0 + lane;
+      const int a = min(max(t.offsets[min(e, t.E)], 0), t.R), z = min(max(t.offsets[min(e + 1, t.E)], 0), t.R);
+      const int n = (z > a ? (z - a + bm - 1) / bm : 0) * nblk;
+      int s = n;
+#pragma unroll
+      for (int x = 1; x < 64; x <<= 1) {
+        const int o = __shfl_up(s, x);
+        if (lane >= x) s += o;
+      }
+      const int total = __builtin_amdgcn_readlane(s, 63);
+      if (tile < before + total) {
+        const int at = __builtin_ctzll(__ballot(before + s > tile));
+        const int rows = __builtin_amdgcn_readlane(n, at) / nblk;
+        const int i = tile - before - (__builtin_amdgcn_readlane(s, at) - __builtin_amdgcn_readlane(n, at));
+        const int g = i / (8 * rows), rem = i - g * 8 * rows, cols = min(8, nblk - 8 * g);
+        const int mb = rem / cols;
+        nb = 8 * g + rem - mb * cols;
+        out.expert = e0 + at;
+        out.first = __builtin_amdgcn_readlane(a, at) + bm * mb;
+        out.end = min(__builtin_amdgcn_readlane(z, at), out.first + bm);
+        return true;
+      }
+      before += total;
+    }
+    return false;
+  }
+
   // (pair of row r: inside the tables whatever they say)
   __device__ __forceinline__ int pair(int r) const { return min(max(t.order[r], 0), t.R - 1); }
   __device__ __forceinline__ int source(int r) const { return GATHER ? pair(r) / t.k : r; }

@@ -89,7 +89,42 @@ __global__ __launch_bounds__(kThreads) void share_grad_kernel(ExpertRouting t, c
   }
 }
 
+// A wavefront per pair: its partial dots in order, and dy[m] . bias[e].
+__global__ __launch_bounds__(kThreads) void dots_kernel(ExpertRouting t, const float* __restrict__ dots, int count,
+                                                        const uint16_t* __restrict__ dy,
+                                                        const uint16_t* __restrict__ bias,
+                                                        float* __restrict__ dweights, int N) {
+  const int p = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (p >= t.R) return;
+  const int row = t.place[p], e = t.ids[p];
+  float dot = 0.0f;
+  if ((uint32_t)row < (uint32_t)t.R && (uint32_t)e < (uint32_t)t.E) {
+    for (int i = lane; i < count; i += 64) dot += dots[(size_t)i * t.R + row];
+    if (bias) {
+      for (int c = lane; c < N / 4; c += 64) {
+        const uint2 a = *(const uint2*)(dy + (size_t)(p / t.k) * N + 4 * c);
+        const uint2 b = *(const uint2*)(bias + (size_t)e * N + 4 * c);
+        dot = __builtin_fmaf(half_lo(a.x), half_lo(b.x), dot);
+        dot = __builtin_fmaf(half_hi(a.x), half_hi(b.x), dot);
+        dot = __builtin_fmaf(half_lo(a.y), half_lo(b.y), dot);
+        dot = __builtin_fmaf(half_hi(a.y), half_hi(b.y), dot);
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) dot += __shfl_xor(dot, s);
+  if (lane == 0) dweights[p] = dot;
+}
+
 }  // namespace
+
+hipError_t launch_experts_dots(const ExpertRouting& t, const float* dots, int count, const uint16_t* dy,
+                               const uint16_t* bias, float* dweights, int64_t N, hipStream_t stream) {
+  const unsigned per = kThreads / 64;
+  hipLaunchKernelGGL(dots_kernel, dim3(((unsigned)t.R + per - 1) / per), dim3(kThreads), 0, stream, t, dots, count, dy,
+                     bias, dweights, (int)N);
+  return hipGetLastError();
+}
 
 hipError_t launch_experts_sum(const ExpertRouting& t, const float* part, int splits, const uint16_t* residual,
                               uint16_t* y, int64_t N, hipStream_t stream) {

@@ -319,12 +319,29 @@ hipError_t launch_experts_route_backward(const void* logits, int type, int64_t M
 hipError_t launch_w4_experts_tiles(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                    const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                    int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
+// The same in 256 x 256 tiles (w4_experts_wide.hip), and whichever fits.
+hipError_t launch_w4_experts_wide(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
+                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
+hipError_t launch_w4_experts(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                             const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
+                             int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
 // part [splits][R][d] = dz W_hat of each row's expert, in pieces of the
 // contraction (w4_input_grad_rows.hip); gather: dz by token, else by row.
 int experts_grad_rows_splits(const ExpertRouting& t, int64_t P, int64_t d);
 hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, const uint16_t* dz,
                                        const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                                        float* part, int64_t P, int64_t d, int group, hipStream_t stream);
+// The same in large tiles for experts of many rows (w4_experts_grad.hip): part [R][d]
+// (dz by row), or dh = w U and the partial dots U . h (dy by token).
+bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P);
+size_t experts_grad_dots(const ExpertRouting& t, int64_t d);
+hipError_t launch_w4_experts_grad_part(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight,
+                                       const uint16_t* scales, const uint8_t* zeros, float* part, int64_t P, int64_t d,
+                                       int group, hipStream_t stream);
+hipError_t launch_w4_experts_grad_share(const ExpertRouting& t, const uint16_t* dy, const uint8_t* qweight,
+                                        const uint16_t* scales, const uint8_t* zeros, float* dots, const uint16_t* h,
+                                        uint16_t* dh, int64_t P, int64_t d, int group, hipStream_t stream);
 // Sums over a token's experts and the weights' gradients (experts_sum.hip):
 //   y[m] = residual[m] + sum_s sum_p part[p][place[m][s]]  (fp16 [M][N]);
 //   dh[r] = w U[r], dw[p] = U[r] . h[r] + dy[m] . bias[e], U = sum_p part[p].
@@ -333,6 +350,9 @@ hipError_t launch_experts_sum(const ExpertRouting& t, const float* part, int spl
 hipError_t launch_experts_share_grad(const ExpertRouting& t, const float* part, int splits, const uint16_t* h,
                                      const uint16_t* dy, const uint16_t* bias, uint16_t* dh, float* dweights,
                                      int64_t N, int64_t d, hipStream_t stream);
+//   dw[p] = the pair's partial dots [count][R] + dy[m] . bias[e]
+hipError_t launch_experts_dots(const ExpertRouting& t, const float* dots, int count, const uint16_t* dy,
+                               const uint16_t* bias, float* dweights, int64_t N, hipStream_t stream);
 
 // Distillation from a teacher's top logits (distill.hip).
 struct DistillArgs {

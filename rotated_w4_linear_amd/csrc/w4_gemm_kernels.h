@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "expert_rows.h"
 #include "paro_internal.h"
 #include "w4_common.h"
 #include "w4_epilogue.h"
@@ -534,15 +535,18 @@ __device__ __forceinline__ void sched_order() {
 // plus at most one partial tile at each end. The pieces of a partial tile
 // meet through fp32 partial tiles in the workspace; the last to arrive adds
 // them in k order and runs the epilogue.
-// EPI as for w4_gemm_kernel.
-template <int WN, bool PANEL, int MODE, int EPI>
+// EPI as for w4_gemm_kernel. ROWS: the tokens, or (kModeTile) the experts' rows: an
+// m-block then is a block of one expert's rows, by that expert's weights.
+template <int WN, bool PANEL, int MODE, int EPI, class ROWS = AllRows>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
 void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qw,
                          const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
                          const uint16_t* __restrict__ bias, uint16_t* y, int M, int N,
                          int d, int gsh, int mblk, int nblk, int slots, float* __restrict__ part,
-                         uint32_t* __restrict__ cnt, int sys, const uint16_t* aux, ActForm act, int erf) {
+                         uint32_t* __restrict__ cnt, int sys, const uint16_t* aux, ActForm act, int erf,
+                         ROWS rows_of) {
   constexpr bool GT = epi_gated(EPI);
+  static_assert(!ROWS::kExperts || MODE == kModeTile, "an expert's tile is one workgroup's");
   __shared__ __attribute__((aligned(1024))) _Float16 X0[GW_XSTAGE], X1[GW_XSTAGE], X2[GW_XSTAGE];
   __shared__ __attribute__((aligned(1024))) u4 W0[GB_WSTAGE], W1[GB_WSTAGE];
   __shared__ __attribute__((aligned(16))) uint32_t S0[GB_N], S1[GB_N], Z0[GB_N], Z1[GB_N];
@@ -559,7 +563,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   const int wn = w % NWAV, wm = w / NWAV;                   // the wavefront's n and m blocks
   // XCD-aware tile order, as in w4_gemm_kernel
   const int xcd = blockIdx.x & 7;
-  const int nbx = (nblk - xcd + 7) >> 3;
+  const int nbx = ROWS::kExperts ? 1 : (nblk - xcd + 7) >> 3;  // (experts: find_tile says where)
   if (nbx <= 0) return;
   const int groups = d >> (6 + gsh);
   const int L = d / GB_K;  // k-tiles per tile
@@ -577,22 +581,22 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
     return j;
   };
 
-  // One segment: k-tiles kt0 .. kt0 + KT - 1 (KT even) of tile (mb, nb), the
-  // XCD's tile tl; first: the workgroup's first segment
-  auto segment = [&](const int mb, const int nb, const int kt0, const int KT, const int tl, const bool first) {
+  // One segment: k-tiles kt0 .. kt0 + KT - 1 (KT even) of the tile at row m0 and
+  // n-block nb, the XCD's tile tl; first: the workgroup's first segment
+  auto segment = [&](const int m0, const int nb, const int kt0, const int KT, const int tl, const bool first) {
   // the lane index through an opaque copy, so that nothing derived from it is
   // hoisted out of the segment loop and held (spilled) across the k-loop
   int tid_o = tid_k;
   asm volatile("" : "+v"(tid_o));
   const int tid = tid_o, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
-  const int m0 = mb * GW_M;
   const int nw0 = nb * (GT ? GB_N / 2 : GB_N);
   const int pg0 = PANEL ? ((kt0 >> gsh) & ~7) : 0;  // first group of the panel
 
   // buffer resources at the tile's first row (byte offsets < 2^31: d <= 2^21,
   // checked on the host); rows past M or N are clamped to the last row
   const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(x + (size_t)m0 * d), (short)0, min(M - m0, GW_M) * d * 2, kRsrcWord3);
+      (void*)(x + (ROWS::kGather ? 0 : (size_t)m0 * d)), (short)0,
+      (ROWS::kGather ? rows_tokens(rows_of) : min(M - m0, GW_M)) * d * 2, kRsrcWord3);
   const int wrows = weight_rows<GT>(N, nw0, GB_N);
   const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(qw + (size_t)nw0 * (d >> 1)), (short)0, wrows * (d >> 1), kRsrcWord3);
@@ -605,7 +609,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const int r = 8 * (8 * w + c) + (lane >> 3);
-    const int row = min(r, M - 1 - m0);
+    const int row = source_row(rows_of, m0, min(r, M - 1 - m0));
     xoff[c] = (uint32_t)(row * d + 8 * ((lane & 7) ^ ((r >> 1) & 7))) * 2u;
   }
   // code DMA c (0..1) of wavefront w fills tile rows 32 (2 w + c) .. + 31
@@ -934,7 +938,24 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // w4_gemm_kernel
   const int n0 = nw0 + (GT ? 16 : 32) * WN * wn, mw0 = m0 + 32 * MTW * wm;
   uint8_t* stage = (uint8_t*)X0 + 8192 * w;
-  if constexpr (EPI != kEpiPlain) {
+  if constexpr (EPI == kEpiShare) {
+#pragma unroll
+    for (int mm = 0; mm < MTW; ++mm) {
+      const int m = mw0 + 32 * mm + l32;
+      if (m < M) {
+        const float share = rows_of.weight(m);
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = n0 + 32 * j + 8 * q + 4 * g;
+            if (n < N)
+              epi_share(f4{acc[j][mm][4 * q], acc[j][mm][4 * q + 1], acc[j][mm][4 * q + 2], acc[j][mm][4 * q + 3]},
+                        share, m, n, N, bias, (float*)y);
+          }
+      }
+    }
+  } else if constexpr (EPI != kEpiPlain) {
     // blocks of 64 tokens by two tiles, the second operand two blocks ahead
     constexpr int PS = MTW / 2, BLOCKS = WN / 2 * PS;
     u4 av[2][8];
@@ -1007,9 +1028,21 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
     // of 8 m-blocks, fewer misses at the same work)
     const int idx = blockIdx.x >> 3;
     const int mb = idx / nbx;
-    const int nb = xcd + 8 * (idx - mb * nbx);
-    if (mb >= mblk) return;
-    segment(mb, nb, 0, L, 0, true);
+    int nb = xcd + 8 * (idx - mb * nbx);
+    if (!ROWS::kExperts && mb >= mblk) return;
+    int m0 = mb * GW_M;
+    if constexpr (ROWS::kExperts) {
+      ExpertTile tile;
+      if (!rows_of.find_tile(blockIdx.x, GW_M, nblk, tile, nb)) return;
+      m0 = tile.first;
+      M = tile.end;
+      const size_t row0 = (size_t)tile.expert * (GT ? 2 * N : N);  // the expert's first weight row
+      qw += row0 * (size_t)(d >> 1);
+      sc += row0 * groups;
+      zr += row0 * groups;
+      if (bias) bias += row0;
+    }
+    segment(m0, nb, 0, L, 0, true);
   } else {
     // the XCD's tile t, its n-blocks walked in super-blocks of 8 m-blocks
     // (the last super-block may hold fewer)
@@ -1022,7 +1055,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
       const int sb = t / (8 * nbx);
       const int rows = min(8, mblk - 8 * sb);
       const int rem = t - sb * 8 * nbx;
-      segment(8 * sb + rem % rows, xcd + 8 * (rem / rows), (int)(u - (int64_t)t * L), (int)(ue - u), t, true);
+      segment(GW_M * (8 * sb + rem % rows), xcd + 8 * (rem / rows), (int)(u - (int64_t)t * L), (int)(ue - u), t, true);
     } else {
       while (u < ue) {
         const int t = (int)(u / L);
@@ -1031,7 +1064,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
         const int sb = t / (8 * nbx);
         const int rows = min(8, mblk - 8 * sb);
         const int rem = t - sb * 8 * nbx;
-        segment(8 * sb + rem % rows, xcd + 8 * (rem / rows), k0, k1 - k0, t, t == tfirst);
+        segment(GW_M * (8 * sb + rem % rows), xcd + 8 * (rem / rows), k0, k1 - k0, t, t == tfirst);
         u += k1 - k0;
         if (u < ue) {
           // the epilogue's LDS reads before the next segment's DMA and panel
@@ -1121,7 +1154,7 @@ hipError_t launch_w4_gemm_epi(const uint16_t* x, const uint8_t* qweight, const u
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)bw), dim3(256), 0, stream, x, qweight, scales, zeros, bias, y,
                          (int)M, (int)N, (int)d, gsh, mblkw, nblk256, plan.sk_slots, part, cnt, sys, ep.aux, act_form(ep.act),
-                         ep.act == PARO_ACT_GELU);
+                         ep.act == PARO_ACT_GELU, AllRows{});
     };
     if (plan.sk && one_tile) {
       if (panel) go(w4_gemm_wide_kernel<kWideWN, true, kModeSkOne, EPI>);
@@ -1152,6 +1185,28 @@ hipError_t launch_w4_gemm_epi(const uint16_t* x, const uint8_t* qweight, const u
   else if (half) launch_gemm<1, 2, 2, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
   else if (ks2) launch_gemm<2, 4, 2, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
   else launch_gemm<1, 4, 2, EPI>(g, stream, x, qweight, scales, zeros, bias, y, M, N, d, gsh, mblk, nblk, mmaj, ep);
+  return hipGetLastError();
+}
+
+// The experts' product in 256 x 256 tiles, one per workgroup; y as for
+// launch_w4_experts_tiles. d >= 256 (two k-tiles at a time, four at least).
+template <int EPI, bool GATHER>
+hipError_t launch_w4_experts_wide_epi(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                                      const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
+                                      int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
+  const int64_t P = epi_gated(EPI) ? 2 * N : N;
+  const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
+  const int64_t groups = d >> (6 + gsh);
+  const int nblk = (int)((P + GB_N - 1) / GB_N), mblk = (int)expert_blocks(t, GW_M);
+  // (an expert's scales and zeros start at a multiple of 16 rows' groups)
+  const bool panel = groups <= kPanelGroups && groups % 8 == 0;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(((unsigned)nblk * (unsigned)mblk + 7) / 8 * 8), dim3(256), 0, stream, x, qweight,
+                       scales, zeros, bias, (uint16_t*)y, t.R, (int)N, (int)d, gsh, mblk, nblk, 0, nullptr, nullptr, 0,
+                       ep.aux, act_form(ep.act), (int)(ep.act == PARO_ACT_GELU), ExpertRows<GATHER>{t});
+  };
+  if (panel) go(w4_gemm_wide_kernel<kWideWN, true, kModeTile, EPI, ExpertRows<GATHER>>);
+  else go(w4_gemm_wide_kernel<kWideWN, false, kModeTile, EPI, ExpertRows<GATHER>>);
   return hipGetLastError();
 }
 

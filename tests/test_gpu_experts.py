@@ -171,6 +171,8 @@ PRODUCTS = [
     (33, 3, 2, 528, 512, 128, 0.0), (64, 64, 8, 64, 512, 64, 0.1), (100, 8, 2, 208, 2560, 128, 0.0),
     (130, 100, 4, 48, 384, 128, 0.5), (200, 2, 1, 1040, 1024, 64, 0.0), (333, 16, 3, 336, 896, 128, 0.1),
     (700, 4, 2, 272, 512, 256, 0.0), (1500, 8, 2, 288, 256, 64, 0.05), (2500, 3, 1, 528, 384, 128, 0.0),
+    (300, 2, 2, 64, 128, 128, 0.0), (400, 3, 1, 80, 256, 64, 0.2), (260, 1, 1, 48, 256, 256, 0.0),
+    (150, 2, 2, 160, 640, 128, 0.0), (1200, 40, 6, 96, 384, 128, 0.0),
 ]
 
 
