@@ -61,7 +61,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   constexpr int BM = 64 * TM, CB = BM / 32, NF = 4 * TM;
   __shared__ __attribute__((aligned(1024))) _Float16 A0[kN * kK], A1[kN * kK];
   __shared__ __attribute__((aligned(1024))) _Float16 B0[BM * kK], B1[BM * kK];
-  __shared__ __attribute__((aligned(16))) uint2 T0[4 * kK], T1[4 * kK];
+  __shared__ __attribute__((aligned(16))) uint32_t T0[4 * kK], T1[4 * kK];
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = w & 1, wm = w >> 1;
@@ -71,8 +71,6 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   const int n0 = kN * nb, m0 = tile.first, rows = tile.end - tile.first;
   const int groups = d >> (6 + gsh), half = d >> 1;
   const size_t first = (size_t)tile.expert * P;  // the expert's first weight row
-  sc += first * groups;
-  zr += first * groups;
   const int KT = (P + kK - 1) / kK;
   const __amdgpu_buffer_rsrc_t rw =
       __builtin_amdgcn_make_buffer_rsrc((void*)(qw + first * half), (short)0, P * half, kRsrcWord3);
@@ -90,8 +88,8 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
     const int r = 8 * (CB * w + c) + (lane >> 3);
     boff[c] = (uint32_t)(source_row(rows_of, m0, min(r, rows - 1)) * P + 8 * ((lane & 7) ^ ((r >> 1) & 7))) * 2u;
   }
-  auto dma_b = [&](int kt, _Float16* bs) {
-    const int at = row0(kt) * 2;
+  auto dma_b = [&](int row, _Float16* bs) {
+    const int at = row * 2;
 #pragma unroll
     for (int c = 0; c < CB; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)&bs[(CB * w + c) * 512], 16, boff[c], at, 0, 0);
@@ -99,54 +97,65 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
 
   // codes: rows 8 pr .. + 7 of the k-tile, channels n0 + 8 cb .. + 7
   const int pr = tid >> 5, cb = tid & 31;
-  const uint32_t coff = (uint32_t)(8 * pr * half + (n0 >> 1) + 4 * cb);
+  uint32_t coff[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) coff[i] = (uint32_t)((8 * pr + i) * half + (n0 >> 1) + 4 * cb);
   struct Codes {
     uint32_t c[8];
   };
-  auto load_codes = [&](int kt, Codes& q) {
-    const int at = row0(kt) * half;
+  auto load_codes = [&](int at, Codes& q) {  // at: the k-tile's first row, in bytes
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q.c[i] = __builtin_amdgcn_raw_buffer_load_b32(rw, coff, at + i * half, 0);
+    for (int i = 0; i < 8; ++i) q.c[i] = __builtin_amdgcn_raw_buffer_load_b32(rw, coff[i], at, 0);
   };
   // scale and zero: thread t has row t % 64 and group t / 64 of the channels
   // (those past the last group: the last one's, never used)
   const int trow = tid & 63, tgi = min((n0 >> (6 + gsh)) + (tid >> 6), groups - 1);
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(sc + first * groups), (short)0, P * groups * 2, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rz =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(zr + first * groups), (short)0, P * groups, kRsrcWord3);
+  const uint32_t zoff = (uint32_t)(trow * groups + tgi);
   struct Scale {
     uint32_t s, z;
-    bool done;
   };
-  auto load_scale = [&](int kt, Scale& q) {
-    const size_t at = (size_t)(row0(kt) + trow) * groups + tgi;
-    q.s = sc[at];
-    q.z = zr[at];
-    q.done = kt >= KT - 1 && row0(kt) + trow < kK * (KT - 1);
+  auto load_scale = [&](int at, Scale& q) {  // at: the k-tile's first row, in groups
+    q.s = __builtin_amdgcn_raw_buffer_load_b16(rs, 2 * zoff, 2 * at, 0);
+    q.z = __builtin_amdgcn_raw_buffer_load_b8(rz, zoff, at, 0);
   };
-  // scale | 0, 1024 + z | 64 + z
-  auto put_scale = [&](const Scale& q, uint2* t) {
-    const float zf = (float)q.z;
-    const h2 b = {(_Float16)(1024.0f + zf), (_Float16)(64.0f + zf)};
-    t[tid] = make_uint2(q.done ? 0u : q.s, __builtin_bit_cast(uint32_t, b));
+  // scale | 1024 + z; the k-tile's first `done` rows: 0 | 1024 + z (chosen here:
+  // beside the loads, the compiler waits for them there, a k-tile before)
+  auto put_scale = [&](int done, const Scale& q, uint32_t* t) {
+    t[tid] = (trow < done ? 0u : q.s & 0xffffu) | half_bits(1024.0f + (float)(q.z & 0xffu)) << 16;
+  };
+  auto done_rows = [&](int kt) { return kt >= KT - 1 ? kK * KT - P : 0; };
+  struct Rows {  // of a thread's eight rows: scale | 1024 + z
+    u4 v[2];
   };
 
   const uint32_t one = fp16_1024_pair();
-  const h2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+  const h2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f}, less = {(_Float16)960.0f, (_Float16)960.0f};
   const int tgroup = kK * (cb >> (3 + gsh)) + 8 * pr;
+  auto get_scales = [&](const uint32_t* t, Rows& r) {
+    r.v[0] = *(const u4*)(t + tgroup);
+    r.v[1] = *(const u4*)(t + tgroup + 4);
+  };
   // fragment of channel 8 cb + e: row arow + 32 (e / 2) + 16 (e % 2), chunk pr
   const int arow = 128 * (cb >> 4) + (cb & 15);
   const int achunk = 8 * (pr ^ ((cb & 15) >> 1));
   // channels 2 j and 2 j + 1
-  auto fragments = [&](const Codes& q, const uint2* t, int j, _Float16* as) {
+  auto fragments = [&](const Codes& q, const Rows& t, int j, _Float16* as) {
     uint32_t v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint2 sz = t[tgroup + i];
-      const h2 s = __builtin_bit_cast(h2, sz.x), z = __builtin_bit_cast(h2, sz.y);
+      const uint32_t word = t.v[i >> 2][i & 3];
+      const h2 sz = __builtin_bit_cast(h2, word);
       const uint32_t c = j < 2 ? q.c[i] : q.c[i] >> 8;
       h2 x;
-      if (j % 2 == 0) x = __builtin_bit_cast(h2, (c & 0x000F000Fu) | one) - splat2(z[0]);
-      else x = __builtin_elementwise_fma(__builtin_bit_cast(h2, (c & 0x00F000F0u) | one), sixteenth, -splat2(z[1]));
-      v[i] = __builtin_bit_cast(uint32_t, x * splat2(s[0]));
+      if (j % 2 == 0)
+        x = __builtin_bit_cast(h2, (c & 0x000F000Fu) | one) - splat2(sz[1]);
+      else  // (64 + z is exact)
+        x = __builtin_elementwise_fma(__builtin_bit_cast(h2, (c & 0x00F000F0u) | one), sixteenth, less - splat2(sz[1]));
+      v[i] = __builtin_bit_cast(uint32_t, x * splat2(sz[0]));
     }
     u4 lo, hi;
 #pragma unroll
@@ -186,13 +195,13 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
 #pragma unroll
     for (int f = 0; f < NF; ++f)
       acc[f / TM][f % TM] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[f / TM], b[f % TM], acc[f / TM][f % TM], 0, 0, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 4 + TM + (NW > 0 ? 4 : 0), 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 4 + TM + (NL == 10 ? 2 : 0), 0);
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (NV > 0) __builtin_amdgcn_sched_group_barrier(0x002, (NV + NF - 1) / NF, 0);
       if (f < NL) {
-        __builtin_amdgcn_sched_group_barrier(0x004, 2, 0);  // a load's scalar operands
+        __builtin_amdgcn_sched_group_barrier(0x004, NW > 0 ? 1 : 2, 0);  // a DMA's scalar operands
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       }
       if (NW > 0 && f % (NF / 2) == NF / 2 - 1) __builtin_amdgcn_sched_group_barrier(0x200, NW / 2, 0);
@@ -215,25 +224,35 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
     __builtin_amdgcn_sched_barrier(0);
   };
   Scale szr;
+  // where k-tile kt + 2 starts, and kt + 3's scales: made in the step before
+  struct Ahead {
+    int row, codes, scales, done;
+  };
+  auto ahead = [&](int kt) { return Ahead{row0(kt + 2), row0(kt + 2) * half, row0(kt + 3) * groups, done_rows(kt + 2)}; };
+  Ahead at = ahead(0);
   // k-tile kt in (as, bs), kt + 1's dz in bs1 and its codes in q1; fragments of
   // kt + 1 go to as1, scales of kt + 2 to the table of kt (t), codes of kt + 2 to q
-  auto ktile = [&](int kt, const _Float16* as, _Float16* bs, uint2* t, Codes& q, _Float16* as1, const _Float16* bs1,
-                   const uint2* t1, const Codes& q1) {
-    put_scale(szr, t);
-    load_codes(kt + 2, q);
-    load_scale(kt + 3, szr);
+  auto ktile = [&](int kt, const _Float16* as, _Float16* bs, uint32_t* t, Codes& q, _Float16* as1, const _Float16* bs1,
+                   const uint32_t* t1, const Codes& q1) {
+    Rows r1;
+    get_scales(t1, r1);
+    put_scale(at.done, szr, t);
+    load_codes(at.codes, q);
+    load_scale(at.scales, szr);
     read(as, bs, 1, an, bn);
-    fragments(q1, t1, 0, as1);
-    fragments(q1, t1, 1, as1);
+    fragments(q1, r1, 0, as1);
+    fragments(q1, r1, 1, as1);
     step(std::integral_constant<int, 80>{}, std::integral_constant<int, 10>{}, std::integral_constant<int, 4>{});
     read(as, bs, 2, an, bn);
-    fragments(q1, t1, 2, as1);
-    fragments(q1, t1, 3, as1);
+    fragments(q1, r1, 2, as1);
+    fragments(q1, r1, 3, as1);
     step(std::integral_constant<int, 80>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 4>{});
     read(as, bs, 3, an, bn);
+    const int row = at.row;
+    at = ahead(kt + 1);
     step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
     meet(1);  // still on their way: the codes of kt + 2, the scale and zero of kt + 3
-    dma_b(kt + 2, bs);
+    dma_b(row, bs);
     read(as1, bs1, 0, an, bn);
     step(std::integral_constant<int, 0>{}, std::integral_constant<int, CB>{}, std::integral_constant<int, 0>{});
   };
@@ -241,18 +260,20 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   Codes q0, q1;
   {
     Scale s0, s1;
-    dma_b(0, B0);
-    dma_b(1, B1);
-    load_scale(0, s0);
-    load_scale(1, s1);
-    load_codes(0, q0);
-    load_codes(1, q1);
-    load_scale(2, szr);
-    put_scale(s0, T0);
-    put_scale(s1, T1);
+    dma_b(row0(0), B0);
+    dma_b(row0(1), B1);
+    load_scale(row0(0) * groups, s0);
+    load_scale(row0(1) * groups, s1);
+    load_codes(row0(0) * half, q0);
+    load_codes(row0(1) * half, q1);
+    load_scale(row0(2) * groups, szr);
+    put_scale(done_rows(0), s0, T0);
+    put_scale(done_rows(1), s1, T1);
     __syncthreads();
+    Rows r0;
+    get_scales(T0, r0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fragments(q0, T0, j, A0);
+    for (int j = 0; j < 4; ++j) fragments(q0, r0, j, A0);
     meet(0);
     read(A0, B0, 0, a, b);
   }
