@@ -19,16 +19,19 @@
 // (4 x TM accumulator tiles of v_mfma_f32_32x32x16_f16). dz comes by load-to-LDS
 // DMA, two stages; fragments into two stages as well:
 //  * fragments [256][64 p]: channel 8 c + e of the tile at row 128 (c / 16) + 32
-//    (e / 2) + 16 (e % 2) + c % 16, chunk q of 8 p at q ^ ((row >> 1) & 7). The 16
-//    lanes of a write have 16 consecutive rows, and so do those of a read: each
-//    touches every bank once. And a lane's accumulators hold all eight channels of
-//    c, so that it stores them as they are;
-//  * dz [64 TM rows][64 p], chunks likewise;
+//    (e / 2) + 16 (e % 2) + c % 16, chunk q of 8 p at q ^ (row % 8) ^ (row / 8 % 2).
+//    Reads and writes go over consecutive rows; 8 of them (a write's pace) lie in 8
+//    places modulo 128 bytes, 16 (a read's) in 16 modulo 256. And a lane's
+//    accumulators hold all eight channels of c, so that it stores them as they are;
+//  * dz [64 TM rows][64 p], chunk q at q ^ ((row >> 1) & 7);
 //  * scales and zeros of the k-tile's rows [4 groups][64], in the forms that the
 //    dequantization takes.
-// While k-tile kt is multiplied, the fragments of kt + 1 are made from codes that
-// were loaded a k-tile before, the codes of kt + 2 and the scales of kt + 3 are on
-// their way, and dz of kt + 2 goes out as soon as nobody reads kt's any more.
+// A k-tile is four steps of 16 p. In steps 0 and 1 of k-tile kt the fragments of kt
+// + 1 are made, from codes that were loaded a k-tile before; after step 2 the
+// wavefronts meet, nobody reads the stages of kt any more, and step 3 sends dz of kt
+// + 2. (A quarter of the fragments in every step, the first ones of kt + 2 and the
+// loads of codes in step 3 beside dz: 631 -> 645 us for 2048 tokens, 2 of 8 experts
+// 14336 -> 4096.)
 // P is a multiple of 16, k-tiles of 64: the last one is the 64 rows at the end,
 // with scale 0 for those that the one before has done already.
 #include <algorithm>
@@ -49,6 +52,9 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
 constexpr int kN = 256, kK = 64;        // channels per workgroup, k-tile
+
+// Which chunk of fragment row r takes chunk q's place: q ^ aswap(r).
+__device__ __forceinline__ int aswap(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 // SHARE: dh[r] = w U[r] (fp16) and dots[2 nb + half][r], the sums over 128
 // channels of U[r] h[r]; else part[r] = U[r] (fp32).
@@ -141,7 +147,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   };
   // fragment of channel 8 cb + e: row arow + 32 (e / 2) + 16 (e % 2), chunk pr
   const int arow = 128 * (cb >> 4) + (cb & 15);
-  const int achunk = 8 * (pr ^ ((cb & 15) >> 1));
+  const int achunk = 8 * (pr ^ aswap(cb));
   // channels 2 j and 2 j + 1
   auto fragments = [&](const Codes& q, const Rows& t, int j, _Float16* as) {
     uint32_t v[8];
@@ -179,7 +185,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = 32 * (4 * wn + j) + l32;
-      a[j] = *(const h8*)(as + r * kK + 8 * ((4 * g + s) ^ ((r >> 1) & 7)));
+      a[j] = *(const h8*)(as + r * kK + 8 * ((4 * g + s) ^ aswap(r)));
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -188,23 +194,24 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
     }
   };
   h8 a[4], b[4], an[4], bn[4];
-  // a step's MFMAs on the operands in hand, behind the next step's reads; NV
-  // vector instructions, NL loads and two LDS writes out of NW spread among them
-  auto step = [&](auto nv, auto nl, auto nw) {
-    constexpr int NV = decltype(nv)::value, NL = decltype(nl)::value, NW = decltype(nw)::value;
+  // a step's MFMAs on the operands in hand, among them the next step's reads, NV
+  // vector instructions, NL loads and the LDS writes of two fragments
+  auto step = [&](auto nv, auto nl) {
+    constexpr int NV = decltype(nv)::value, NL = decltype(nl)::value;
 #pragma unroll
     for (int f = 0; f < NF; ++f)
       acc[f / TM][f % TM] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[f / TM], b[f % TM], acc[f / TM][f % TM], 0, 0, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 4 + TM + (NL == 10 ? 2 : 0), 0);
+    if (NL == 10) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // the scales
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (f < 4 + TM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       if (NV > 0) __builtin_amdgcn_sched_group_barrier(0x002, (NV + NF - 1) / NF, 0);
       if (f < NL) {
-        __builtin_amdgcn_sched_group_barrier(0x004, NW > 0 ? 1 : 2, 0);  // a DMA's scalar operands
+        __builtin_amdgcn_sched_group_barrier(0x004, NV > 0 ? 1 : 2, 0);  // a load's scalar operands
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       }
-      if (NW > 0 && f % (NF / 2) == NF / 2 - 1) __builtin_amdgcn_sched_group_barrier(0x200, NW / 2, 0);
+      if (NV > 0 && f % (NF / 2) == NF / 2 - 1) __builtin_amdgcn_sched_group_barrier(0x200, 2, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -228,7 +235,9 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   struct Ahead {
     int row, codes, scales, done;
   };
-  auto ahead = [&](int kt) { return Ahead{row0(kt + 2), row0(kt + 2) * half, row0(kt + 3) * groups, done_rows(kt + 2)}; };
+  auto ahead = [&](int kt) {
+    return Ahead{row0(kt + 2), row0(kt + 2) * half, row0(kt + 3) * groups, done_rows(kt + 2)};
+  };
   Ahead at = ahead(0);
   // k-tile kt in (as, bs), kt + 1's dz in bs1 and its codes in q1; fragments of
   // kt + 1 go to as1, scales of kt + 2 to the table of kt (t), codes of kt + 2 to q
@@ -242,19 +251,19 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
     read(as, bs, 1, an, bn);
     fragments(q1, r1, 0, as1);
     fragments(q1, r1, 1, as1);
-    step(std::integral_constant<int, 80>{}, std::integral_constant<int, 10>{}, std::integral_constant<int, 4>{});
+    step(std::integral_constant<int, 80>{}, std::integral_constant<int, 10>{});
     read(as, bs, 2, an, bn);
     fragments(q1, r1, 2, as1);
     fragments(q1, r1, 3, as1);
-    step(std::integral_constant<int, 80>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 4>{});
+    step(std::integral_constant<int, 80>{}, std::integral_constant<int, 0>{});
     read(as, bs, 3, an, bn);
     const int row = at.row;
     at = ahead(kt + 1);
-    step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
     meet(1);  // still on their way: the codes of kt + 2, the scale and zero of kt + 3
     dma_b(row, bs);
     read(as1, bs1, 0, an, bn);
-    step(std::integral_constant<int, 0>{}, std::integral_constant<int, CB>{}, std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 0>{}, std::integral_constant<int, CB>{});
   };
 
   Codes q0, q1;
@@ -287,6 +296,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
 
   // acc[j][i][4 q + c] = U[m0 + 32 (TM wm + i) + l32][channel 8 (16 (nb 2 + wn) + 8 (q % 2) + 4 g + c) + 2 j + q / 2]
   const int nw0 = n0 + 128 * wn;
+  auto channel = [&](int x) { return nw0 + 8 * (8 * (x >> 2) + 4 * g + (x & 3)); };
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int m = m0 + 32 * (TM * wm + i) + l32;
@@ -296,7 +306,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
         const float share = rows_of.weight(m);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int qb = x >> 2, c = x & 3, ch = nw0 + 8 * (8 * qb + 4 * g + c);
+          const int qb = x >> 2, c = x & 3, ch = channel(x);
           if (ch < d) {
             const u4 hv = *(const u4*)(h + (size_t)m * d + ch);
             u4 o;
@@ -318,7 +328,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
       if (m < tile.end) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int qb = x >> 2, c = x & 3, ch = nw0 + 8 * (8 * qb + 4 * g + c);
+          const int qb = x >> 2, c = x & 3, ch = channel(x);
           if (ch < d) {
             float* o = part + (size_t)m * d + ch;
 #pragma unroll
