@@ -51,7 +51,7 @@ using namespace w4;
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
-constexpr int kN = 256, kK = 64;        // channels per workgroup, k-tile
+constexpr int kN = 256, kM = 256, kK = 64;  // channels and rows per workgroup, k-tile
 
 // Which chunk of fragment row r takes chunk q's place: q ^ aswap(r).
 __device__ __forceinline__ int aswap(int r) { return (r & 7) ^ ((r >> 3) & 1); }
@@ -59,21 +59,17 @@ __device__ __forceinline__ int aswap(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 // SHARE: dh[r] = w U[r] (fp16) and dots[2 nb + half][r], the sums over 128
 // channels of U[r] h[r]; else part[r] = U[r] (fp32).
 template <int TM, bool GATHER, bool SHARE>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
-void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__ qw, const uint16_t* __restrict__ sc,
-                         const uint8_t* __restrict__ zr, const uint16_t* __restrict__ dz, int P, int d, int gsh,
-                         int nblk, float* __restrict__ part, const uint16_t* __restrict__ h,
-                         uint16_t* __restrict__ dh) {
+__device__ __forceinline__ void grad_tile(const ExpertRows<GATHER>& rows_of, const ExpertTile& tile, const int nb,
+                                          _Float16* A0, _Float16* A1, _Float16* B0, _Float16* B1, uint32_t* T0,
+                                          uint32_t* T1, const uint8_t* __restrict__ qw,
+                                          const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
+                                          const uint16_t* __restrict__ dz, const int P, const int d, const int gsh,
+                                          float* __restrict__ part, const uint16_t* __restrict__ h,
+                                          uint16_t* __restrict__ dh) {
   constexpr int BM = 64 * TM, CB = BM / 32, NF = 4 * TM;
-  __shared__ __attribute__((aligned(1024))) _Float16 A0[kN * kK], A1[kN * kK];
-  __shared__ __attribute__((aligned(1024))) _Float16 B0[BM * kK], B1[BM * kK];
-  __shared__ __attribute__((aligned(16))) uint32_t T0[4 * kK], T1[4 * kK];
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = w & 1, wm = w >> 1;
-  ExpertTile tile;
-  int nb;
-  if (!rows_of.find_tile(blockIdx.x, BM, nblk, tile, nb)) return;
   const int n0 = kN * nb, m0 = tile.first, rows = tile.end - tile.first;
   const int groups = d >> (6 + gsh), half = d >> 1;
   const size_t first = (size_t)tile.expert * P;  // the expert's first weight row
@@ -342,14 +338,33 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   }
 }
 
-template <int TM, bool GATHER, bool SHARE>
+// Tiles of up to 256 rows. An expert's last one may be short: up to 128 rows in
+// wavefront tiles of half the height, which take 0.6 of a whole tile's time.
+template <bool GATHER, bool SHARE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
+void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__ qw, const uint16_t* __restrict__ sc,
+                         const uint8_t* __restrict__ zr, const uint16_t* __restrict__ dz, int P, int d, int gsh,
+                         int nblk, float* __restrict__ part, const uint16_t* __restrict__ h,
+                         uint16_t* __restrict__ dh) {
+  __shared__ __attribute__((aligned(1024))) _Float16 A0[kN * kK], A1[kN * kK], B0[kM * kK], B1[kM * kK];
+  __shared__ __attribute__((aligned(16))) uint32_t T0[4 * kK], T1[4 * kK];
+  ExpertTile tile;
+  int nb;
+  if (!rows_of.find_tile(blockIdx.x, kM, nblk, tile, nb)) return;
+  if (tile.end - tile.first > kM / 2)
+    grad_tile<4, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, d, gsh, part, h, dh);
+  else
+    grad_tile<2, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, d, gsh, part, h, dh);
+}
+
+template <bool GATHER, bool SHARE>
 hipError_t launch(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
                   const uint8_t* zeros, int64_t P, int64_t d, int group, float* part, const uint16_t* h, uint16_t* dh,
                   hipStream_t stream) {
   const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
   const unsigned nblk = (unsigned)((d + kN - 1) / kN);
-  const unsigned tiles = nblk * (unsigned)expert_blocks(t, 64 * TM);
-  hipLaunchKernelGGL((experts_grad_kernel<TM, GATHER, SHARE>), dim3((tiles + 7) / 8 * 8), dim3(256), 0, stream,
+  const unsigned tiles = nblk * (unsigned)expert_blocks(t, kM);
+  hipLaunchKernelGGL((experts_grad_kernel<GATHER, SHARE>), dim3((tiles + 7) / 8 * 8), dim3(256), 0, stream,
                      ExpertRows<GATHER>{t}, qweight, scales, zeros, dz, (int)P, (int)d, gsh, (int)nblk, part, h, dh);
   return hipGetLastError();
 }
@@ -365,13 +380,13 @@ size_t experts_grad_dots(const ExpertRouting& t, int64_t d) { return (size_t)((d
 hipError_t launch_w4_experts_grad_part(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight,
                                        const uint16_t* scales, const uint8_t* zeros, float* part, int64_t P, int64_t d,
                                        int group, hipStream_t stream) {
-  return launch<4, false, false>(t, dz, qweight, scales, zeros, P, d, group, part, nullptr, nullptr, stream);
+  return launch<false, false>(t, dz, qweight, scales, zeros, P, d, group, part, nullptr, nullptr, stream);
 }
 
 hipError_t launch_w4_experts_grad_share(const ExpertRouting& t, const uint16_t* dy, const uint8_t* qweight,
                                         const uint16_t* scales, const uint8_t* zeros, float* dots, const uint16_t* h,
                                         uint16_t* dh, int64_t P, int64_t d, int group, hipStream_t stream) {
-  return launch<4, true, true>(t, dy, qweight, scales, zeros, P, d, group, dots, h, dh, stream);
+  return launch<true, true>(t, dy, qweight, scales, zeros, P, d, group, dots, h, dh, stream);
 }
 
 }  // namespace paro

@@ -75,6 +75,8 @@ constexpr int kAuxSysW = 17;
 constexpr int kWaitVmLgkm0 = 0x70;
 // vmcnt(8) lgkmcnt(0)
 constexpr int kWaitVm8Lgkm0 = 0x78;
+// vmcnt(4) lgkmcnt(0)
+constexpr int kWaitVm4Lgkm0 = 0x74;
 // lgkmcnt(0) alone (vmcnt and expcnt at their maxima)
 constexpr int kWaitLgkm0 = 0xC07F;
 // Output tiles (at 128 tokens) below which 64-token tiles are used: measured
@@ -492,14 +494,14 @@ constexpr int kModeTile = 0, kModeSkOne = 1, kModeSkMany = 2;
 // dequantization); NG global loads (part of a k-tile's DMA) are spread evenly
 // among the MFMAs, so that issuing the loads, which holds the wavefront's
 // in-order issue, overlaps running MFMAs.
-// One chunk of four MFMAs: the chunk's ND LDS reads first, then each MFMA
+// One chunk of NM = 4 MFMAs: the chunk's ND LDS reads first, then each MFMA
 // followed by up to NV vector instructions and, for the first NG, one global
 // load with the scalar write of its LDS address (M0) before it.
-template <int ND, int NV, int NG>
+template <int ND, int NV, int NG, int NM = 4>
 __device__ __forceinline__ void sched_chunk() {
   if constexpr (ND > 0) __builtin_amdgcn_sched_group_barrier(0x100, ND, 0);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < NM; ++k) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if constexpr (NV > 0) __builtin_amdgcn_sched_group_barrier(0x002, NV, 0);
     if (k < NG) {
@@ -509,14 +511,14 @@ __device__ __forceinline__ void sched_chunk() {
   }
 }
 
-template <int ND, int NW, int NV, int NG>
+template <int ND, int NW, int NV, int NG, int NM = 16>
 __device__ __forceinline__ void sched_order() {
   __builtin_amdgcn_sched_group_barrier(0x100, ND, 0);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
+  for (int k = 0; k < NM; ++k) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if (k >= NW) __builtin_amdgcn_sched_group_barrier(0x002, NV, 0);
-    if (NG > 0 && k % (16 / (NG > 0 ? NG : 1)) == 0) {
+    if (NG > 0 && k % (NM / (NG > 0 ? NG : 1)) == 0) {
       __builtin_amdgcn_sched_group_barrier(0x004, 1, 0);  // the load's M0 write
       __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
@@ -559,7 +561,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   constexpr bool SK = MODE != kModeTile;
   const int tid_k = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid_k >> 6);  // wavefront 0..3
-  constexpr int MTW = 16 / WN, NWAV = 8 / WN;               // m tiles; wavefronts along n
+  constexpr int NWAV = 8 / WN;                              // wavefronts along n
   const int wn = w % NWAV, wm = w / NWAV;                   // the wavefront's n and m blocks
   // XCD-aware tile order, as in w4_gemm_kernel
   const int xcd = blockIdx.x & 7;
@@ -582,8 +584,11 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   };
 
   // One segment: k-tiles kt0 .. kt0 + KT - 1 (KT even) of the tile at row m0 and
-  // n-block nb, the XCD's tile tl; first: the workgroup's first segment
-  auto segment = [&](const int m0, const int nb, const int kt0, const int KT, const int tl, const bool first) {
+  // n-block nb, the XCD's tile tl; first: the workgroup's first segment. The tile
+  // has 256 rows, or half as many (H2, for an expert's last rows).
+  auto segment = [&](auto h2_, const int m0, const int nb, const int kt0, const int KT, const int tl, const bool first) {
+  constexpr int H2 = decltype(h2_)::value ? 2 : 1;
+  constexpr int MTW = 16 / WN / H2, XD = 8 / H2;  // m tiles; X' DMAs per lane and k-tile
   // the lane index through an opaque copy, so that nothing derived from it is
   // hoisted out of the segment loop and held (spilled) across the k-loop
   int tid_o = tid_k;
@@ -607,8 +612,8 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // X' DMA c (0..7) of wavefront w fills tile rows 8 (8 w + c) .. + 7
   uint32_t xoff[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const int r = 8 * (8 * w + c) + (lane >> 3);
+  for (int c = 0; c < XD; ++c) {
+    const int r = 8 * (XD * w + c) + (lane >> 3);
     const int row = source_row(rows_of, m0, min(r, M - 1 - m0));
     xoff[c] = (uint32_t)(row * d + 8 * ((lane & 7) ^ ((r >> 1) & 7))) * 2u;
   }
@@ -628,8 +633,8 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   // and zeros (two more)
   auto dma_x = [&](int half, int ktl, _Float16* xs) {
 #pragma unroll
-    for (int c = 4 * half; c < 4 * half + 4; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)&xs[(8 * w + c) * 64 * 8], 16, xoff[c],
+    for (int c = XD / 2 * half; c < XD / 2 * (half + 1); ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)&xs[(XD * w + c) * 64 * 8], 16, xoff[c],
                                                (kt0 + ktl) * GB_K * 2, 0, 0);
   };
   auto dma_w = [&](int ktl, u4* ws, uint32_t* ss_l, uint32_t* zs_l) {
@@ -717,10 +722,11 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
       for (int mm = 0; mm < MTW; ++mm)
         acc[j][mm] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[j], bf[mm], acc[j][mm], 0, 0, 0);
   };
-  // MFMAs 4 q .. 4 q + 3 of the 16 of one step (j major)
+  // the q-th quarter of the MFMAs of one step (j major)
+  constexpr int Q4 = WN * MTW / 4;
   auto mma4 = [&](int q, const h8* af, const h8* bf) {
 #pragma unroll
-    for (int f = 4 * q; f < 4 * q + 4; ++f)
+    for (int f = Q4 * q; f < Q4 * (q + 1); ++f)
       acc[f / MTW][f % MTW] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[f / MTW], bf[f % MTW], acc[f / MTW][f % MTW], 0, 0, 0);
   };
   // Pipeline: while the MFMAs of step i of k-tile kt run, the wavefront reads
@@ -746,8 +752,8 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
       read_b(xb, i + 1, bn);
       deq(P, i + 1, an);
       mma(a, b);
-      if (i < 2) sched_order<MTW, 0, WN + 1, 4>();
-      else sched_order<MTW, 0, WN + 1, 0>();
+      if (i < 2) sched_order<MTW, 0, H2 * WN + 1, XD / 2, 4 * Q4>();
+      else sched_order<MTW, 0, H2 * WN + 1, 0, 4 * Q4>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
@@ -755,7 +761,8 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
         if (t < MTW) b[t] = bn[t];
       }
     }
-    __builtin_amdgcn_s_waitcnt(kWaitVm8Lgkm0);  // still on their way: the X' rows of kt + 2
+    // still on their way: the X' rows of kt + 2
+    __builtin_amdgcn_s_waitcnt(H2 == 1 ? kWaitVm8Lgkm0 : kWaitVm4Lgkm0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     // step 3 in four chunks of four MFMAs, the first with the codes' DMA of kt +
@@ -765,21 +772,21 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
     read_b(xn, 0, bn);
     mma4(0, a, b);
     dma_w(kd, wl, sb, zb);
-    sched_chunk<MTW + 3 * WN, 0, PANEL ? 2 : 4>();
+    sched_chunk<MTW + 3 * WN, 0, PANEL ? 2 : 4, Q4>();
     __builtin_amdgcn_sched_barrier(0);
     convert(raw, Pn);
     mma4(1, a, b);
-    sched_chunk<0, 3 * WN, 0>();
+    sched_chunk<0, H2 * 3 * WN, 0, Q4>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < WN / 2; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.zz64[j], Pn.ss[j], one);
     mma4(2, a, b);
-    sched_chunk<0, (13 * WN / 2 + 3) / 4, 0>();
+    sched_chunk<0, (13 * WN / 2 + Q4 - 1) / Q4, 0, Q4>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = WN / 2; j < WN; ++j) an[j] = dequant8(Pn.wf[j][0], Pn.zz[j], Pn.zz64[j], Pn.ss[j], one);
     mma4(3, a, b);
-    sched_chunk<0, (13 * WN / 2 + 3) / 4, 0>();
+    sched_chunk<0, (13 * WN / 2 + Q4 - 1) / Q4, 0, Q4>();
     __builtin_amdgcn_sched_barrier(0);
     P = Pn;
 #pragma unroll
@@ -939,22 +946,25 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   const int n0 = nw0 + (GT ? 16 : 32) * WN * wn, mw0 = m0 + 32 * MTW * wm;
   uint8_t* stage = (uint8_t*)X0 + 8192 * w;
   if constexpr (EPI == kEpiShare) {
+    float share[8];
 #pragma unroll
-    for (int mm = 0; mm < MTW; ++mm) {
-      const int m = mw0 + 32 * mm + l32;
-      if (m < M) {
-        const float share = rows_of.weight(m);
+    for (int mm = 0; mm < MTW; ++mm) share[mm] = rows_of.weight(min(mw0 + 32 * mm + l32, M - 1));
 #pragma unroll
-        for (int j = 0; j < WN; ++j)
+    for (int j = 0; j < WN; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = n0 + 32 * j + 8 * q + 4 * g;
-            if (n < N)
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + 32 * j + 8 * q + 4 * g;
+        if (n < N) {
+#pragma unroll
+          for (int mm = 0; mm < MTW; ++mm) {
+            const int m = mw0 + 32 * mm + l32;
+            if (m < M)
               epi_share(f4{acc[j][mm][4 * q], acc[j][mm][4 * q + 1], acc[j][mm][4 * q + 2], acc[j][mm][4 * q + 3]},
-                        share, m, n, N, bias, (float*)y);
+                        share[mm], m, n, N, bias, (float*)y);
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
   } else if constexpr (EPI != kEpiPlain) {
     // blocks of 64 tokens by two tiles, the second operand two blocks ahead
     constexpr int PS = MTW / 2, BLOCKS = WN / 2 * PS;
@@ -1041,8 +1051,13 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
       sc += row0 * groups;
       zr += row0 * groups;
       if (bias) bias += row0;
+      // an expert's last rows, up to 128: wavefront tiles of half the height
+      if (M - m0 <= GW_M / 2) {
+        segment(std::true_type{}, m0, nb, 0, L, 0, true);
+        return;
+      }
     }
-    segment(m0, nb, 0, L, 0, true);
+    segment(std::false_type{}, m0, nb, 0, L, 0, true);
   } else {
     // the XCD's tile t, its n-blocks walked in super-blocks of 8 m-blocks
     // (the last super-block may hold fewer)
@@ -1055,7 +1070,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
       const int sb = t / (8 * nbx);
       const int rows = min(8, mblk - 8 * sb);
       const int rem = t - sb * 8 * nbx;
-      segment(GW_M * (8 * sb + rem % rows), xcd + 8 * (rem / rows), (int)(u - (int64_t)t * L), (int)(ue - u), t, true);
+      segment(std::false_type{}, GW_M * (8 * sb + rem % rows), xcd + 8 * (rem / rows), (int)(u - (int64_t)t * L), (int)(ue - u), t, true);
     } else {
       while (u < ue) {
         const int t = (int)(u / L);
@@ -1064,7 +1079,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
         const int sb = t / (8 * nbx);
         const int rows = min(8, mblk - 8 * sb);
         const int rem = t - sb * 8 * nbx;
-        segment(GW_M * (8 * sb + rem % rows), xcd + 8 * (rem / rows), k0, k1 - k0, t, t == tfirst);
+        segment(std::false_type{}, GW_M * (8 * sb + rem % rows), xcd + 8 * (rem / rows), k0, k1 - k0, t, t == tfirst);
         u += k1 - k0;
         if (u < ue) {
           // the epilogue's LDS reads before the next segment's DMA and panel
