@@ -23,6 +23,7 @@
 //    four bits): 16 lanes of an operand read hit 16 positions modulo 16.
 // MT: tokens staged (1, 4 or 16); operand columns past it repeat token r % MT,
 // and columns past M are not stored.
+#include "expert_rows.h"
 #include "paro_internal.h"
 #include "w4_common.h"
 #include "w4_epilogue.h"
@@ -45,22 +46,38 @@ constexpr int kCus = 256;
 // LDS bytes of a wavefront, and wavefronts per workgroup at most: two
 // workgroups fit a CU up to 4 tokens, one with 16
 constexpr int wave_bytes(bool gated, int mt) { return (gated ? 8192 : 4096) + 1024 * mt; }
-constexpr int max_waves(bool gated, int mt) { return mt == 1 ? (gated ? 8 : 16) : mt == 4 ? (gated ? 6 : 10) : (gated ? 6 : 7); }
+constexpr int max_waves(bool gated, int mt) {
+  return mt == 1 ? (gated ? 8 : 16) : mt == 4 ? (gated ? 6 : 10) : mt == 8 ? (gated ? 5 : 6) : (gated ? 6 : 7);
+}
 
 // SZV: group 128 and whole chunks, so that a row's four scales and four zeros
-// of a chunk are one 8-byte and one 4-byte load.
-template <int EPI, int MT, bool SZV>
+// of a chunk are one 8-byte and one 4-byte load. ROWS: the tokens, or blocks of at
+// most MT rows of one expert.
+template <int EPI, int MT, bool SZV, class ROWS = AllRows>
 __global__ __launch_bounds__(64 * max_waves(epi_gated(EPI), MT))
 void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qw,
                     const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
                     const uint16_t* __restrict__ bias, uint16_t* y, int M, int N, int d, int gsh, int nblk, int per,
-                    const uint16_t* aux, ActForm act, int erf) {
+                    const uint16_t* aux, ActForm act, int erf, ROWS rows_of) {
   constexpr bool GT = epi_gated(EPI);
   constexpr int TJ = GT ? 2 : 1, WB = wave_bytes(GT, MT), NW = max_waves(GT, MT);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * WB];
   // neighbouring channels on one XCD: they share output lines
-  const int blk = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (blk >= nblk) return;
+  int blk = (blockIdx.x & 7) * per + (blockIdx.x >> 3), m0 = 0;
+  if constexpr (ROWS::kExperts) {
+    ExpertTile tile;
+    if (!rows_of.find_tile(blockIdx.x, MT, nblk, tile, blk)) return;
+    m0 = tile.first;
+    M = tile.end - tile.first;
+    const size_t first = (size_t)tile.expert * (GT ? 2 * N : N);  // the expert's first weight row
+    qw += first * (size_t)(d >> 1);
+    sc += first * (d >> (6 + gsh));
+    zr += first * (d >> (6 + gsh));
+    if (bias) bias += first;
+    if (!ROWS::kGather) x += (size_t)m0 * d;
+  } else {
+    if (blk >= nblk) return;
+  }
   const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), nw = blockDim.x >> 6;
   uint8_t* wl = lds + w * WB;
@@ -69,7 +86,11 @@ void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
   const int segs = d >> 7, chunks = (segs + 3) >> 2;
   const int sgr = d >> (6 + gsh);  // quantization groups per row
   const bool token = r < M;
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)x, (short)0, M * d * 2, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)x, (short)0, (ROWS::kGather ? rows_tokens(rows_of) : M) * d * 2, kRsrcWord3);
+  uint32_t source[16];  // where the block's rows of x start (not sized by MT: the host pass could not instantiate it)
+#pragma unroll
+  for (int t = 0; t < MT; ++t) source[t] = (uint32_t)(source_row(rows_of, m0, min(t, M - 1)) * d * 2);
   auto rows = [&](int j) {  // the block's rows of tile j (rows past N repeat the last one and are never stored)
     return __builtin_amdgcn_make_buffer_rsrc((void*)(qw + ((size_t)c0 + (size_t)j * N) * (size_t)(d >> 1)), (short)0,
                                              min(16, N - c0) * (d >> 1), kRsrcWord3);
@@ -117,8 +138,8 @@ void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int piece = min((lane & 48) | ((lane ^ t) & 15), 16 * nq - 1);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(xl + 1024 * t), 16, min(t, M - 1) * d * 2 + 16 * piece,
-                                               1024 * c, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(xl + 1024 * t), 16, source[t] + 16 * piece, 1024 * c, 0,
+                                               0);
     }
     __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
     if constexpr (SZV) {
@@ -169,7 +190,12 @@ void w4_rows_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ 
   for (int k = 1; k < nw; ++k)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) z[j] += *(const f4*)(lds + k * WB + 1024 * j + 16 * lane);
-  if (token && c0 + 4 * kq < N) epi_lane<EPI>(z, r, c0 + 4 * kq, N, bias, aux, act, erf, y);
+  if (token && c0 + 4 * kq < N) {
+    if constexpr (EPI == kEpiShare)
+      epi_share(z[0], rows_of.weight(m0 + r), m0 + r, c0 + 4 * kq, N, bias, (float*)y);
+    else
+      epi_lane<EPI>(z, m0 + r, c0 + 4 * kq, N, bias, aux, act, erf, y);
+  }
 }
 
 // The same for layers with more 16-channel blocks than CUs: one workgroup per
@@ -369,9 +395,9 @@ hipError_t launch(const uint16_t* x, const uint8_t* qweight, const uint16_t* sca
   const int nblk = (int)((N + 15) / 16), per = (nblk + 7) / 8;
   const int chunks = (int)((d + 511) / 512);
   const bool szv = group == 128 && d % 512 == 0 && ((uintptr_t)scales & 7) == 0 && ((uintptr_t)zeros & 3) == 0;
-  auto go = [&](auto kernel, unsigned blocks, int nw) {
+  auto go = [&](auto kernel, unsigned blocks, int nw, auto... rows) {
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * nw), 0, stream, x, qweight, scales, zeros, bias, y, (int)M,
-                       (int)N, (int)d, gsh, nblk, per, ep.aux, act_form(ep.act), (int)(ep.act == PARO_ACT_GELU));
+                       (int)N, (int)d, gsh, nblk, per, ep.aux, act_form(ep.act), (int)(ep.act == PARO_ACT_GELU), rows...);
   };
   // as many wavefronts as give each the same number of chunks
   constexpr int most = stream_waves(gated);
@@ -392,8 +418,8 @@ hipError_t launch(const uint16_t* x, const uint8_t* qweight, const uint16_t* sca
   constexpr int most1 = max_waves(gated, MT);
   const int rounds1 = (chunks + most1 - 1) / most1;
   const int nw = (chunks + rounds1 - 1) / rounds1;
-  if (szv) go(w4_rows_kernel<EPI, MT, true>, 8u * (unsigned)per, nw);
-  else go(w4_rows_kernel<EPI, MT, false>, 8u * (unsigned)per, nw);
+  if (szv) go(w4_rows_kernel<EPI, MT, true>, 8u * (unsigned)per, nw, AllRows{});
+  else go(w4_rows_kernel<EPI, MT, false>, 8u * (unsigned)per, nw, AllRows{});
   return hipGetLastError();
 }
 
@@ -413,6 +439,57 @@ hipError_t launch_w4_rows(bool gated, const uint16_t* x, const uint8_t* qweight,
                           int group, const W4Epilogue& ep, hipStream_t stream) {
   return gated ? launch_tokens<kEpiGated>(x, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream)
                : launch_tokens<kEpiAct>(x, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream);
+}
+
+namespace {
+
+template <int EPI, int MT>
+hipError_t launch_experts(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+                          const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, int group,
+                          const W4Epilogue& ep, hipStream_t stream) {
+  constexpr bool gated = epi_gated(EPI);
+  typedef ExpertRows<EPI != kEpiShare> Rows;
+  const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
+  const int64_t nblk = (N + 15) / 16, tiles = nblk * expert_blocks(t, MT);
+  const int chunks = (int)((d + 511) / 512);
+  constexpr int most = max_waves(gated, MT);
+  const int rounds = (chunks + most - 1) / most, nw = (chunks + rounds - 1) / rounds;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * nw), 0, stream, x, qweight, scales,
+                       zeros, bias, (uint16_t*)y, t.R, (int)N, (int)d, gsh, (int)nblk, 0, ep.aux, act_form(ep.act),
+                       (int)(ep.act == PARO_ACT_GELU), Rows{t});
+  };
+  if (group == 128 && d % 512 == 0) go(w4_rows_kernel<EPI, MT, true, Rows>);
+  else go(w4_rows_kernel<EPI, MT, false, Rows>);
+  return hipGetLastError();
+}
+
+template <int EPI>
+hipError_t launch_experts_epi(int mt, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                              const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
+                              int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
+  auto go = mt == 1 ? launch_experts<EPI, 1> : mt == 4 ? launch_experts<EPI, 4>
+            : mt == 8 ? launch_experts<EPI, 8> : launch_experts<EPI, 16>;
+  return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
+}
+
+}  // namespace
+
+hipError_t launch_w4_experts_rows(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
+                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
+  const int mt = experts_rows_fit(t);
+  auto go = epi == kEpiGated       ? launch_experts_epi<kEpiGated>
+            : epi == kEpiGatedGrad ? launch_experts_epi<kEpiGatedGrad>
+                                   : launch_experts_epi<kEpiShare>;
+  return go(mt, t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
+}
+
+// Rows per block by the mean number of rows of an expert that has any.
+int experts_rows_fit(const ExpertRouting& t) {
+  const int64_t used = t.E < t.R ? t.E : t.R;
+  if (t.R <= used) return 1;
+  return t.R <= 2 * used ? 4 : t.R <= 6 * used ? 8 : t.R <= 12 * used ? 16 : 0;
 }
 
 }  // namespace paro

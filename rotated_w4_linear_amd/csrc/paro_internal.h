@@ -319,6 +319,12 @@ hipError_t launch_experts_route_backward(const void* logits, int type, int64_t M
 hipError_t launch_w4_experts_tiles(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                    const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                    int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
+// The same for experts of few rows (decode_rows.hip); experts_rows_fit: the rows per
+// block, 0 where the tiles are taken.
+int experts_rows_fit(const ExpertRouting& t);
+hipError_t launch_w4_experts_rows(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
+                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
 // The same in 256 x 256 tiles (w4_experts_wide.hip), and whichever fits.
 hipError_t launch_w4_experts_wide(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
