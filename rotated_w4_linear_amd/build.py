@@ -21,7 +21,7 @@ SOURCES = ["api.cpp", "plan.cpp", "pairs.cpp", "rotate.hip", "quantize.hip", "w4
            "backward.hip", "layer_loss.hip", "noalloc.hip", "dense_gemm.hip", "measure.hip",
            "w4_linear_act.hip", "w4_linear_gated.hip", "w4_linear_act_grad.hip", "w4_linear_gated_grad.hip",
            "decode_act.hip", "decode_gated.hip", "decode_rows.hip", "w4_tiles.hip", "w4_input_grad_rows.hip",
-           "w4_input_grad.hip", "adamw.hip", "api_block.cpp", "experts_route.hip", "experts_sum.hip", "w4_experts_wide.hip", "w4_experts_grad.hip",
+           "w4_input_grad.hip", "adamw.hip", "api_block.cpp", "experts_route.hip", "experts_sum.hip", "w4_experts_wide.hip", "w4_experts_mid.hip", "w4_experts_grad.hip",
            "distill.hip", "api_experts.cpp"]
 
 COMPILE_FLAGS = [

@@ -325,6 +325,12 @@ int experts_rows_fit(const ExpertRouting& t);
 hipError_t launch_w4_experts_rows(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
+// The same for a few rows to some dozens of an expert (w4_experts_mid.hip); P: rows of
+// its weights.
+bool experts_mid_fit(const ExpertRouting& t, int64_t P);
+hipError_t launch_w4_experts_mid(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                                 const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
+                                 int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
 // The same in 256 x 256 tiles (w4_experts_wide.hip), and whichever fits.
 hipError_t launch_w4_experts_wide(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,

@@ -23,8 +23,11 @@ bool experts_wide_fit(const ExpertRouting& t, int64_t P, int64_t d) {
 hipError_t launch_w4_experts(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                              const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
                              int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
-  auto go = experts_wide_fit(t, epi_gated(epi) ? 2 * N : N, d) ? launch_w4_experts_wide
-            : experts_rows_fit(t)                               ? launch_w4_experts_rows
+  const int64_t P = epi_gated(epi) ? 2 * N : N;
+  auto go = experts_wide_fit(t, P, d)   ? launch_w4_experts_wide
+            : experts_rows_fit(t) == 1  ? launch_w4_experts_rows
+            : experts_mid_fit(t, P)     ? launch_w4_experts_mid
+            : experts_rows_fit(t)       ? launch_w4_experts_rows
                                                                 : launch_w4_experts_tiles;
   return go(epi, t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }

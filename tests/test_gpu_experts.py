@@ -173,6 +173,9 @@ PRODUCTS = [
     (700, 4, 2, 272, 512, 256, 0.0), (1500, 8, 2, 288, 256, 64, 0.05), (2500, 3, 1, 528, 384, 128, 0.0),
     (300, 2, 2, 64, 128, 128, 0.0), (400, 3, 1, 80, 256, 64, 0.2), (260, 1, 1, 48, 256, 256, 0.0),
     (150, 2, 2, 160, 640, 128, 0.0), (1200, 40, 6, 96, 384, 128, 0.0),
+    (40, 64, 4, 1040, 640, 64, 0.0), (64, 48, 8, 816, 256, 256, 0.1), (130, 100, 4, 400, 384, 128, 0.5),
+    (500, 40, 2, 880, 896, 64, 0.0), (150, 50, 4, 784, 128, 128, 0.0), (300, 30, 4, 1296, 1152, 128, 0.05),
+    (90, 40, 8, 1056, 768, 256, 0.0), (33, 70, 7, 528, 1408, 64, 0.0), (20, 36, 6, 1040, 1280, 256, 0.0),
 ]
 
 
