@@ -2,18 +2,19 @@
 // dozens: the weights are what has to be moved, and every expert's are read once
 // (once per 16 TT rows).
 //
-// A workgroup owns up to 16 TT rows of one expert by 256 of its weight rows (gated:
-// 128 gate rows and the same channels' up rows), four wavefronts of 64 weight rows
-// each, and goes over k in chunks of 128. Codes and X' come by load-to-LDS DMA
-// into a ring of NS stages, each an LDS object of its own; X' is shared by the
-// wavefronts, so there is one barrier a chunk, and NS - 1 chunks are on their way
-// meanwhile. Two workgroups fit a CU: one's start and end are the other's loads.
+// A workgroup owns up to 16 TT rows of one expert by 64 TC of its weight rows (gated:
+// half of them gate rows, and the same channels' up rows), four wavefronts of 16 TC
+// weight rows each, and goes over k in chunks of 128. Codes and X' come by
+// load-to-LDS DMA into two stages, each an LDS object of its own; X' is shared by
+// the wavefronts, so there is one barrier a chunk. Two to four workgroups fit a CU
+// and keep its loads coming. (Three stages and fewer workgroups: the same bytes on
+// their way, but longer rounds.)
 // (w4_tiles_kernel, whose wavefronts share out k and meet in LDS, holds a CU alone
 // and does nothing else while its operands arrive: 64 tokens, 8 of 64 experts,
 // gated 2048 -> 1024, 80 us.)
 //  * X' [16 TT rows][16 pieces of 8 channels], piece p of row t at p ^ t (low four
 //    bits);
-//  * codes of a wavefront [4][16 rows][4 pieces of 32 codes], piece p of row r at
+//  * codes of a wavefront [TC][16 rows][4 pieces of 32 codes], piece p of row r at
 //    p ^ (r / 4): 16 lanes of an operand read touch every bank once.
 // Scales and zeros: lane l has weight row l of its wavefront, four chunks' at a
 // time in registers, and passes them on: a load touches a line per row, so that
@@ -36,21 +37,23 @@ using namespace w4;
 
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
+constexpr int kWaitVmLgkm0 = 0x70;      // s_waitcnt vmcnt(0) lgkmcnt(0)
 constexpr int kCus = 256;
-constexpr int kRows = 256;  // weight rows per workgroup
+// LDS bytes of a workgroup, and workgroups that fit a CU at once
+constexpr int mid_lds(int tt, int tc) { return 2 * (4096 * tt + 4096 * tc); }
+constexpr int mid_slots(int tt, int tc) { return 163840 / mid_lds(tt, tc) >= 4 ? 4 : 163840 / mid_lds(tt, tc); }
 
 // GSH: log2(group / 64).
-template <int EPI, int TT, int NS, int GSH, class ROWS>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+template <int EPI, int TT, int TC, int GSH, class ROWS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(mid_slots(TT, TC))))
 void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint8_t* __restrict__ qw,
                         const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
                         const uint16_t* __restrict__ bias, uint16_t* y, int N, int d, int nblk, const uint16_t* aux,
                         ActForm act, int erf) {
   constexpr bool GT = epi_gated(EPI);
-  constexpr int CT = GT ? 2 : 4;           // tiles of 16 output channels of a wavefront
-  constexpr int XB = 4096 * TT, CB = 4096;  // bytes of a stage's X', and of a wavefront's codes
-  __shared__ __attribute__((aligned(1024))) uint8_t X0[XB], X1[XB], X2[NS > 2 ? XB : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t C0[4 * CB], C1[4 * CB], C2[NS > 2 ? 4 * CB : 16];
+  constexpr int CT = GT ? TC / 2 : TC;          // tiles of 16 output channels of a wavefront
+  constexpr int XB = 4096 * TT, CB = 1024 * TC;  // bytes of a stage's X', and of a wavefront's codes
+  __shared__ __attribute__((aligned(1024))) uint8_t X0[XB], X1[XB], C0[4 * CB], C1[4 * CB];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, kq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   ExpertTile tile;
@@ -78,7 +81,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
   // code DMA j: tile j's 16 rows
   auto weight_row = [&](int j, int row) { return base + min(16 * (j % CT) + row, left - 1) + (j / CT) * N; };
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < TC; ++j) {
     const int row = lane >> 2;
     woff[j] = (uint32_t)(weight_row(j, row) * half + 16 * ((lane & 3) ^ (row >> 2)));
   }
@@ -86,7 +89,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     const int k = min(c, segs - 1);
     if (any) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < TC; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(cs + CB * w + 1024 * j), 16, woff[j], 64 * k, 0, 0);
     }
 #pragma unroll
@@ -102,7 +105,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
       __builtin_amdgcn_make_buffer_rsrc((void*)(sc + first * groups), (short)0, P * groups * 2, kRsrcWord3);
   const __amdgpu_buffer_rsrc_t rz =
       __builtin_amdgcn_make_buffer_rsrc((void*)(zr + first * groups), (short)0, P * groups, kRsrcWord3);
-  const int srow = weight_row(lane >> 4, lane & 15) * groups;
+  const int srow = weight_row((lane >> 4) % TC, lane & 15) * groups;
   struct Scales {
     uint32_t s[5], z[3];  // the words
     uint32_t at;          // bytes to skip in them: zeros, scales << 8
@@ -148,7 +151,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
   const uint32_t one = fp16_1024_pair();
   f4 acc[4][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < TC; ++j)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[j][t] = f4{0.f, 0.f, 0.f, 0.f};
   const int used = (rows + 15) >> 4;  // blocks of 16 rows that there are
@@ -167,7 +170,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     u4 v[4];
     h2 ss[4], zz[4], zz64[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < TC; ++j) {
       uint32_t sz = __shfl((int)mine, 16 * j + r);
       if constexpr (GSH == 0) {
         const uint32_t other = __shfl((int)second, 16 * j + r);
@@ -186,7 +189,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
       for (int t = 0; t < TT; ++t)
         if (t < used) b[t] = *(const h8*)(xs + 4096 * t + 256 * r + 16 * ((4 * kq + i) ^ r));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < TC; ++j) {
         const h8 a = dequant8(v[j][i], zz[j], zz64[j], ss[j], one);
 #pragma unroll
         for (int t = 0; t < TT; ++t)
@@ -194,21 +197,17 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
       }
     }
   };
-  // s_waitcnt with lgkmcnt(0) and at most v loads still on their way
-  constexpr auto wait_vm = [](int v) { return 0x70 | (v & 15) | ((v >> 4) << 14); };
   Scales now, next;
   if (any) load_scales(0, now);
   dma(0, X0, C0);
-  if constexpr (NS > 2) dma(1, X1, C1);
-  // chunk c in (xs, cs); its ring's last stage (xn, cn), which nobody reads after
-  // the barrier, takes chunk c + NS - 1
+  // chunk c in (xs, cs); the other stage, which nobody reads after the barrier,
+  // takes chunk c + 1
   auto chunk = [&](int c, uint8_t* xs, uint8_t* cs, uint8_t* xn, uint8_t* cn) {
     asm volatile("" ::: "memory");
-    if (any) __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * (4 + TT)));
-    else __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * TT));
+    __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    dma(c + NS - 1, xn, cn);
+    dma(c + 1, xn, cn);
     if (!any) return;
     if ((c & 3) == 0) {
       if (c) now = next;
@@ -218,22 +217,12 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     compute(xs, cs, now, c & 3);
   };
   int c = 0;
-  if constexpr (NS > 2) {
-    for (; c + 3 <= segs; c += 3) {
-      chunk(c, X0, C0, X2, C2);
-      chunk(c + 1, X1, C1, X0, C0);
-      chunk(c + 2, X2, C2, X1, C1);
-    }
-    if (c < segs) chunk(c, X0, C0, X2, C2);
-    if (c + 1 < segs) chunk(c + 1, X1, C1, X0, C0);
-  } else {
-    for (; c + 2 <= segs; c += 2) {
-      chunk(c, X0, C0, X1, C1);
-      chunk(c + 1, X1, C1, X0, C0);
-    }
-    if (c < segs) chunk(c, X0, C0, X1, C1);
+  for (; c + 2 <= segs; c += 2) {
+    chunk(c, X0, C0, X1, C1);
+    chunk(c + 1, X1, C1, X0, C0);
   }
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));  // (the last DMA lands before the workgroup's LDS is another's)
+  if (c < segs) chunk(c, X0, C0, X1, C1);
+  __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);  // (the last DMA lands before the workgroup's LDS is another's)
 
   // acc[j][t][e] = Z[row m0 + 16 t + r][weight row 16 j + 4 kq + e of the wavefront]
 #pragma unroll
@@ -248,7 +237,7 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
           if constexpr (EPI == kEpiShare) {
             epi_share(acc[j][t], rows_of.weight(m), m, n, N, b, (float*)y);
           } else {
-            f4 z[2] = {acc[j][t], GT ? acc[j + 2][t] : acc[j][t]};
+            f4 z[2] = {acc[j][t], acc[GT ? j + CT : j][t]};
             epi_lane<EPI>(z, m, n, N, b, aux, act, erf, y);
           }
         }
@@ -257,60 +246,65 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
   }
 }
 
-template <int EPI, int TT, int GSH>
+template <int EPI, int TT, int TC, int GSH>
 hipError_t launch(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                   const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, const W4Epilogue& ep,
                   hipStream_t stream) {
   typedef ExpertRows<EPI != kEpiShare> Rows;
-  constexpr int NS = TT == 4 ? 2 : 3;
-  const int64_t P = epi_gated(EPI) ? 2 * N : N, nblk = (P + kRows - 1) / kRows;
+  const int64_t P = epi_gated(EPI) ? 2 * N : N, nblk = (P + 64 * TC - 1) / (64 * TC);
   const int64_t tiles = nblk * expert_blocks(t, 16 * TT);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), 0, stream, Rows{t}, x, qweight, scales,
-                       zeros, bias, (uint16_t*)y, (int)N, (int)d, (int)nblk, ep.aux, act_form(ep.act),
-                       (int)(ep.act == PARO_ACT_GELU));
-  };
-  go(experts_mid_kernel<EPI, TT, NS, GSH, Rows>);
+  hipLaunchKernelGGL((experts_mid_kernel<EPI, TT, TC, GSH, Rows>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), 0,
+                     stream, Rows{t}, x, qweight, scales, zeros, bias, (uint16_t*)y, (int)N, (int)d, (int)nblk, ep.aux,
+                     act_form(ep.act), (int)(ep.act == PARO_ACT_GELU));
   return hipGetLastError();
 }
 
-template <int EPI, int TT>
+template <int EPI, int TT, int TC>
 hipError_t launch_group(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                         const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, int group,
                         const W4Epilogue& ep, hipStream_t stream) {
-  auto go = group == 64 ? launch<EPI, TT, 0> : group == 128 ? launch<EPI, TT, 1> : launch<EPI, TT, 2>;
+  auto go = group == 64 ? launch<EPI, TT, TC, 0> : group == 128 ? launch<EPI, TT, TC, 1> : launch<EPI, TT, TC, 2>;
   return go(t, x, qweight, scales, zeros, bias, y, N, d, ep, stream);
 }
 
-template <int EPI>
-hipError_t launch_epi(int tt, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
-                      const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
-                      int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
-  auto go = tt == 1 ? launch_group<EPI, 1> : tt == 2 ? launch_group<EPI, 2> : launch_group<EPI, 4>;
-  return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
+// Rows per tile (blocks of 16) by the mean number of rows of an expert that has
+// any; then the weight tiles of a wavefront: four, or two where that fills the
+// rounds better.
+struct Shape {
+  int tt, tc;
+  int64_t tiles;  // that are expected
+};
+Shape shape_of(const ExpertRouting& t, int64_t P) {
+  const int64_t used = std::min<int64_t>(t.E, t.R);
+  Shape s{t.R <= 8 * used ? 1 : t.R <= 20 * used ? 2 : 4, 4, 0};
+  const int64_t blocks = std::max<int64_t>(used, t.R / (16 * s.tt) + used / 4);
+  auto tiles = [&](int tc) { return blocks * ((P + 64 * tc - 1) / (64 * tc)); };
+  auto rounds = [&](int tc) { return (tiles(tc) + kCus * mid_slots(s.tt, tc) - 1) / (kCus * mid_slots(s.tt, tc)); };
+  if (rounds(2) * 6 <= rounds(4) * 10) s.tc = 2;
+  s.tiles = tiles(s.tc);
+  return s;
 }
 
-// Blocks of 16 rows per tile, by the mean number of rows of an expert that has any.
-int blocks_of(const ExpertRouting& t) {
-  const int64_t used = std::min<int64_t>(t.E, t.R);
-  return t.R <= 8 * used ? 1 : t.R <= 20 * used ? 2 : 4;
+template <int EPI>
+hipError_t launch_epi(const Shape& s, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
+                      const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
+                      int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
+  auto go = s.tc == 4 ? (s.tt == 1 ? launch_group<EPI, 1, 4> : s.tt == 2 ? launch_group<EPI, 2, 4> : launch_group<EPI, 4, 4>)
+                      : (s.tt == 1 ? launch_group<EPI, 1, 2> : s.tt == 2 ? launch_group<EPI, 2, 2> : launch_group<EPI, 4, 2>);
+  return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }
 
 }  // namespace
 
 // Enough workgroups to share the CUs.
-bool experts_mid_fit(const ExpertRouting& t, int64_t P) {
-  const int64_t used = std::min<int64_t>(t.E, t.R);
-  const int64_t tiles = std::max<int64_t>(used, t.R / (16 * blocks_of(t))) * ((P + kRows - 1) / kRows);
-  return tiles >= kCus / 2;
-}
+bool experts_mid_fit(const ExpertRouting& t, int64_t P) { return shape_of(t, P).tiles >= kCus / 2; }
 
 hipError_t launch_w4_experts_mid(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
   auto go = epi == kEpiGated ? launch_epi<kEpiGated> : epi == kEpiGatedGrad ? launch_epi<kEpiGatedGrad>
                                                                             : launch_epi<kEpiShare>;
-  return go(blocks_of(t), t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
+  return go(shape_of(t, epi_gated(epi) ? 2 * N : N), t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }
 
 }  // namespace paro
