@@ -16,6 +16,17 @@ struct AllRows {
   static constexpr bool kExperts = false, kGather = false;
 };
 
+// Inclusive sum over the wavefront's lanes (rows of 16 by shifts, then across them).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // row_shr 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // row_shr 4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // row_shr 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
 // Rows first .. end - 1 (in expert order) of one expert.
 struct ExpertTile {
   int expert, first, end;
@@ -27,49 +38,36 @@ struct ExpertRows {
   static constexpr bool kExperts = true, kGather = GATHER;
   ExpertRouting t;
 
-  // Block `index` of all experts' rows cut into blocks of at most bm; false
-  // past the last one. Every wavefront looks for itself, 64 experts at a time:
-  // the tables have no room for the blocks of each kernel's size, and a scan of
-  // offsets that sit in L2 is shorter than a tile's first loads. (Offsets are
-  // held inside the rows whatever the tables say.)
+  // Rows of expert e0 + lane: first and last + 1, inside the rows whatever the
+  // tables say.
+  __device__ __forceinline__ void rows_of(int e0, int& a, int& z) const {
+    const int e = e0 + (int)(threadIdx.x & 63);
+    a = min(max(t.offsets[min(e, t.E)], 0), t.R);
+    z = min(max(t.offsets[min(e + 1, t.E)], 0), t.R);
+  }
+
+  // Every wavefront looks for its workgroup's tile itself, 64 experts at a time: the
+  // routing has no room for the tiles of each kernel's size.
+  //
+  // find: block `index` of all experts' rows cut into blocks of at most bm; false
+  // past the last one.
   __device__ __forceinline__ bool find(int index, int bm, ExpertTile& out) const {
-    const int lane = threadIdx.x & 63;
     for (int e0 = 0; e0 < t.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int a = min(max(t.offsets[min(e, t.E)], 0), t.R), b = min(max(t.offsets[min(e + 1, t.E)], 0), t.R);
-      const int n = b > a ? (b - a + bm - 1) / bm : 0;
-      int s = n;
-#pragma unroll
-      for (int x = 1; x < 64; x <<= 1) {
-        const int o = __shfl_up(s, x);
-        if (lane >= x) s += o;
-      }
+      int a, z;
+      rows_of(e0, a, z);
+      const int n = z > a ? (z - a + bm - 1) / bm : 0, s = wave_scan(n);
       const int total = __builtin_amdgcn_readlane(s, 63);
       if (index < total) {
         const int at = __builtin_ctzll(__ballot(s > index));
+        const int mb = index - (__builtin_amdgcn_readlane(s, at) - __builtin_amdgcn_readlane(n, at));
         out.expert = e0 + at;
-        out.first = __builtin_amdgcn_readlane(a, at) +
-                    bm * (index - (__builtin_amdgcn_readlane(s, at) - __builtin_amdgcn_readlane(n, at)));
-        out.end = min(__builtin_amdgcn_readlane(b, at), out.first + bm);
+        out.first = __builtin_amdgcn_readlane(a, at) + bm * mb;
+        out.end = min(__builtin_amdgcn_readlane(z, at), out.first + bm);
         return true;
       }
       index -= total;
     }
     return false;
-  }
-
-  // Blocks of bm rows that the experts make.
-  __device__ __forceinline__ int blocks(int bm) const {
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    for (int e0 = 0; e0 < t.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int a = min(max(t.offsets[min(e, t.E)], 0), t.R), b = min(max(t.offsets[min(e + 1, t.E)], 0), t.R);
-      n += b > a ? (b - a + bm - 1) / bm : 0;
-    }
-#pragma unroll
-    for (int x = 32; x > 0; x >>= 1) n += __shfl_xor(n, x);
-    return __builtin_amdgcn_readfirstlane(n);
   }
 
   // The tile of workgroup b, of all blocks of at most bm rows by nblk column
@@ -80,37 +78,36 @@ struct ExpertRows {
   // and columns. (Column blocks dealt out to the XCDs instead, as for one weight
   // block, leave XCDs idle where there are few of them.)
   __device__ __forceinline__ bool find_tile(int b, int bm, int nblk, ExpertTile& out, int& nb) const {
-    const int lane = threadIdx.x & 63;
-    const int all = blocks(bm) * nblk, per = (all + 7) >> 3;
+    int a, z, blocks = 0;
+    for (int e0 = 64; e0 < t.E; e0 += 64) {
+      rows_of(e0, a, z);
+      blocks += __builtin_amdgcn_readlane(wave_scan(z > a ? (z - a + bm - 1) / bm : 0), 63);
+    }
+    rows_of(0, a, z);
+    int n = z > a ? (z - a + bm - 1) / bm : 0, s = wave_scan(n), total = __builtin_amdgcn_readlane(s, 63);
+    const int all = (blocks + total) * nblk, per = (all + 7) >> 3;
     const int idx = b >> 3, tile = (b & 7) * per + idx;
     if (idx >= per || tile >= all) return false;
-    int before = 0;  // tiles of the experts before e0
-    for (int e0 = 0; e0 < t.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int a = min(max(t.offsets[min(e, t.E)], 0), t.R), z = min(max(t.offsets[min(e + 1, t.E)], 0), t.R);
-      const int n = (z > a ? (z - a + bm - 1) / bm : 0) * nblk;
-      int s = n;
-#pragma unroll
-      for (int x = 1; x < 64; x <<= 1) {
-        const int o = __shfl_up(s, x);
-        if (lane >= x) s += o;
-      }
-      const int total = __builtin_amdgcn_readlane(s, 63);
-      if (tile < before + total) {
-        const int at = __builtin_ctzll(__ballot(before + s > tile));
-        const int rows = __builtin_amdgcn_readlane(n, at) / nblk;
-        const int i = tile - before - (__builtin_amdgcn_readlane(s, at) - __builtin_amdgcn_readlane(n, at));
-        const int g = i / (8 * rows), rem = i - g * 8 * rows, cols = min(8, nblk - 8 * g);
-        const int mb = rem / cols;
-        nb = 8 * g + rem - mb * cols;
-        out.expert = e0 + at;
-        out.first = __builtin_amdgcn_readlane(a, at) + bm * mb;
-        out.end = min(__builtin_amdgcn_readlane(z, at), out.first + bm);
-        return true;
-      }
-      before += total;
+    int block = tile / nblk, e0 = 0;  // (its expert has the block of rows that it would be in, were they walked first)
+    while (block >= total) {
+      block -= total;
+      e0 += 64;
+      rows_of(e0, a, z);
+      n = z > a ? (z - a + bm - 1) / bm : 0;
+      s = wave_scan(n);
+      total = __builtin_amdgcn_readlane(s, 63);
     }
-    return false;
+    const int at = __builtin_ctzll(__ballot(s > block));
+    const int rows = __builtin_amdgcn_readlane(n, at);
+    // the expert's tiles: its blocks before it times nblk come first
+    const int i = tile % nblk + (block - (__builtin_amdgcn_readlane(s, at) - rows)) * nblk;
+    const int g = i / (8 * rows), rem = i - g * 8 * rows, cols = min(8, nblk - 8 * g);
+    const int mb = rem / cols;
+    nb = 8 * g + rem - mb * cols;
+    out.expert = e0 + at;
+    out.first = __builtin_amdgcn_readlane(a, at) + bm * mb;
+    out.end = min(__builtin_amdgcn_readlane(z, at), out.first + bm);
+    return true;
   }
 
   // (pair of row r: inside the tables whatever they say)
