@@ -514,7 +514,7 @@ typedef struct paro_routing {
  *   logits   device [M][E] of a paro_type, aligned to it.
  *   ids, weights, offsets, order, place: outputs, as above (M == 0: offsets = 0).
  *   1 <= k <= E <= 1024, k <= 16, R <= 2^30.
- *   workspace: paro_experts_route_workspace_size(M, E, k) bytes (0 up to 256
+ *   workspace: paro_experts_route_workspace_size(M, E, k) bytes (0 up to 128
  *            tokens), 256-byte aligned; scratch, not shared by calls that may
  *            run at the same time.
  * paro_experts_sort makes the tables of given ids (a router of the caller's, or

@@ -595,17 +595,17 @@ def paro_w4_gated_backward(x, qweight, scales, zeros, dy, bias=None, act: str = 
                      True, x, qweight, scales, zeros, dy, bias, act, dz, dx, want_dx, group, workspace, stream)
 
 
-def _types():
-    import torch
-    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_TYPES = {}
 
 
 def _type(t, name) -> int:
     """paro_type of a tensor."""
-    types = _types()
-    if t.dtype not in types:
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    if t.dtype not in _TYPES:
         raise TypeError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
-    return types[t.dtype]
+    return _TYPES[t.dtype]
 
 
 class Routing:
@@ -616,25 +616,62 @@ class Routing:
 
     def __init__(self, ids, weights, offsets, order, place):
         import torch
-        self.M, self.k = ids.shape
-        self.E = offsets.shape[0] - 1
-        self.ids, self.weights, self.offsets, self.order, self.place = ids, weights, offsets, order, place
-        self.device, i32, R = ids.get_device(), torch.int32, self.M * self.k
-        at = self.device
-        self._c = _Routing(self.M, self.E, self.k, _expect(ids, "ids", (self.M, self.k), i32, at),
-                           _expect(offsets, "offsets", (self.E + 1,), i32, at), _expect(order, "order", (R,), i32, at),
-                           _expect(place, "place", (R,), i32, at),
-                           _expect(weights, "weights", (self.M, self.k), torch.float32, at))
+        M, k = ids.shape
+        E = offsets.shape[0] - 1
+        at, i32, R = ids.get_device(), torch.int32, M * k
+        self._tensors = ids, weights, offsets, order, place
+        self._set(M, E, k, at, _expect(ids, "ids", (M, k), i32, at), _expect(offsets, "offsets", (E + 1,), i32, at),
+                  _expect(order, "order", (R,), i32, at), _expect(place, "place", (R,), i32, at),
+                  _expect(weights, "weights", (M, k), torch.float32, at))
+
+    def _set(self, M, E, k, device, *pointers):
+        self.M, self.E, self.k, self.device = M, E, k, device
+        self._c = _Routing(M, E, k, *pointers)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def _made(cls, table, M, E, k, device, given=None):
+        """A routing in one int32 tensor: order, place, offsets, then ids and weights, which may be ``given``
+        instead. The tensors are cut out of it when they are asked for."""
+        self = cls.__new__(cls)
+        self._tensors, self._table, self._given = None, table, given
+        R, at = M * k, table.data_ptr()
+        if given is None:
+            ids = at + 4 * (2 * R + E + 1)
+            weights = ids + 4 * R
+        else:
+            ids, weights = (None if t is None else t.data_ptr() for t in given)
+        self._set(M, E, k, device, ids, at + 8 * R, at, at + 4 * R, weights)
+        return self
+
+    def _cut(self):
+        if self._tensors is None:
+            import torch
+            R = self.M * self.k
+            order, place, offsets, *own = self._table.split_with_sizes(
+                [R, R, self.E + 1] + ([R, R] if self._given is None else []))
+            ids, weights = self._given or (own[0].view(self.M, self.k),
+                                           own[1].view(torch.float32).view(self.M, self.k))
+            self._tensors = ids, weights, offsets, order, place
+        return self._tensors
+
+    ids = property(lambda self: self._cut()[0])
+    weights = property(lambda self: self._cut()[1])
+    offsets = property(lambda self: self._cut()[2])
+    order = property(lambda self: self._cut()[3])
+    place = property(lambda self: self._cut()[4])
 
     def _on(self, device):
         if self.device != device:
             raise ValueError("routing must be on the current device")
-        return ctypes.byref(self._c)
+        return self._ref
 
 
 def _route_workspace(M, E, k, workspace, device, current):
-    need = int(load_library().paro_experts_route_workspace_size(M, E, k)) if workspace is None else 0
-    if need:
+    if workspace is None:
+        need = load_library().paro_experts_route_workspace_size(M, E, k)
+        if not need:
+            return None, None, 0
         import torch
         workspace = torch.empty(need, dtype=torch.uint8, device=device)  # (scratch: nothing has to be zero)
     return _workspace(workspace, 0, device, current)
@@ -645,13 +682,6 @@ def new_experts_route_workspace(M: int, E: int, k: int, device="cuda"):
     return _workspace(None, int(load_library().paro_experts_route_workspace_size(M, E, k)), device)[0]
 
 
-def _tables(M, k, E, device):
-    """offsets, order and place of a routing, not yet written."""
-    import torch
-    t = torch.empty(2 * M * k + E + 1, dtype=torch.int32, device=device)
-    return t[2 * M * k:], t[:M * k], t[M * k:2 * M * k]
-
-
 def paro_experts_route(logits, k: int, normalize: bool = True, workspace=None, stream=None) -> Routing:
     """The ``k`` experts of every token with the largest logits ([M][E], fp32, fp16 or bf16), their softmax
     weights (``normalize``: divided by their sum) and the tables of the routing."""
@@ -659,16 +689,15 @@ def paro_experts_route(logits, k: int, normalize: bool = True, workspace=None, s
     M, E = logits.shape
     dev = torch.cuda.current_device()
     with _made_on(stream):
-        ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((M, k), dtype=torch.float32, device=logits.device)
-        offsets, order, place = _tables(M, k, E, logits.device)
+        table = torch.empty(4 * M * k + E + 1, dtype=torch.int32, device=logits.device)
         workspace, ws_ptr, ws_bytes = _route_workspace(M, E, k, workspace, logits.device, dev)
-    _handed_out(stream, ids, weights, offsets)
+    _handed_out(stream, table)
+    r = Routing._made(table, M, E, k, dev)
+    c = r._c
     _check(load_library().paro_experts_route(
         _expect(logits, "logits", (M, E), logits.dtype, dev), _type(logits, "logits"), M, E, k, int(normalize),
-        ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), ws_ptr, ws_bytes,
-        _raw_stream(stream, dev)))
-    return Routing(ids, weights, offsets, order, place)
+        c.ids, c.weights, c.offsets, c.order, c.place, ws_ptr, ws_bytes, _raw_stream(stream, dev)))
+    return r
 
 
 def paro_experts_sort(ids, E: int, weights=None, workspace=None, stream=None) -> Routing:
@@ -676,14 +705,17 @@ def paro_experts_sort(ids, E: int, weights=None, workspace=None, stream=None) ->
     import torch
     M, k = ids.shape
     dev = torch.cuda.current_device()
+    at = _expect(ids, "ids", (M, k), torch.int32, dev)
+    _expect(weights, "weights", (M, k), torch.float32, dev)
     with _made_on(stream):
-        offsets, order, place = _tables(M, k, E, ids.device)
+        table = torch.empty(2 * M * k + E + 1, dtype=torch.int32, device=ids.device)
         workspace, ws_ptr, ws_bytes = _route_workspace(M, E, k, workspace, ids.device, dev)
-    _handed_out(stream, offsets)
-    _check(load_library().paro_experts_sort(
-        _expect(ids, "ids", (M, k), torch.int32, dev), M, E, k, offsets.data_ptr(), order.data_ptr(),
-        place.data_ptr(), ws_ptr, ws_bytes, _raw_stream(stream, dev)))
-    return Routing(ids, weights, offsets, order, place)
+    _handed_out(stream, table)
+    r = Routing._made(table, M, E, k, dev, (ids, weights))
+    c = r._c
+    _check(load_library().paro_experts_sort(at, M, E, k, c.offsets, c.order, c.place, ws_ptr, ws_bytes,
+                                            _raw_stream(stream, dev)))
+    return r
 
 
 def paro_experts_route_backward(logits, ids, weights, dweights, normalize: bool = True, dlogits=None, stream=None):
@@ -746,14 +778,12 @@ def paro_w4_experts_gated(routing: Routing, x, qweight, scales, zeros, bias=None
     M, d = routing.M, x.shape[1]
     N = qweight.shape[1] // 2
     dev, f16 = torch.cuda.current_device(), torch.float16
-    need = _experts_size("gated", M, routing.E, routing.k, N, d) if workspace is None else 0
-    made = []
-    with _made_on(stream):
-        if h is None:
+    if h is None:
+        with _made_on(stream):
             h = x.new_empty((M * routing.k, N))
-            made.append(h)
-        workspace, ws_ptr, ws_bytes = _workspace(workspace, need, x.device, dev)
-    _handed_out(stream, *made)
+        _handed_out(stream, h)
+    # (the call needs no workspace)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, 0, x.device, dev)
     _check(load_library().paro_w4_experts_gated(
         routing._on(dev), _expect(x, "x", (M, d), f16, dev),
         *_experts_weights(routing, qweight, scales, zeros, bias, 2 * N, d, group, dev), _act(act),

@@ -1,10 +1,10 @@
 // gfx950 kernels of the experts' router:
 //   p = softmax(l) over the E experts of a token, S its k largest logits (the
 //   lower expert first where they are equal), w_s = p_s, or p_s / sum_S p;
-// then the (token, slot) pairs in expert order, by counting: chunks of 256
+// then the (token, slot) pairs in expert order, by counting: chunks of 128
 // tokens count their pairs per expert, and each chunk then adds up the counts of
 // the chunks before it and of the experts before each one, and places its pairs,
-// in pair order inside an expert. Up to 256 tokens one launch does all of it.
+// in pair order inside an expert. Up to 128 tokens one launch does all of it.
 // (Chunks of 64 tokens with a third kernel that turned the counts into first
 // rows, one workgroup walking over the chunks: 16384 tokens, 8 of 256 experts,
 // 234 us.)
@@ -23,7 +23,7 @@
 namespace paro {
 namespace {
 
-constexpr int kChunkTokens = 256;
+constexpr int kChunkTokens = 128;
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 
 // Order of the floats as unsigned numbers, never 0 for an expert that can be
@@ -43,51 +43,60 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// Largest of the lanes' numbers, in every lane (rows of 16 by shifts, then across
+// them: a few cycles a step, where a shuffle through LDS takes a hundred).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  auto with = [&](int moved) { v = max(v, (uint32_t)moved); };
+  with(__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));  // row_shr 1
+  with(__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));  // row_shr 2
+  with(__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));  // row_shr 4
+  with(__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));  // row_shr 8
+  with(__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));  // row_bcast 15
+  with(__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));  // row_bcast 31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // The k largest of a token's E logits: lane s < k returns the s-th's expert (-1:
-// none left) and its weight.
+// none left) and its weight. The largest number first, then the lowest expert
+// that has it, by a ballot for each 64 experts.
 template <class T, int EPL>
 __device__ __forceinline__ void route_token(const typename T::raw* __restrict__ l, int E, int k, int normalize,
                                             int lane, int& id, float& weight) {
-  uint32_t r[EPL];
+  uint32_t r[EPL], all[EPL];
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = 64 * j + lane;
     const float v = e < E ? T::value(l[e]) : -__builtin_inff();
     bad = bad || v != v;
-    r[j] = rank_of(v);
+    all[j] = r[j] = rank_of(v);
   }
-  uint32_t all[EPL];
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) all[j] = r[j];
   uint32_t mine = 0;  // lane s: the s-th logit's rank
   id = -1;
   uint32_t high = 0;
   for (int s = 0; s < k; ++s) {
-    uint32_t best = 0, expert = ~0u;
+    uint32_t best = r[0];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (r[j] > best) {  // (the lower expert stays where they are equal)
-        best = r[j];
-        expert = 64 * j + lane;
-      }
-#pragma unroll
-    for (int x = 32; x > 0; x >>= 1) {
-      const uint32_t ob = __shfl_xor(best, x), oe = __shfl_xor(expert, x);
-      if (ob > best || (ob == best && oe < expert)) {
-        best = ob;
-        expert = oe;
-      }
-    }
+    for (int j = 1; j < EPL; ++j) best = max(best, r[j]);
+    best = wave_max(best);
     if (best == 0) break;
     if (s == 0) high = best;
+    bool found = false;
+    int expert = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const uint64_t has = __ballot(r[j] == best);
+      if (!found && has != 0) {
+        found = true;
+        const int at = __builtin_ctzll(has);
+        expert = 64 * j + at;
+        if (lane == at) r[j] = 0;
+      }
+    }
     if (lane == s) {
       mine = best;
-      id = (int)expert;
+      id = expert;
     }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (expert == (uint32_t)(64 * j + lane)) r[j] = 0;
   }
   const float top = value_of(high);
   const float e = id >= 0 ? expf(value_of(mine) - top) : 0.0f;
@@ -269,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const typename T::raw* 
 }
 
 // The tables of one chunk, from all chunks' counts [chunks][E + 1]. (Every
-// workgroup reads them all: 66 KB at 16384 tokens and 256 experts, from L2.)
+// workgroup reads them all: 132 KB at 16384 tokens and 256 experts, from L2.)
 __global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__ ids, int M, int E, int k,
                                                          const int* __restrict__ counts, int chunks,
                                                          int* __restrict__ offsets, int* __restrict__ order,
