@@ -39,12 +39,12 @@ def route(logits, k, normalize):
 
 
 def route_tolerance(logits, ids, w, normalize):
-    """expf within 3 ulps of an argument rounded once, fp32 sums over at most E experts."""
+    """exp2 within 3 ulps (0 below 2^-126) of an argument rounded twice, fp32 sums over at most E experts."""
     x = np.asarray(logits, np.float64)
     E = x.shape[1]
     top = np.where(np.isfinite(x).any(1), np.max(np.where(np.isfinite(x), x, -np.inf), 1, initial=-1e30), 0.0)
     span = top[:, None] - np.take_along_axis(np.where(np.isfinite(x), x, 0.0), np.maximum(ids, 0), 1)
-    return np.abs(w) * U32 * (2 * np.abs(span) + E + 16) + 2.0 ** -140
+    return np.abs(w) * U32 * (2 * np.abs(span) + E + 16) + 2.0 ** -126
 
 
 def tables(ids, E):

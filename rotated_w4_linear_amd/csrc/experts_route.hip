@@ -1,18 +1,19 @@
 // gfx950 kernels of the experts' router:
 //   p = softmax(l) over the E experts of a token, S its k largest logits (the
 //   lower expert first where they are equal), w_s = p_s, or p_s / sum_S p;
-// then the (token, slot) pairs in expert order, by counting: chunks of 128
-// tokens count their pairs per expert, and each chunk then adds up the counts of
-// the chunks before it and of the experts before each one, and places its pairs,
-// in pair order inside an expert. Up to 128 tokens one launch does all of it.
-// (Chunks of 64 tokens with a third kernel that turned the counts into first
-// rows, one workgroup walking over the chunks: 16384 tokens, 8 of 256 experts,
-// 234 us.)
+// then the (token, slot) pairs in expert order, by counting: chunks of tokens
+// count their pairs per expert, and each chunk then adds up the counts of the
+// chunks before it and of the experts before each one, and places its pairs, in
+// pair order inside an expert. Up to 128 tokens one launch does all of it. (A third
+// kernel that turned the counts into first rows, one workgroup walking over the
+// chunks: 16384 tokens, 8 of 256 experts, 234 us in all.)
 //
-// A wavefront takes a token, 64 experts at a time in a register per lane, and
-// picks the largest of (logit, -expert) k times with a reduction over the
-// lanes. What bounds it: at a few tokens the launch and the k reductions one
-// after the other; at many their instructions (the logits are read once).
+// A wavefront takes a token. A lane has up to four neighbouring experts' logits,
+// sorted, and the largest of the lanes' firsts is picked k times: the lowest lane
+// that has it has the lowest expert. (More than 256 experts: a register for each
+// 64 experts, and a ballot for each.) What bounds it: at a few tokens the launch
+// and the k rounds, one after the other; at many the rounds' instructions (the
+// logits are read once).
 #include <algorithm>
 
 #include "paro_internal.h"
@@ -23,7 +24,12 @@
 namespace paro {
 namespace {
 
-constexpr int kChunkTokens = 128;
+// Tokens per chunk: few, so that the chunks fill the CUs, and more where there are
+// so many chunks that adding up their counts would take longer.
+constexpr int kOneChunk = 128;
+int chunk_tokens(int64_t M) { return M <= kOneChunk ? kOneChunk : M <= 16384 ? 64 : M <= 32768 ? 128 : 256; }
+// Counts of a chunk: whole words of two
+__host__ __device__ __forceinline__ int count_stride(int E) { return (E + 2) & ~1; }
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 
 // Order of the floats as unsigned numbers, never 0 for an expert that can be
@@ -38,10 +44,18 @@ __device__ __forceinline__ float value_of(uint32_t r) {
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
-  return v;
+  auto with = [&](int moved) { v += __builtin_bit_cast(float, moved); };
+  with(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x111, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x112, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x114, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x118, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xa, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xc, 0xf, false));
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
+
+// e^x, x <= 0: an argument rounded once, an ulp or two of exp2; 0 below 2^-126
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(1.4426950408889634f * x); }
 
 // Largest of the lanes' numbers, in every lane (rows of 16 by shifts, then across
 // them: a few cycles a step, where a shuffle through LDS takes a hundred).
@@ -57,40 +71,72 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 // The k largest of a token's E logits: lane s < k returns the s-th's expert (-1:
-// none left) and its weight. The largest number first, then the lowest expert
-// that has it, by a ballot for each 64 experts.
+// none left) and its weight. EPL: logits per lane, neighbours up to four (then a
+// lane's are sorted first), 64 apart beyond.
 template <class T, int EPL>
 __device__ __forceinline__ void route_token(const typename T::raw* __restrict__ l, int E, int k, int normalize,
                                             int lane, int& id, float& weight) {
+  constexpr bool kSorted = EPL <= 4;
   uint32_t r[EPL], all[EPL];
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const int e = 64 * j + lane;
+    const int e = kSorted ? EPL * lane + j : 64 * j + lane;
     const float v = e < E ? T::value(l[e]) : -__builtin_inff();
     bad = bad || v != v;
     all[j] = r[j] = rank_of(v);
+  }
+  int at[EPL];  // which of the lane's logits
+  if constexpr (kSorted) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) at[j] = j;
+    // (neighbours change places only where the later one is larger: equal ones stay in order)
+#pragma unroll
+    for (int n = EPL - 1; n > 0; --n)
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const bool swap = r[j + 1] > r[j];
+        const uint32_t a = r[j], b = r[j + 1];
+        const int x = at[j], y = at[j + 1];
+        r[j] = swap ? b : a;
+        r[j + 1] = swap ? a : b;
+        at[j] = swap ? y : x;
+        at[j + 1] = swap ? x : y;
+      }
   }
   uint32_t mine = 0;  // lane s: the s-th logit's rank
   id = -1;
   uint32_t high = 0;
   for (int s = 0; s < k; ++s) {
     uint32_t best = r[0];
+    if constexpr (!kSorted) {
 #pragma unroll
-    for (int j = 1; j < EPL; ++j) best = max(best, r[j]);
+      for (int j = 1; j < EPL; ++j) best = max(best, r[j]);
+    }
     best = wave_max(best);
     if (best == 0) break;
     if (s == 0) high = best;
-    bool found = false;
     int expert = 0;
+    if constexpr (kSorted) {
+      const int from = __builtin_ctzll(__ballot(r[0] == best));
+      expert = EPL * from + __builtin_amdgcn_readlane(at[0], from);
+      const bool taken = lane == from;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const uint64_t has = __ballot(r[j] == best);
-      if (!found && has != 0) {
-        found = true;
-        const int at = __builtin_ctzll(has);
-        expert = 64 * j + at;
-        if (lane == at) r[j] = 0;
+      for (int j = 0; j < EPL; ++j) {
+        r[j] = taken ? (j + 1 < EPL ? r[j + 1 < EPL ? j + 1 : j] : 0u) : r[j];
+        if (j + 1 < EPL) at[j] = taken ? at[j + 1] : at[j];
+      }
+    } else {
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const uint64_t has = __ballot(r[j] == best);
+        if (!found && has != 0) {
+          found = true;
+          const int from = __builtin_ctzll(has);
+          expert = 64 * j + from;
+          if (lane == from) r[j] = 0;
+        }
       }
     }
     if (lane == s) {
@@ -99,13 +145,12 @@ __device__ __forceinline__ void route_token(const typename T::raw* __restrict__ 
     }
   }
   const float top = value_of(high);
-  const float e = id >= 0 ? expf(value_of(mine) - top) : 0.0f;
+  const float e = id >= 0 ? fast_exp(value_of(mine) - top) : 0.0f;
   float total = e;
   if (!normalize) {
     total = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (all[j]) total += expf(value_of(all[j]) - top);
+    for (int j = 0; j < EPL; ++j) total += all[j] ? fast_exp(value_of(all[j]) - top) : 0.0f;
   }
   total = wave_sum(total);
   weight = id >= 0 ? e / total : 0.0f;
@@ -237,15 +282,15 @@ __device__ __forceinline__ int bucket(int id, int E) { return (uint32_t)id < (ui
 // one chunk in all (gridDim.x == 1) also the offsets and the tables.
 template <class T, int EPL, bool ROUTE>
 __global__ __launch_bounds__(kThreads) void route_kernel(const typename T::raw* __restrict__ logits,
-                                                         const int* given, int M, int E, int k, int normalize,
-                                                         int* ids, float* __restrict__ weights,
-                                                         int* __restrict__ counts, int* __restrict__ offsets,
+                                                         const int* given, int M, int E, int k, int chunk,
+                                                         int normalize, int* ids, float* __restrict__ weights,
+                                                         uint16_t* __restrict__ counts, int* __restrict__ offsets,
                                                          int* __restrict__ order, int* __restrict__ place) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int t0 = kChunkTokens * blockIdx.x, tokens = min(kChunkTokens, M - t0);
+  const int t0 = chunk * blockIdx.x, tokens = min(chunk, M - t0);
   const int pairs = tokens * k;
-  const ChunkLds l = chunk_lds(dyn, min(kChunkTokens, M) * k, E);
+  const ChunkLds l = chunk_lds(dyn, min(chunk, M) * k, E);
   for (int i = tid; i <= E; i += kThreads) l.first[i] = 0;
   __syncthreads();
   if constexpr (ROUTE) {
@@ -270,40 +315,49 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const typename T::raw* 
   }
   __syncthreads();
   if (gridDim.x > 1) {
-    for (int i = tid; i <= E; i += kThreads) counts[(size_t)blockIdx.x * (E + 1) + i] = l.first[i];
+    for (int i = tid; i < count_stride(E); i += kThreads)
+      counts[(size_t)blockIdx.x * count_stride(E) + i] = (uint16_t)(i <= E ? l.first[i] : 0);
     return;
   }
   scan_first(l, E, offsets, [](int) { return 0; });
   place_chunk(l, pairs, 0, E, order, place);
 }
 
-// The tables of one chunk, from all chunks' counts [chunks][E + 1]. (Every
+// The tables of one chunk, from all chunks' counts, two buckets a word. (Every
 // workgroup reads them all: 132 KB at 16384 tokens and 256 experts, from L2.)
-__global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__ ids, int M, int E, int k,
-                                                         const int* __restrict__ counts, int chunks,
+__global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__ ids, int M, int E, int k, int chunk,
+                                                         const uint32_t* __restrict__ counts, int chunks,
                                                          int* __restrict__ offsets, int* __restrict__ order,
                                                          int* __restrict__ place) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   __shared__ int before[kExpertsMax + 1];
   const int tid = threadIdx.x, mine = blockIdx.x;
-  const int t0 = kChunkTokens * mine, pairs = min(kChunkTokens, M - t0) * k;
+  const int t0 = chunk * mine, pairs = min(chunk, M - t0) * k;
   const int pair0 = t0 * k;
-  const ChunkLds l = chunk_lds(dyn, kChunkTokens * k, E);
+  const ChunkLds l = chunk_lds(dyn, chunk * k, E);
   for (int i = tid; i <= E; i += kThreads) l.first[i] = before[i] = 0;
   __syncthreads();
   for (int p = tid; p < pairs; p += kThreads) l.ids[p] = bucket(ids[pair0 + p], E);
   // parts of the chunks side by side, as many as there are threads for
-  const int EB = E + 1, parts = max(1, kThreads / EB), part = tid / EB;
-  for (int e = tid - part * EB; part < parts && e < EB; e += kThreads) {
-    int sum = 0, all = 0;
+  const int words = count_stride(E) / 2, parts = kThreads / words, part = tid / words, i = tid - part * words;
+  if (part < parts) {
+    int sum0 = 0, sum1 = 0, all0 = 0, all1 = 0;
 #pragma unroll 8
     for (int c = part; c < chunks; c += parts) {
-      const int n = counts[(size_t)c * EB + e];
-      all += n;
-      sum += c < mine ? n : 0;
+      const uint32_t n = counts[(size_t)c * words + i];
+      const int n0 = (int)(n & 0xffffu), n1 = (int)(n >> 16);
+      all0 += n0;
+      all1 += n1;
+      sum0 += c < mine ? n0 : 0;
+      sum1 += c < mine ? n1 : 0;
     }
-    atomicAdd(&l.first[e], all);  // (whole numbers: the same in any order)
-    atomicAdd(&before[e], sum);
+    // (whole numbers: the same in any order)
+    atomicAdd(&l.first[2 * i], all0);
+    atomicAdd(&before[2 * i], sum0);
+    if (2 * i + 1 <= E) {
+      atomicAdd(&l.first[2 * i + 1], all1);
+      atomicAdd(&before[2 * i + 1], sum1);
+    }
   }
   __syncthreads();
   scan_first(l, E, mine == 0 ? offsets : nullptr, [&](int e) { return before[e]; });
@@ -370,15 +424,16 @@ hipError_t allow_lds(K kernel, size_t bytes) {
 }
 
 template <class T, bool ROUTE>
-hipError_t launch_route(int chunks, hipStream_t stream, const void* logits, const int* given, int M, int E, int k,
-                        int normalize, int* ids, float* weights, int* counts, int* offsets, int* order, int* place) {
-  const size_t lds = chunk_lds_bytes((int64_t)std::min(kChunkTokens, M) * k, E);
+hipError_t launch_route(int chunk, int chunks, hipStream_t stream, const void* logits, const int* given, int M, int E,
+                        int k, int normalize, int* ids, float* weights, uint16_t* counts, int* offsets, int* order,
+                        int* place) {
+  const size_t lds = chunk_lds_bytes((int64_t)std::min(chunk, M) * k, E);
   auto go = [&](auto kernel) {
     const hipError_t e = allow_lds(kernel, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3((unsigned)chunks), dim3(kThreads), (unsigned)lds, stream,
-                       (const typename T::raw*)logits, given, M, E, k, normalize, ids, weights, counts, offsets, order,
-                       place);
+                       (const typename T::raw*)logits, given, M, E, k, chunk, normalize, ids, weights, counts, offsets,
+                       order, place);
     return hipGetLastError();
   };
   switch (ROUTE ? experts_per_lane(E) : 1) {
@@ -393,29 +448,29 @@ hipError_t launch_route(int chunks, hipStream_t stream, const void* logits, cons
 }  // namespace
 
 size_t experts_route_scratch(int64_t M, int E) {
-  const int64_t chunks = (M + kChunkTokens - 1) / kChunkTokens;
-  return chunks > 1 ? (size_t)chunks * (E + 1) * 4 : 0;
+  const int64_t chunk = chunk_tokens(M), chunks = (M + chunk - 1) / chunk;
+  return chunks > 1 ? (size_t)chunks * count_stride(E) * 2 : 0;
 }
 
 hipError_t launch_experts_route(const void* logits, int type, int64_t M, int E, int k, int normalize, int* ids,
                                 float* weights, int* offsets, int* order, int* place, void* scratch,
                                 hipStream_t stream) {
-  const int chunks = (int)((M + kChunkTokens - 1) / kChunkTokens);
-  int* counts = (int*)scratch;
+  const int chunk = chunk_tokens(M), chunks = (int)((M + chunk - 1) / chunk);
+  uint16_t* counts = (uint16_t*)scratch;
   hipError_t e = hipSuccess;
   if (!logits)
-    e = launch_route<F32, false>(chunks, stream, nullptr, ids, (int)M, E, k, 0, nullptr, nullptr, counts, offsets,
-                                 order, place);
+    e = launch_route<F32, false>(chunk, chunks, stream, nullptr, ids, (int)M, E, k, 0, nullptr, nullptr, counts,
+                                 offsets, order, place);
   else
     with_type(type, [&](auto t) {
-      e = launch_route<decltype(t), true>(chunks, stream, logits, nullptr, (int)M, E, k, normalize, ids, weights,
-                                          counts, offsets, order, place);
+      e = launch_route<decltype(t), true>(chunk, chunks, stream, logits, nullptr, (int)M, E, k, normalize, ids,
+                                          weights, counts, offsets, order, place);
     });
   if (e != hipSuccess || chunks == 1) return e;
-  const size_t lds = chunk_lds_bytes((int64_t)kChunkTokens * k, E);
+  const size_t lds = chunk_lds_bytes((int64_t)chunk * k, E);
   if ((e = allow_lds(place_kernel, lds)) != hipSuccess) return e;
   hipLaunchKernelGGL(place_kernel, dim3((unsigned)chunks), dim3(kThreads), (unsigned)lds, stream, ids, (int)M, E, k,
-                     counts, chunks, offsets, order, place);
+                     chunk, (const uint32_t*)scratch, chunks, offsets, order, place);
   return hipGetLastError();
 }
 

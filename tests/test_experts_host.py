@@ -143,7 +143,7 @@ def test_route_refusals(paro):
                         ({"ws_bytes": 17}, WORKSPACE), ({"ws": A + 128}, ALIGN)]:
         refused(paro, fn, args(**bad), status)
     assert lib.paro_experts_route_workspace_size(128, 8, 2) == 0
-    assert lib.paro_experts_route_workspace_size(129, 8, 2) == 2 * 9 * 4
+    assert lib.paro_experts_route_workspace_size(129, 8, 2) == 3 * 10 * 2
     for M, E, k in [(-1, 8, 2), (10, 0, 1), (10, 8, 9), (100, 2000, 2), (1 << 30, 8, 2)]:
         assert lib.paro_experts_route_workspace_size(M, E, k) == 0
 
