@@ -9,11 +9,18 @@
 //
 // One workgroup per row. A first pass over z takes the running maximum and sum
 // of exponentials (leaving the entries out, by a bitmap of V bits in LDS, where
-// the rest is a class of its own); the entries are done in fp64, and the sum of
-// everything is the rest's plus the entries': where teacher and student agree,
-// L is a small difference, and an error of the rest's sum then enters by Q - P
-// only. A second pass writes the gradient. NV > 0: the row stays in registers
-// between the passes, 16 bytes NV times a lane; else it is read again.
+// the rest is a class of its own); the entries are done in fp64 by one
+// wavefront, and the sum of everything is the rest's plus the entries': where
+// teacher and student agree, L is a small difference, and an error of the rest's
+// sum then enters by Q - P only. A second pass reads z again, from the memory-side
+// cache, and writes the gradient.
+//
+// What bounds it: with a gradient memory (4096 rows of 131072 bf16 in 503 us, 4.3 TB/s
+// of one read and one write, the second read in part from the cache; 574 with stores
+// that go through it); on short rows the entries' chain of latencies, 10 us, which
+// the other workgroups of the CU cover. (Reductions over the whole workgroup for the
+// entries too: 14 us a row. Rows kept in registers between the passes, 1024 lanes
+// a row: 706 us, nothing then covers the chain.)
 #include "paro_internal.h"
 #include "paro_types.h"
 
@@ -23,7 +30,6 @@ namespace paro {
 namespace {
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
 // The VE values of 16 bytes, and back.
@@ -46,40 +52,93 @@ struct Vec {
   }
 };
 
-// Sum, or maximum, over the workgroup, in a fixed order; every thread has it.
-template <int NT, class V, class Op>
-__device__ __forceinline__ V block_reduce(V v, V* red, Op op) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v = op(v, (V)__shfl_xor(v, s));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < NT / 64; ++i) v = op(v, red[i]);
-  return v;
+// Reductions over a wavefront in a fixed order, in every lane: rows of 16 lanes by
+// shifts, then across them, then the last lane's. `none` takes no part.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float v, float none) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                                               __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v, double none) {
+  const uint64_t a = __builtin_bit_cast(uint64_t, v), b = __builtin_bit_cast(uint64_t, none);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(b >> 32), (int)(a >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t a = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)a, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(a >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <class V, class Op>
+__device__ __forceinline__ V wave_reduce(V v, V none, Op op) {
+  v = op(v, moved<0x111, 0xf>(v, none));
+  v = op(v, moved<0x112, 0xf>(v, none));
+  v = op(v, moved<0x114, 0xf>(v, none));
+  v = op(v, moved<0x118, 0xf>(v, none));
+  v = op(v, moved<0x142, 0xa>(v, none));
+  v = op(v, moved<0x143, 0xc>(v, none));
+  return last_lane(v);
+}
+template <class V>
+__device__ __forceinline__ V wave_sum(V v) {
+  return wave_reduce(v, (V)0, [](V a, V b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_reduce(v, -kInf, [](float a, float b) { return fmaxf(a, b); });
 }
 
-template <class Z, class TV, int NT, int NV>
-__global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a) {
+// The teacher's value i, of any type (the same for all lanes).
+__device__ __forceinline__ float value_of(const void* p, int type, int64_t i) {
+  if (type == PARO_TYPE_F32) return ((const float*)p)[i];
+  const uint16_t raw = ((const uint16_t*)p)[i];
+  return type == PARO_TYPE_F16 ? F16::value(raw) : BF16::value(raw);
+}
+
+template <class Z, int NT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void distill_kernel(DistillArgs a, int value_type) {
   typedef typename Z::raw raw;
-  constexpr int VE = Vec<Z>::VE;
-  __shared__ double red[NT / 64];
-  __shared__ int any_twice;
+  constexpr int VE = Vec<Z>::VE, NW = NT / 64, B = 2;
+  __shared__ float wmax[NW], wsum[NW];
+  __shared__ float factor;
+  __shared__ int none_left;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  double* p = (double*)dyn;                // [K]: p_i, then what the gradient at j_i is
-  int* index = (int*)(p + a.K);            // [K], -1: no entry
-  uint32_t* bits = (uint32_t*)(index + a.K);  // V bits and 8 (the words past K even are 4-byte aligned)
-  const int tid = threadIdx.x, V = a.V, K = a.K;
+  const int tid = threadIdx.x, lane = tid & 63, V = a.V, K = a.K;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the wavefront that does the entries: another one in the workgroups of a CU, which
+  // would all keep the same SIMD busy
+  const int own = (int)(blockIdx.x + (blockIdx.x >> 8)) & (NW - 1);
+  double* p = (double*)dyn;                   // [K] the entries' masses, then their gradients
+  double* e = p + K;                          // [K] e^(z / T) in the sum's unit
+  float* zj = (float*)(e + K);                // [K] the student there
+  int* index = (int*)(zj + K);                // [K] -1: no entry
+  uint32_t* bits = (uint32_t*)(index + K);    // V bits and VE
   const int64_t m = blockIdx.x;
   const raw* z = (const raw*)a.z + m * V;
   raw* dz = a.dz ? (raw*)a.dz + m * V : nullptr;
-  const float w = a.weight ? a.weight[m] : 1.0f;
+  const float weight = a.weight ? a.weight[m] : 1.0f;
+  const bool rest = a.lse != nullptr;
+  // the first 64 entries and lse, on their way while the bitmap is cleared
+  int j0 = -1;
+  float t0 = -kInf, z0 = 0.0f, lse = 0.0f;
+  if (w == own) {
+    if (lane < K) {
+      j0 = a.index[m * K + lane];
+      t0 = value_of(a.values, value_type, m * K + lane);
+    }
+    if (rest) lse = a.lse[m];
+    if ((uint32_t)j0 < (uint32_t)V) z0 = Z::value(z[j0]);
+  }
   // 16-byte vectors from the first aligned element on; the elements before and
-  // behind them one by one. Element j has bit j + shift: a vector's lie in one byte.
+  // behind them one by one. Element j has bit j + skip: a vector's lie in one byte.
   const int head = min(V, (int)((16 - ((uintptr_t)z & 15)) & 15) / (int)sizeof(raw));
-  const int nvec = (V - head) / VE, tail0 = head + nvec * VE, shift = (VE - head % VE) % VE;
-  const int vbase = (head + shift) / VE;  // the first vector, in units of VE bits
+  const int nvec = (V - head) / VE, tail0 = head + nvec * VE, skip = (VE - head % VE) % VE;
+  const int vbase = (head + skip) / VE;  // the first vector, in units of VE bits
 
   auto zeros = [&]() {
     if (dz) {
@@ -89,64 +148,99 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a) {
     }
     if (tid == 0) a.loss[m] = 0.0f;
   };
-  if (w == 0.0f) return zeros();  // (a row that is left out: whatever it holds)
+  if (weight == 0.0f) return zeros();  // (a row that is left out: whatever it holds)
 
   // the teacher's entries
   const double it = 1.0 / (double)a.temperature;
   const int words = (V + VE + 31) / 32;
   for (int i = tid; i < words; i += NT) bits[i] = 0;
-  if (tid == 0) any_twice = 0;
   __syncthreads();
-  float tmax = -kInf;
-  int entries = 0;
-  for (int i = tid; i < K; i += NT) {
-    const int j = a.index[m * K + i];
-    const bool in = (uint32_t)j < (uint32_t)V;
-    index[i] = in ? j : -1;
-    if (!in) continue;
-    const float t = TV::value(((const typename TV::raw*)a.values)[m * K + i]);
-    if (t > -kInf || t != t) entries = 1;
-    tmax = fmaxf(tmax, t);
-    const uint32_t b = 1u << ((j + shift) & 31);
-    if (atomicOr(&bits[(j + shift) >> 5], b) & b) any_twice = 1;
+  double psum = 0.0, pscale = 1.0, P = 0.0, A = 1.0;
+  bool twice = false;
+  if (w == own) {
+    float tmax = -kInf;
+    bool again = false, entries = false;
+#pragma unroll 1
+    for (int i = lane; i < K; i += 64) {
+      const int j = i < 64 ? j0 : a.index[m * K + i];
+      const bool in = (uint32_t)j < (uint32_t)V;
+      const float t = i < 64 ? t0 : value_of(a.values, value_type, m * K + i);
+      index[i] = in ? j : -1;
+      p[i] = (double)t * it;
+      if (!in) continue;
+      zj[i] = i < 64 ? z0 : Z::value(z[j]);
+      entries = entries || t > -kInf || t != t;
+      tmax = fmaxf(tmax, t);
+      const uint32_t b = 1u << ((j + skip) & 31);
+      again = again || (atomicOr(&bits[(j + skip) >> 5], b) & b) != 0;
+    }
+    twice = __ballot(again) != 0;
+    const bool any = __ballot(entries) != 0;
+    if (lane == 0) none_left = !rest && !any;  // (a mask that leaves nothing of the teacher)
+    psum = tmax;
   }
-  const bool rest = a.lse != nullptr;
-  entries = __syncthreads_or(entries);
-  if (!rest && !entries) return zeros();  // (a mask that leaves nothing of the teacher)
-  if (!rest) tmax = block_reduce<NT>(tmax, (float*)red, [](float x, float y) { return fmaxf(x, y); });
-  const double ref = rest ? (double)a.lse[m] : (double)tmax * it;
-  double psum = 0.0;
-  for (int i = tid; i < K; i += NT) {
-    double v = 0.0;
-    if (index[i] >= 0) v = exp((double)TV::value(((const typename TV::raw*)a.values)[m * K + i]) * it - ref);
-    p[i] = v;
-    psum += v;
+  __syncthreads();
+  if (w == own) {  // (the others go on meanwhile)
+    const double ref = rest ? (double)lse : (double)wave_max((float)psum) * it;
+    psum = 0.0;
+#pragma unroll 1
+    for (int i = lane; i < K; i += 64) {
+      const double v = index[i] >= 0 ? exp(p[i] - ref) : 0.0;
+      p[i] = v;
+      psum += v;
+    }
+    psum = wave_sum(psum);
+    if (rest) {
+      P = fmax(1.0 - psum, 0.0);
+      A = psum + P;
+    } else {
+      pscale = 1.0 / psum;
+    }
   }
-  auto add = [](double x, double y) { return x + y; };
-  psum = block_reduce<NT>(psum, red, add);
-  double P = 0.0, A = 1.0;
-  if (rest) {
-    P = fmax(1.0 - psum, 0.0);
-    A = psum + P;
-  }
-  const double pscale = rest ? 1.0 : 1.0 / psum;
 
-  // pass 1: maximum and sum
-  const float c = (float)((double)kLog2e * it);
-  float mx = -kInf, base = 0.0f, sum = 0.0f;  // base: mx, or 0 while nothing is above -inf
-  auto taken = [&](int j) { return (bits[(j + shift) >> 5] >> ((j + shift) & 31)) & 1u; };
+  // all vectors of the lane, the next two on their way meanwhile (dz may be z: a
+  // lane reads a vector before anyone writes it)
+  auto stream = [&](auto use) {
+    const u4* src = (const u4*)(z + head);
+    u4 now[B], next[B];
+    auto load = [&](int v0, u4* to) {
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (v0 + b * NT < nvec) to[b] = src[v0 + b * NT];
+    };
+    load(tid, now);
+    for (int v0 = tid; v0 < nvec; v0 += B * NT) {
+      load(v0 + B * NT, next);
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (v0 + b * NT < nvec) use(now[b], v0 + b * NT);
+#pragma unroll
+      for (int b = 0; b < B; ++b) now[b] = next[b];
+    }
+  };
+
+  // pass 1: maximum and sum of 2^(c x - shift), shift = c max rounded (0 while
+  // nothing is above -inf): one fma and one exp2 a logit, the fma's rounding alone
+  const float c = (float)(1.4426950408889634 * it);
+  float mx = -kInf, shift = 0.0f, sum = 0.0f;
+  auto power = [&](float x, float of) { return __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, -of)); };
+  auto taken = [&](int j) { return (bits[(j + skip) >> 5] >> ((j + skip) & 31)) & 1u; };
   auto more = [&](float hi) {
     if (hi > mx) {
-      sum = mx > -kInf ? sum * __builtin_amdgcn_exp2f((mx - hi) * c) : 0.0f;
-      base = mx = hi;
+      const float to = hi * c;
+      sum = mx > -kInf ? sum * __builtin_amdgcn_exp2f(shift - to) : 0.0f;
+      mx = hi;
+      shift = to;
     }
   };
   auto one = [&](int j) {
     const float x = Z::value(z[j]);
     more(x);
-    if (!rest || !taken(j)) sum += __builtin_amdgcn_exp2f((x - base) * c);
+    if (!rest || !taken(j)) sum += power(x, shift);
   };
-  auto vec = [&](const u4& v, int at) {
+  for (int j = tid; j < head; j += NT) one(j);
+  for (int j = tail0 + tid; j < V; j += NT) one(j);
+  stream([&](const u4& v, int at) {
     float x[VE], hi = -kInf;
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
@@ -159,113 +253,122 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a) {
     float part = 0.0f;
     if (out == 0) {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) part += __builtin_amdgcn_exp2f((x[i] - base) * c);
+      for (int i = 0; i < VE; ++i) part += power(x[i], shift);
     } else {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) part += (out >> i) & 1u ? 0.0f : __builtin_amdgcn_exp2f((x[i] - base) * c);
+      for (int i = 0; i < VE; ++i) part += (out >> i) & 1u ? 0.0f : power(x[i], shift);
     }
     sum += part;
+  });
+  // a lane's, a wavefront's, then the workgroup's: sums in the unit of the larger
+  // maximum (0 where nothing is above -inf). A NaN: fmax passes over it, the sum
+  // does not.
+  auto rescaled = [&](float s, float of, float to) {
+    return of < to && s == s ? (of > -kInf ? s * __builtin_amdgcn_exp2f(of * c - to * c) : 0.0f) : s;
   };
-  u4 held[NV > 0 ? NV : 1];
-  if constexpr (NV > 0) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (tid + k * NT < nvec) held[k] = *(const u4*)(z + head + (tid + k * NT) * VE);
-  }
-  for (int j = tid; j < head; j += NT) one(j);
-  for (int j = tail0 + tid; j < V; j += NT) one(j);
-  if constexpr (NV > 0) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (tid + k * NT < nvec) vec(held[k], tid + k * NT);
-  } else {
-    for (int v = tid; v < nvec; v += NT) vec(*(const u4*)(z + head + v * VE), v);
-  }
-  // (a thread whose values are all -inf, or that has none: no sum)
-  const float top = block_reduce<NT>(mx, (float*)red, [](float x, float y) { return fmaxf(x, y); });
-  // NaN: fmax passes over it, the sum does not
-  if (mx < top && sum == sum) sum = mx > -kInf ? sum * __builtin_amdgcn_exp2f((mx - top) * c) : 0.0f;
-  const double left = block_reduce<NT>((double)sum, red, add);
-
-  // the entries: p_i final, the student's mass there (each index once: the lowest
-  // entry's, and its gradient with the masses of all entries of that index)
-  const bool twice = any_twice != 0;
-  double loss = 0.0, mass = 0.0;
-  for (int i = tid; i < K; i += NT) {
-    const int j = index[i];
-    if (j < 0) continue;
-    const double y = ((double)Z::value(z[j]) - (double)top) * it, pi = p[i] * pscale;
-    if (pi != 0.0) loss += pi * (log(pi) - y);
-    bool first = true;
-    if (twice)
-      for (int e = 0; e < i; ++e) first = first && index[e] != j;
-    if (rest && first) mass += exp(y);
-  }
-  loss = block_reduce<NT>(loss, red, add);
-  mass = block_reduce<NT>(mass, red, add);
-  const double total = left + mass;  // (left holds everything without a class for the rest)
-  if (tid == 0) {
-    loss += A * log(total);
-    if (P != 0.0) loss += P * (log(P) - log(left));
-    a.loss[m] = (float)(loss * ((double)w * a.temperature * a.temperature));
-  }
-  if (!dz) return;
-  const double g = (double)w * a.temperature * a.grad_scale;
-  // the gradient at the entries, before anything of the row is overwritten (dz may be z)
-  double mine[4];
-  for (int i = tid, s = 0; i < K; i += NT, ++s) {
-    const int j = index[i];
-    double v = 0.0;
-    if (j >= 0) {
-      double all = p[i];
-      if (twice) {
-        all = 0.0;
-        for (int e = 0; e < K; ++e) all += index[e] == j ? p[e] : 0.0;
-      }
-      v = (A * exp(((double)Z::value(z[j]) - (double)top) * it) / total - all * pscale) * g;
-    }
-    if (s == 0) mine[0] = v;
-    else if (s == 1) mine[1] = v;
-    else if (s == 2) mine[2] = v;
-    else mine[3] = v;
+  const float wtop = wave_max(mx);
+  const float wtotal = wave_sum(rescaled(sum, mx, wtop));
+  if (lane == 0) {
+    wmax[w] = wtop;
+    wsum[w] = wtotal;
   }
   __syncthreads();
-  const float cf = (float)(g * (rest && left > 0.0 ? A / total - P / left : A / total));
+  if (none_left) return zeros();
+  const float top = wave_max(wmax[lane & (NW - 1)]);
+  const float mine = rescaled(wsum[lane & (NW - 1)], wmax[lane & (NW - 1)], top);
+  const double left = wave_sum(lane < NW ? (double)mine : 0.0);
+  const float tshift = top > -kInf ? top * c : 0.0f;
 
-  // pass 2 (a student without mass outside the entries has no gradient there)
-  auto grad = [&](float x) { return __builtin_amdgcn_exp2f((x - top) * c) * cf; };
-  auto grads = [&](const u4& v) {
+  // the entries: the student's mass there, each index once (the lowest entry's).
+  // unit: log of e^(z / T) in the sum's unit of a logit equal to the largest
+  const double g = (double)weight * a.temperature * a.grad_scale;
+  double total = left;
+  if (w == own) {
+    const double unit = ((double)top * (double)c - (double)tshift) * 0.6931471805599453;
+    double mass = 0.0;
+#pragma unroll 1
+    for (int i = lane; i < K; i += 64) {
+      if (index[i] < 0) continue;
+      const double v = exp(((double)zj[i] - (double)top) * it + unit);
+      e[i] = v;
+      bool first = true;
+      if (twice)
+        for (int b = 0; b < i; ++b) first = first && index[b] != index[i];
+      if (rest && first) mass += v;
+    }
+    total = left + wave_sum(mass);  // (left holds everything without a class for the rest)
+    // (a student without mass outside the entries has no gradient there)
+    if (lane == 0) factor = (float)(g * (rest && left > 0.0 ? A / total - P / left : A / total));
+  }
+  __syncthreads();
+  if (w == own) {  // the loss, and the gradient at the entries, with the masses of all entries of an index
+    const double unit = ((double)top * (double)c - (double)tshift) * 0.6931471805599453;
+    double loss = 0.0;
+    const double inverse = 1.0 / total;
+#pragma unroll 1
+    for (int i = lane; i < K; i += 64) {
+      if (index[i] < 0) continue;
+      const double pi = p[i] * pscale;
+      if (pi != 0.0) loss += pi * (log(pi) - (((double)zj[i] - (double)top) * it + unit));
+      double all = pi;
+      if (twice) {
+        all = 0.0;
+        for (int b = 0; b < K; ++b) all += index[b] == index[i] ? p[b] * pscale : 0.0;
+      }
+      e[i] = (A * e[i] * inverse - all) * g;
+    }
+    loss = wave_sum(loss);
+    // the three logarithms side by side
+    const double part = lane == 0 ? total : lane == 1 ? P : left, by = lane == 0 ? A : lane == 1 ? P : -P;
+    const double whole = lane < 3 && by != 0.0 ? by * log(part) : 0.0;
+    loss += wave_sum(whole);
+    if (lane == 0) {
+      a.loss[m] = (float)(loss * ((double)weight * a.temperature * a.temperature));
+    }
+  }
+  if (!dz) return;
+
+  // pass 2
+  const float cf = factor;
+  auto grad = [&](float x) { return power(x, tshift) * cf; };
+  for (int j = tid; j < head; j += NT) dz[j] = Z::pack(grad(Z::value(z[j])));
+  for (int j = tail0 + tid; j < V; j += NT) dz[j] = Z::pack(grad(Z::value(z[j])));
+  stream([&](const u4& v, int at) {
     float f[VE];
 #pragma unroll
     for (int i = 0; i < VE; ++i) f[i] = grad(Vec<Z>::get(v, i));
-    return Vec<Z>::put(f);
-  };
-  for (int j = tid; j < head; j += NT) dz[j] = Z::pack(grad(Z::value(z[j])));
-  for (int j = tail0 + tid; j < V; j += NT) dz[j] = Z::pack(grad(Z::value(z[j])));
-  if constexpr (NV > 0) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (tid + k * NT < nvec) *(u4*)(dz + head + (tid + k * NT) * VE) = grads(held[k]);
-  } else {
-    for (int v = tid; v < nvec; v += NT) *(u4*)(dz + head + v * VE) = grads(*(const u4*)(z + head + v * VE));
-  }
+    __builtin_nontemporal_store(Vec<Z>::put(f), (u4*)(dz + head + at * VE));
+  });
   __syncthreads();  // the entries' places have been written
-  for (int i = tid, s = 0; i < K; i += NT, ++s) {
-    const double v = s == 0 ? mine[0] : s == 1 ? mine[1] : s == 2 ? mine[2] : mine[3];
-    if (index[i] >= 0) dz[index[i]] = Z::pack((float)v);
+  if (w == own) {
+#pragma unroll 1
+    for (int i = lane; i < K; i += 64)
+      if (index[i] >= 0) dz[index[i]] = Z::pack((float)e[i]);
   }
 }
 
 }  // namespace
 
+// Lanes per row. Many rows: as few as keep a CU's memory path busy with several
+// rows, so that they cover each other's latencies; with a gradient the rows in flight
+// have to stay in the memory-side cache until the second pass, so that long rows
+// take more lanes (4096 bf16 rows with 256 / 512 / 1024 lanes: of 131072 630 / 514 /
+// 503 us, of 32000 133 / 131 / 155, of 8000 50 / 60 / 95; the loss alone, of 131072,
+// 209 / 231 / 253). Few rows: the row itself is the latency (16 rows of 131072 40 /
+// 27 / 24).
 hipError_t launch_distill(const DistillArgs& a, int z_type, int value_type, hipStream_t stream) {
   with_type(z_type, [&](auto z) {
-    with_type(value_type, [&](auto v) {
-      typedef decltype(z) Z;
-      typedef decltype(v) TV;
-      const unsigned lds = (unsigned)(a.K * 12 + (a.V + Vec<Z>::VE + 31) / 32 * 4);
-      hipLaunchKernelGGL((distill_kernel<Z, TV, 256, 0>), dim3((unsigned)a.M), dim3(256), lds, stream, a);
-    });
+    typedef decltype(z) Z;
+    constexpr int VE = Vec<Z>::VE;
+    const unsigned lds = (unsigned)(a.K * 24 + (a.V + VE + 31) / 32 * 4);
+    auto go = [&](auto kernel, int threads) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)a.M), dim3(threads), lds, stream, a, value_type);
+    };
+    const int kb = a.V / 1024 * (16 / VE);  // of a row
+    const bool few = a.M <= 512;
+    if (few ? kb >= 32 : a.dz && kb >= 192) go(distill_kernel<Z, 1024>, 1024);
+    else if (few ? kb >= 8 : a.dz && kb >= 48) go(distill_kernel<Z, 512>, 512);
+    else go(distill_kernel<Z, 256>, 256);
   });
   return hipGetLastError();
 }
