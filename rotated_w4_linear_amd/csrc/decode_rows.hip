@@ -468,8 +468,7 @@ template <int EPI>
 hipError_t launch_experts_epi(int mt, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                               const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
                               int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
-  auto go = mt == 1 ? launch_experts<EPI, 1> : mt == 4 ? launch_experts<EPI, 4>
-            : mt == 8 ? launch_experts<EPI, 8> : launch_experts<EPI, 16>;
+  auto go = mt == 1 ? launch_experts<EPI, 1> : launch_experts<EPI, 4>;
   return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }
 
@@ -478,18 +477,11 @@ hipError_t launch_experts_epi(int mt, const ExpertRouting& t, const uint16_t* x,
 hipError_t launch_w4_experts_rows(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
-  const int mt = experts_rows_fit(t);
+  const int mt = t.M == 1 ? 1 : 4;  // (a token's experts differ)
   auto go = epi == kEpiGated       ? launch_experts_epi<kEpiGated>
             : epi == kEpiGatedGrad ? launch_experts_epi<kEpiGatedGrad>
                                    : launch_experts_epi<kEpiShare>;
   return go(mt, t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
-}
-
-// Rows per block by the mean number of rows of an expert that has any.
-int experts_rows_fit(const ExpertRouting& t) {
-  const int64_t used = t.E < t.R ? t.E : t.R;
-  if (t.R <= used) return 1;
-  return t.R <= 2 * used ? 4 : t.R <= 6 * used ? 8 : t.R <= 12 * used ? 16 : 0;
 }
 
 }  // namespace paro

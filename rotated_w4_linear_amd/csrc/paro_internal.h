@@ -314,20 +314,12 @@ hipError_t launch_experts_route(const void* logits, int type, int64_t M, int E, 
 hipError_t launch_experts_route_backward(const void* logits, int type, int64_t M, int E, int k, int normalize,
                                          const int* ids, const float* weights, const float* dweights, void* dlogits,
                                          hipStream_t stream);
-// The experts' products in small tiles (w4_tiles.hip): epi kEpiGated and
-// kEpiGatedGrad on tokens x, kEpiShare on rows x in expert order; y by row.
-hipError_t launch_w4_experts_tiles(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
-                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
-                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
-// The same for experts of few rows (decode_rows.hip); experts_rows_fit: the rows per
-// block, 0 where the tiles are taken.
-int experts_rows_fit(const ExpertRouting& t);
+// The experts' products: epi kEpiGated and kEpiGatedGrad on tokens x, kEpiShare on rows
+// x in expert order; y by row. For few pairs in all (decode_rows.hip).
 hipError_t launch_w4_experts_rows(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
-// The same for a few rows to some dozens of an expert (w4_experts_mid.hip); P: rows of
-// its weights.
-bool experts_mid_fit(const ExpertRouting& t, int64_t P);
+// The same for a few rows to some dozens of an expert (w4_experts_mid.hip).
 hipError_t launch_w4_experts_mid(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
@@ -346,7 +338,7 @@ hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, cons
                                        float* part, int64_t P, int64_t d, int group, hipStream_t stream);
 // The same in large tiles for experts of many rows (w4_experts_grad.hip): part [R][d]
 // (dz by row), or dh = w U and the partial dots U . h (dy by token).
-bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P);
+bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d);
 size_t experts_grad_dots(const ExpertRouting& t, int64_t d);
 hipError_t launch_w4_experts_grad_part(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight,
                                        const uint16_t* scales, const uint8_t* zeros, float* part, int64_t P, int64_t d,

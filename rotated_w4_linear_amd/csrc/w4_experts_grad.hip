@@ -372,7 +372,16 @@ hipError_t launch(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qwe
 }  // namespace
 
 // Experts of enough rows, and a whole k-tile.
-bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P) { return P >= kK && t.R >= 64 * (int64_t)t.E; }
+// Whether the gradient is taken in these tiles, from a mean of 16 rows on if there are
+// tiles for all CUs, else of 160. Microseconds of w4_input_grad_rows_kernel's way | this:
+//   of 2048 -> 1024, 64 experts: a mean of 8 rows 47 | 46, 16: 55 | 48, 64: 107 | 67;
+//   of gated 1408 -> 2048, 60 experts: 16: 151 | 172, 48: 225 | 242, 96: 395 | 356;
+//   of gated 4096 -> 14336, 8 experts (128 tiles): 32: 532 | 604, 128: 966 | 1096,
+//     192: 1290 | 1231.
+bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d) {
+  const int64_t E = t.E;
+  return P >= kK && t.R >= (E * d >= kN * 256 ? 16 : 160) * E;
+}
 
 // partial dots of the weights' gradients: [2 ceil(d / 256)][R]
 size_t experts_grad_dots(const ExpertRouting& t, int64_t d) { return (size_t)((d + kN - 1) / kN) * 2 * t.R * 4; }

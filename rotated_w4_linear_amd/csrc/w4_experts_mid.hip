@@ -1,26 +1,25 @@
-// gfx950 kernel for the experts' products where an expert has a few rows to some
-// dozens: the weights are what has to be moved, and every expert's are read once
+// gfx950 kernel for the experts' products where an expert has from one row to some
+// hundred: the weights are what has to be moved, and every expert's are read once
 // (once per 16 TT rows).
 //
-// A workgroup owns up to 16 TT rows of one expert by 64 TC of its weight rows (gated:
-// half of them gate rows, and the same channels' up rows), four wavefronts of 16 TC
-// weight rows each, and goes over k in chunks of 128. Codes and X' come by
-// load-to-LDS DMA into two stages, each an LDS object of its own; X' is shared by
-// the wavefronts, so there is one barrier a chunk. Two to four workgroups fit a CU
-// and keep its loads coming. (Three stages and fewer workgroups: the same bytes on
-// their way, but longer rounds.)
+// A workgroup owns up to 16 TT rows of one expert by 128 of its weight rows (gated:
+// 64 gate rows, and the same channels' up rows), four wavefronts of 32 weight rows
+// each, and goes over k in chunks of 128. Codes and X' come by load-to-LDS DMA into
+// two stages, each an LDS object of its own; X' is shared by the wavefronts, so there
+// is one barrier a chunk. Four workgroups fit a CU (TT = 4: three) and keep its loads
+// coming. Measured against it, gated 2048 -> 1024, 8 of 64 experts, 768 tokens (90 us)
+// and 16 (28 us): four stages, whose LDS leaves room for fewer workgroups, 161 and
+// 29; 256 weight rows instead of 128, 99 and 38.
 // (w4_tiles_kernel, whose wavefronts share out k and meet in LDS, holds a CU alone
-// and does nothing else while its operands arrive: 64 tokens, 8 of 64 experts,
-// gated 2048 -> 1024, 80 us.)
+// and does nothing else while its operands arrive: 64 tokens, 80 us for 36.)
 //  * X' [16 TT rows][16 pieces of 8 channels], piece p of row t at p ^ t (low four
 //    bits);
-//  * codes of a wavefront [TC][16 rows][4 pieces of 32 codes], piece p of row r at
+//  * codes of a wavefront [2 tiles][16 rows][4 pieces of 32 codes], piece p of row r at
 //    p ^ (r / 4): 16 lanes of an operand read touch every bank once.
 // Scales and zeros: lane l has weight row l of its wavefront, four chunks' at a
 // time in registers, and passes them on: a load touches a line per row, so that
 // loads group by group keep the address path longer than the codes do (777 tokens,
 // 4 of 60 experts, groups of 64, 1408 -> 2064: 74 us).
-#include <algorithm>
 #include <type_traits>
 
 #include "expert_rows.h"
@@ -38,19 +37,18 @@ using namespace w4;
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
 constexpr int kWaitVmLgkm0 = 0x70;      // s_waitcnt vmcnt(0) lgkmcnt(0)
-constexpr int kCus = 256;
-// LDS bytes of a workgroup, and workgroups that fit a CU at once
-constexpr int mid_lds(int tt, int tc) { return 2 * (4096 * tt + 4096 * tc); }
-constexpr int mid_slots(int tt, int tc) { return 163840 / mid_lds(tt, tc) >= 4 ? 4 : 163840 / mid_lds(tt, tc); }
+// workgroups that fit a CU at once
+constexpr int mid_slots(int tt) { return tt == 4 ? 3 : 4; }
 
 // GSH: log2(group / 64).
-template <int EPI, int TT, int TC, int GSH, class ROWS>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(mid_slots(TT, TC))))
+template <int EPI, int TT, int GSH, class ROWS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(mid_slots(TT))))
 void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint8_t* __restrict__ qw,
                         const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
                         const uint16_t* __restrict__ bias, uint16_t* y, int N, int d, int nblk, const uint16_t* aux,
                         ActForm act, int erf) {
   constexpr bool GT = epi_gated(EPI);
+  constexpr int TC = 2;                         // weight tiles of a wavefront
   constexpr int CT = GT ? TC / 2 : TC;          // tiles of 16 output channels of a wavefront
   constexpr int XB = 4096 * TT, CB = 1024 * TC;  // bytes of a stage's X', and of a wavefront's codes
   __shared__ __attribute__((aligned(1024))) uint8_t X0[XB], X1[XB], C0[4 * CB], C1[4 * CB];
@@ -85,16 +83,19 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     const int row = lane >> 2;
     woff[j] = (uint32_t)(weight_row(j, row) * half + 16 * ((lane & 3) ^ (row >> 2)));
   }
-  auto dma = [&](int c, uint8_t* xs, uint8_t* cs) {  // (past the last chunk: the last one again, never read)
+  // (past the last chunk: the last one again, never read)
+  auto dma_x = [&](int c, uint8_t* xs) {
     const int k = min(c, segs - 1);
-    if (any) {
-#pragma unroll
-      for (int j = 0; j < TC; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(cs + CB * w + 1024 * j), 16, woff[j], 64 * k, 0, 0);
-    }
 #pragma unroll
     for (int t = 0; t < TT; ++t)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(xs + 4096 * t + 1024 * w), 16, xoff[t], 256 * k, 0, 0);
+  };
+  auto dma = [&](int c, uint8_t* xs, uint8_t* cs) {
+    const int k = min(c, segs - 1);
+#pragma unroll
+    for (int j = 0; j < TC; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(cs + CB * w + 1024 * j), 16, woff[j], 64 * k, 0, 0);
+    dma_x(c, xs);
   };
 
   // scales and zeros of weight row `lane` of the wavefront, of four chunks: GQ
@@ -187,41 +188,58 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
       h8 b[TT];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
-        if (t < used) b[t] = *(const h8*)(xs + 4096 * t + 256 * r + 16 * ((4 * kq + i) ^ r));
+        if (t == 0 || t < used) b[t] = *(const h8*)(xs + 4096 * t + 256 * r + 16 * ((4 * kq + i) ^ r));
 #pragma unroll
       for (int j = 0; j < TC; ++j) {
         const h8 a = dequant8(v[j][i], zz[j], zz64[j], ss[j], one);
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-          if (t < used) acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[t], acc[j][t], 0, 0, 0);
+          if (t == 0 || t < used) acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[t], acc[j][t], 0, 0, 0);
       }
     }
   };
-  Scales now, next;
-  if (any) load_scales(0, now);
-  dma(0, X0, C0);
-  // chunk c in (xs, cs); the other stage, which nobody reads after the barrier,
-  // takes chunk c + 1
-  auto chunk = [&](int c, uint8_t* xs, uint8_t* cs, uint8_t* xn, uint8_t* cn) {
+  // the stage's chunk is there, and nobody reads the other stage any more
+  auto sync = [&]() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    dma(c + 1, xn, cn);
-    if (!any) return;
-    if ((c & 3) == 0) {
-      if (c) now = next;
-      cut(now);
-      if (c + 4 < segs) load_scales(c + 4, next);
-    }
-    compute(xs, cs, now, c & 3);
   };
-  int c = 0;
-  for (; c + 2 <= segs; c += 2) {
-    chunk(c, X0, C0, X1, C1);
-    chunk(c + 1, X1, C1, X0, C0);
+  if (!any) {
+    dma_x(0, X0);
+    for (int c = 0; c < segs; ++c) {
+      sync();
+      dma_x(c + 1, c & 1 ? X0 : X1);
+    }
+  } else {
+    Scales now, next;
+    load_scales(0, now);
+    dma(0, X0, C0);
+    // chunk c + i in its stage, the other one takes chunk c + i + 1. (Four chunks,
+    // which share their scales' loads, in a row and without a branch: the waits stay
+    // where they are here.)
+    auto chunk = [&](int c, auto at) {
+      constexpr int i = decltype(at)::value;
+      sync();
+      dma(c + i + 1, i & 1 ? X0 : X1, i & 1 ? C0 : C1);
+      if (i == 0) {
+        cut(now);
+        load_scales(min(c + 4, (segs - 1) & ~3), next);
+      }
+      compute(i & 1 ? X1 : X0, i & 1 ? C1 : C0, now, i);
+    };
+    int c = 0;
+    for (; c + 4 <= segs; c += 4) {
+      chunk(c, std::integral_constant<int, 0>{});
+      chunk(c, std::integral_constant<int, 1>{});
+      chunk(c, std::integral_constant<int, 2>{});
+      chunk(c, std::integral_constant<int, 3>{});
+      now = next;
+    }
+    if (c < segs) chunk(c, std::integral_constant<int, 0>{});
+    if (c + 1 < segs) chunk(c, std::integral_constant<int, 1>{});
+    if (c + 2 < segs) chunk(c, std::integral_constant<int, 2>{});
   }
-  if (c < segs) chunk(c, X0, C0, X1, C1);
   __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);  // (the last DMA lands before the workgroup's LDS is another's)
 
   // acc[j][t][e] = Z[row m0 + 16 t + r][weight row 16 j + 4 kq + e of the wavefront]
@@ -246,65 +264,48 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
   }
 }
 
-template <int EPI, int TT, int TC, int GSH>
+template <int EPI, int TT, int GSH>
 hipError_t launch(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                   const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, const W4Epilogue& ep,
                   hipStream_t stream) {
   typedef ExpertRows<EPI != kEpiShare> Rows;
-  const int64_t P = epi_gated(EPI) ? 2 * N : N, nblk = (P + 64 * TC - 1) / (64 * TC);
+  const int64_t P = epi_gated(EPI) ? 2 * N : N, nblk = (P + 127) / 128;
   const int64_t tiles = nblk * expert_blocks(t, 16 * TT);
-  hipLaunchKernelGGL((experts_mid_kernel<EPI, TT, TC, GSH, Rows>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), 0,
+  hipLaunchKernelGGL((experts_mid_kernel<EPI, TT, GSH, Rows>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), 0,
                      stream, Rows{t}, x, qweight, scales, zeros, bias, (uint16_t*)y, (int)N, (int)d, (int)nblk, ep.aux,
                      act_form(ep.act), (int)(ep.act == PARO_ACT_GELU));
   return hipGetLastError();
 }
 
-template <int EPI, int TT, int TC>
+template <int EPI, int TT>
 hipError_t launch_group(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                         const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, int group,
                         const W4Epilogue& ep, hipStream_t stream) {
-  auto go = group == 64 ? launch<EPI, TT, TC, 0> : group == 128 ? launch<EPI, TT, TC, 1> : launch<EPI, TT, TC, 2>;
+  auto go = group == 64 ? launch<EPI, TT, 0> : group == 128 ? launch<EPI, TT, 1> : launch<EPI, TT, 2>;
   return go(t, x, qweight, scales, zeros, bias, y, N, d, ep, stream);
 }
 
-// Rows per tile (blocks of 16) by the mean number of rows of an expert that has
-// any; then the weight tiles of a wavefront: four, or two where that fills the
-// rounds better.
-struct Shape {
-  int tt, tc;
-  int64_t tiles;  // that are expected
-};
-Shape shape_of(const ExpertRouting& t, int64_t P) {
-  const int64_t used = std::min<int64_t>(t.E, t.R);
-  Shape s{t.R <= 8 * used ? 1 : t.R <= 20 * used ? 2 : 4, 4, 0};
-  const int64_t blocks = std::max<int64_t>(used, t.R / (16 * s.tt) + used / 4);
-  auto tiles = [&](int tc) { return blocks * ((P + 64 * tc - 1) / (64 * tc)); };
-  auto rounds = [&](int tc) { return (tiles(tc) + kCus * mid_slots(s.tt, tc) - 1) / (kCus * mid_slots(s.tt, tc)); };
-  if (rounds(2) * 6 <= rounds(4) * 10) s.tc = 2;
-  s.tiles = tiles(s.tc);
-  return s;
-}
-
+// Rows per tile (blocks of 16) by the mean number of an expert's rows: 16, 32 and 64
+// at the means 12 / 24 / 96 of gated 2048 -> 1024, 64 experts, take 36, 37 and - / 46,
+// 43 and - / -, 109 and 90 us; at 14336 -> 4096, 8 experts, - / 93, 82 and - / -, 197
+// and 172.
 template <int EPI>
-hipError_t launch_epi(const Shape& s, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
-                      const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N,
-                      int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
-  auto go = s.tc == 4 ? (s.tt == 1 ? launch_group<EPI, 1, 4> : s.tt == 2 ? launch_group<EPI, 2, 4> : launch_group<EPI, 4, 4>)
-                      : (s.tt == 1 ? launch_group<EPI, 1, 2> : s.tt == 2 ? launch_group<EPI, 2, 2> : launch_group<EPI, 4, 2>);
+hipError_t launch_epi(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
+                      const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, int group,
+                      const W4Epilogue& ep, hipStream_t stream) {
+  const int64_t E = t.E;
+  auto go = t.R <= 16 * E ? launch_group<EPI, 1> : t.R <= 64 * E ? launch_group<EPI, 2> : launch_group<EPI, 4>;
   return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }
 
 }  // namespace
-
-// Enough workgroups to share the CUs.
-bool experts_mid_fit(const ExpertRouting& t, int64_t P) { return shape_of(t, P).tiles >= kCus / 2; }
 
 hipError_t launch_w4_experts_mid(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
   auto go = epi == kEpiGated ? launch_epi<kEpiGated> : epi == kEpiGatedGrad ? launch_epi<kEpiGatedGrad>
                                                                             : launch_epi<kEpiShare>;
-  return go(shape_of(t, epi_gated(epi) ? 2 * N : N), t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
+  return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }
 
 }  // namespace paro

@@ -1203,8 +1203,8 @@ hipError_t launch_w4_gemm_epi(const uint16_t* x, const uint8_t* qweight, const u
   return hipGetLastError();
 }
 
-// The experts' product in 256 x 256 tiles, one per workgroup; y as for
-// launch_w4_experts_tiles. d >= 256 (two k-tiles at a time, four at least).
+// The experts' product in 256 x 256 tiles, one per workgroup; y by
+// row (kEpiShare: fp32). d >= 256 (two k-tiles at a time, four at least).
 template <int EPI, bool GATHER>
 hipError_t launch_w4_experts_wide_epi(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                       const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,

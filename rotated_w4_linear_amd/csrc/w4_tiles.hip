@@ -20,7 +20,6 @@
 //    (low four bits);
 //  * codes [TC][16 rows][4 pieces of 32 codes], piece p of row r at
 //    p ^ (r / 4): 16 lanes of an operand read touch every bank once.
-#include "expert_rows.h"
 #include "paro_internal.h"
 #include "w4_common.h"
 #include "w4_epilogue.h"
@@ -47,15 +46,13 @@ constexpr int tile_waves(int tt, int tc) {
 }
 
 // EPI as in w4_epilogue.h. Gated: half of the TC weight tiles are the gate's,
-// the others the same channels of the up projection. ROWS: the tokens, or the
-// experts' rows (token blocks then are blocks of one expert's rows, and the
-// weight block is that expert's).
-template <class ROWS, int EPI, int TT, int TC>
+// the others the same channels of the up projection.
+template <int EPI, int TT, int TC>
 __global__ __launch_bounds__(64 * tile_waves(TT, TC))
 void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qw,
                      const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
                      const uint16_t* __restrict__ bias, uint16_t* y, int M, int N, int d, int gsh, int mblk,
-                     int blocks, int per, const uint16_t* aux, ActForm act, int erf, ROWS rows_of) {
+                     int blocks, int per, const uint16_t* aux, ActForm act, int erf) {
   constexpr bool GT = epi_gated(EPI);
   constexpr int CT = GT ? TC / 2 : TC;  // tiles of 16 output channels
   constexpr int WB = tile_bytes(TT, TC);
@@ -65,25 +62,12 @@ void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   const int blk = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if (blk >= blocks) return;
   const int nb = blk / mblk;
-  int m0 = 16 * TT * (blk - nb * mblk);
-  const int c0 = 16 * CT * nb;
+  const int m0 = 16 * TT * (blk - nb * mblk), c0 = 16 * CT * nb;
   const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), nw = blockDim.x >> 6;
   const int segs = d >> 7, sgr = d >> (6 + gsh);  // chunks; quantization groups per row
-  if constexpr (ROWS::kExperts) {
-    ExpertTile tile;
-    if (!rows_of.find(blk - nb * mblk, 16 * TT, tile)) return;
-    m0 = tile.first;
-    M = tile.end;
-    const size_t first = (size_t)tile.expert * (GT ? 2 * N : N);  // the expert's first weight row
-    qw += first * (size_t)(d >> 1);
-    sc += first * sgr;
-    zr += first * sgr;
-    if (bias) bias += first;
-  }
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(x + (ROWS::kGather ? 0 : (size_t)m0 * d)), (short)0,
-      (ROWS::kGather ? rows_tokens(rows_of) : min(16 * TT, M - m0)) * d * 2, kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)(x + (size_t)m0 * d), (short)0,
+                                                                      min(16 * TT, M - m0) * d * 2, kRsrcWord3);
   const int rows = min(16 * CT, N - c0);  // rows past N repeat the last one and are never stored
   auto codes = [&](int up) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)(qw + ((size_t)up * N + c0) * (size_t)(d >> 1)), (short)0,
@@ -92,8 +76,8 @@ void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   uint32_t xoff[16], woff[4];  // (not sized by TT and TC: the host pass could not instantiate the loads)
 #pragma unroll
   for (int t = 0; t < 4 * TT; ++t) {
-    const int row = 4 * t + kq, at = min(row, M - 1 - m0);
-    xoff[t] = (uint32_t)(source_row(rows_of, m0, at) * d * 2 + 16 * (r ^ (row & 15)));
+    const int row = 4 * t + kq;
+    xoff[t] = (uint32_t)(min(row, M - 1 - m0) * d * 2 + 16 * (r ^ (row & 15)));
   }
 #pragma unroll
   for (int j = 0; j < TC; ++j) {
@@ -176,29 +160,25 @@ void w4_tiles_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       for (int k = 1; k < nw; ++k) z[u] += *(const f4*)(p + k * WB);
     }
     const int m = m0 + 16 * (b % TT) + r, n = c0 + 16 * (b / TT) + 4 * kq;
-    if (m < M && n < N) {
-      if constexpr (EPI == kEpiShare) epi_share(z[0], rows_of.weight(m), m, n, N, bias, (float*)y);
-      else epi_lane<EPI>(z, m, n, N, bias, aux, act, erf, y);
-    }
+    if (m < M && n < N) epi_lane<EPI>(z, m, n, N, bias, aux, act, erf, y);
   }
 }
 
-template <int EPI, int TT, int TC, class ROWS = AllRows>
+template <int EPI, int TT, int TC>
 hipError_t launch(const uint16_t* x, const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                   const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t d, int group,
-                  const W4Epilogue& ep, hipStream_t stream, const ROWS& rows = ROWS{}) {
+                  const W4Epilogue& ep, hipStream_t stream) {
   const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
   constexpr int NC = epi_gated(EPI) ? 8 * TC : 16 * TC;
-  int mblk = (int)((M + 16 * TT - 1) / (16 * TT));
-  if constexpr (ROWS::kExperts) mblk = (int)expert_blocks(rows.t, 16 * TT);
+  const int mblk = (int)((M + 16 * TT - 1) / (16 * TT));
   const int blocks = (int)((N + NC - 1) / NC) * mblk, per = (blocks + 7) / 8;
   // as many wavefronts as give each the same number of chunks
   const int segs = (int)(d / 128);
   constexpr int most = tile_waves(TT, TC);
   const int rounds = (segs + most - 1) / most, nw = (segs + rounds - 1) / rounds;
-  hipLaunchKernelGGL((w4_tiles_kernel<ROWS, EPI, TT, TC>), dim3(8u * (unsigned)per), dim3(64 * nw), 0, stream, x, qweight,
+  hipLaunchKernelGGL((w4_tiles_kernel<EPI, TT, TC>), dim3(8u * (unsigned)per), dim3(64 * nw), 0, stream, x, qweight,
                      scales, zeros, bias, y, (int)M, (int)N, (int)d, gsh, mblk, blocks, per, ep.aux, act_form(ep.act),
-                     (int)(ep.act == PARO_ACT_GELU), rows);
+                     (int)(ep.act == PARO_ACT_GELU));
   return hipGetLastError();
 }
 
@@ -267,19 +247,6 @@ hipError_t launch_w4_tiles(int epi, const uint16_t* x, const uint8_t* qweight, c
             : epi == kEpiActGrad ? launch_epi<kEpiActGrad>
                                  : launch_epi<kEpiGatedGrad>;
   return go(x, qweight, scales, zeros, bias, y, M, N, d, group, ep, stream);
-}
-
-hipError_t launch_w4_experts_tiles(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
-                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
-                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream) {
-  auto go = [&](auto e) {
-    constexpr int EPI = decltype(e)::value;
-    const ExpertRows<EPI != kEpiShare> rows{t};
-    return launch<EPI, 4, 4>(x, qweight, scales, zeros, bias, (uint16_t*)y, t.R, N, d, group, ep, stream, rows);
-  };
-  if (epi == kEpiGated) return go(std::integral_constant<int, kEpiGated>{});
-  if (epi == kEpiGatedGrad) return go(std::integral_constant<int, kEpiGatedGrad>{});
-  return go(std::integral_constant<int, kEpiShare>{});
 }
 
 }  // namespace paro

@@ -176,6 +176,7 @@ PRODUCTS = [
     (40, 64, 4, 1040, 640, 64, 0.0), (64, 48, 8, 816, 256, 256, 0.1), (130, 100, 4, 400, 384, 128, 0.5),
     (500, 40, 2, 880, 896, 64, 0.0), (150, 50, 4, 784, 128, 128, 0.0), (300, 30, 4, 1296, 1152, 128, 0.05),
     (90, 40, 8, 1056, 768, 256, 0.0), (33, 70, 7, 528, 1408, 64, 0.0), (20, 36, 6, 1040, 1280, 256, 0.0),
+    (700, 100, 4, 80, 768, 128, 0.2), (600, 64, 2, 112, 1152, 64, 0.1),
 ]
 
 
