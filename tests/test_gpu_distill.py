@@ -176,6 +176,23 @@ def test_captured_and_on_another_stream(paro):
             assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_largest(paro):
+    """More than 2^31 logits, as many in a row as there can be, with as many of the teacher's; some rows compared."""
+    M, V, K, T = 2100, 1 << 20, 1024, 1.5
+    print("distill largest", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.empty((M, V), dtype=torch.float16, device="cuda").normal_(0, 2.5, generator=g)
+    values = torch.randn((M, K), device="cuda", generator=g) * 4
+    index = (torch.randperm(V, device="cuda", generator=g)[:K] - torch.arange(M, device="cuda")[:, None]) % V
+    index = index.int()
+    lse = torch.logsumexp(values / T, 1) + 0.1
+    loss, dz = paro.paro_distill_loss(z, values, index, lse=lse, temperature=T, grad_scale=1000.0)
+    at = torch.tensor([0, 2046, 2047, 2048, M - 1], device="cuda")
+    ref = experts.distill(f64(z[at]), f64(values[at]), index[at].cpu().numpy(), f64(lse[at]), None, T, 1000.0, "fp16")
+    within(f64(loss[at]), ref[0], ref[1], "loss")
+    within(f64(dz[at]), ref[2], ref[3], "dz")
+
+
 def test_python_refusals(paro):
     z, values, index, lse = inputs(1, 4, 100, 8, "fp32", "fp32", 1.0)
     with pytest.raises(TypeError):

@@ -429,6 +429,61 @@ def test_transformed_experts(paro):
     within(host(h), ref, tol, "h")
 
 
+def some_rows(c, at):
+    """The chosen rows as a routing of their own, each row one token: offsets, order, tokens."""
+    expert = np.searchsorted(c.offsets, at, side="right") - 1
+    return np.searchsorted(expert, np.arange(c.E + 1)), np.arange(len(at)), c.order[at] // c.k
+
+
+@pytest.mark.parametrize("M,E,k,N,d", [(262144, 9, 8, 1040, 128), (262144, 9, 8, 64, 1152), (1, 1, 1, 16, 1 << 20),
+                                       (1, 1, 1, 1 << 20, 128)])
+def test_largest(paro, M, E, k, N, d):
+    """More than 2^31 values in h, dz and the sums by row; the widest rows of each side. Some rows are compared."""
+    c = Case(paro, M + d, M, E, k, 2 * N, d, 128)
+    R = M * k
+    rng = np.random.default_rng(1)
+    edge = (1 << 31) // max(N, d)
+    at = np.unique(np.clip(np.r_[0, edge - 1:edge + 2, edge // 2 - 1:edge // 2 + 2, c.n - 1, rng.integers(0, c.n, 6)],
+                           0, c.n - 1))
+    offsets, order, tokens = some_rows(c, at)
+    normal = lambda *s: torch.randn(s, device="cuda", dtype=torch.float16)  # noqa: E731
+    x = normal(M, d)
+    w = c.w()
+    log(f"largest gated M={M} E={E} k={k} N={N} d={d}")
+    h = paro.paro_w4_experts_gated(c.r, x, *c.dev, bias=c.bd)
+    ref, tol = experts.gated(offsets, order, 1, host(x[tokens]), w, c.b, "silu")
+    within(host(h[at]), ref, tol, "h")
+    log("  backward")
+    dh = normal(R, N)
+    dx, dz = paro.paro_w4_experts_gated_backward(c.r, x, *c.dev, dh, bias=c.bd)
+    ref, tol = experts.gated_backward_dz(offsets, order, 1, host(x[tokens]), w, c.b, "silu", host(dh[at]))
+    within(host(dz[at]), ref, tol, "dz")
+    some = np.unique(tokens[[0, -1]])
+    rows = np.concatenate([c.place[m * k:(m + 1) * k] for m in some])
+    o, z = np.unique(rows, return_inverse=True)
+    so, _, _ = some_rows(c, o)
+    pair = np.argsort(z)  # the pairs of the chosen tokens, in row order
+    ref, tol = experts.gated_backward_dx(so, pair, k, len(some), w, host(dz[o]))
+    within(host(dx[some]), ref, tol, "dx")
+    del dx, dz, dh, h, c, x
+    torch.cuda.empty_cache()
+    c = Case(paro, M + d + 1, M, E, k, N, d, 128)
+    w = c.w()
+    log("largest combine")
+    hh, dy = normal(R, d), normal(M, N)
+    y = paro.paro_w4_experts_combine(c.r, hh, *c.dev, bias=c.bd)
+    rows = np.concatenate([c.place[m * k:(m + 1) * k] for m in some])
+    o, z = np.unique(rows, return_inverse=True)
+    so, _, _ = some_rows(c, o)
+    pair = np.argsort(z)
+    within(host(y[some]), *experts.combine(so, pair, k, host(hh[o]), w, c.b, c.weights[some], None), "y")
+    log("  backward")
+    dh, dw = paro.paro_w4_experts_combine_backward(c.r, hh, *c.dev, dy, bias=c.bd)
+    ref = experts.combine_backward(so, pair, k, host(hh[o]), w, c.b, c.weights[some], host(dy[some]))
+    within(host(dh[o]), ref[0], ref[1], "dh")
+    within(host(dw[some]), ref[2], ref[3], "dweights")
+
+
 def test_python_refusals(paro):
     c = Case(paro, 1, 8, 4, 2, 64, 256, 128)
     x = dev(c.half(8, 256))
