@@ -7,13 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import experts
-
-
-@pytest.fixture(scope="module")
-def paro():
-    import rotated_w4_linear_amd as p
-    p.load_library()
-    return p
+from test_block_edges_host import FakeStream, FakeTensor, fake, faked, paro  # noqa: F401
 
 
 # ---------------------------------------------------------------------------
@@ -252,3 +246,71 @@ def test_distill_refusals(paro):
                         ({"w": A + 2}, ALIGN), ({"loss": A + 2}, ALIGN)]:
         refused(paro, fn, args(**bad), status)
     assert fn(*args(z=None, values=None, index=None, loss=None, dz=None, M=0)) == 0
+
+
+# ---------------------------------------------------------------------------
+# calls on another stream or device: where their memory is made, what is refused
+# ---------------------------------------------------------------------------
+
+def with_routing(call):
+    def run(p, **k):
+        r = p.Routing(fake(4, 2), fake(4, 2), fake(9), fake(8), fake(8))
+        return call(p, r, **k)
+    return run
+
+
+BLOCK = lambda: (fake(8, 64, 128), fake(8, 64, 2), fake(8, 64, 2))  # noqa: E731
+STREAM_CALLS = {
+    "route": lambda p, **k: p.paro_experts_route(fake(4, 8), 2, **k)._table,
+    "sort": lambda p, **k: p.paro_experts_sort(fake(4, 2), 8, fake(4, 2), **k)._table,
+    "route_backward": lambda p, **k: p.paro_experts_route_backward(fake(4, 8), fake(4, 2), fake(4, 2), fake(4, 2), **k),
+    "gated": with_routing(lambda p, r, **k: p.paro_w4_experts_gated(r, fake(4, 256), *BLOCK(), **k)),
+    "combine": with_routing(lambda p, r, **k: p.paro_w4_experts_combine(r, fake(8, 256), *BLOCK(), **k)),
+    "gated_backward": with_routing(
+        lambda p, r, **k: p.paro_w4_experts_gated_backward(r, fake(4, 256), *BLOCK(), fake(8, 32), **k)),
+    "combine_backward": with_routing(
+        lambda p, r, **k: p.paro_w4_experts_combine_backward(r, fake(8, 256), *BLOCK(), fake(4, 64), **k)),
+    "distill": lambda p, **k: p.paro_distill_loss(fake(4, 100), fake(4, 5), fake(4, 5), **k),
+}
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_memory_belongs_to_the_calls_stream(faked, monkeypatch, name):
+    import torch
+    monkeypatch.setattr(FakeTensor, "dtype", torch.float32, raising=False)
+    s = FakeStream()
+    out = STREAM_CALLS[name](faked, stream=s)
+    assert FakeTensor.made and all(t.stream is s for t in FakeTensor.made)
+    for t in out if isinstance(out, tuple) else (out,):
+        assert t.recorded == ["current"]
+    FakeTensor.made.clear()
+    STREAM_CALLS[name](faked)
+    assert FakeTensor.made and all(t.stream == "current" and not t.recorded for t in FakeTensor.made)
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_stream_of_another_device_is_refused(faked, monkeypatch, name):
+    import torch
+    monkeypatch.setattr(FakeTensor, "dtype", torch.float32, raising=False)
+    s = FakeStream()
+    s.device_index = 1
+    with pytest.raises(ValueError, match="current device"):
+        STREAM_CALLS[name](faked, stream=s)
+
+
+def test_routing_and_workspace_of_another_device_are_refused(faked, monkeypatch):
+    import torch
+    monkeypatch.setattr(FakeTensor, "dtype", torch.float32, raising=False)
+    there = fake(1 << 20)
+    there.get_device = lambda: 1
+    for name in STREAM_CALLS:
+        if name not in ("route_backward", "distill"):
+            with pytest.raises(ValueError, match="current device"):
+                STREAM_CALLS[name](faked, workspace=there)
+    ids = fake(4, 2)
+    ids.get_device = lambda: 1
+    r = faked.Routing(ids, fake(4, 2), fake(9), fake(8), fake(8))
+    with pytest.raises(ValueError, match="routing"):
+        faked.paro_w4_experts_gated(r, fake(4, 256), *BLOCK())
+    with pytest.raises(ValueError, match="routing"):
+        faked.paro_w4_experts_combine(r, fake(8, 256), *BLOCK())
