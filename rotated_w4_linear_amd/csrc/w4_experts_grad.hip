@@ -350,7 +350,7 @@ void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__
   __shared__ __attribute__((aligned(16))) uint32_t T0[4 * kK], T1[4 * kK];
   ExpertTile tile;
   int nb;
-  if (!rows_of.find_tile(blockIdx.x, kM, nblk, tile, nb)) return;
+  if (!rows_of.find_tile_halves(blockIdx.x, kM, nblk, tile, nb)) return;
   if (tile.end - tile.first > kM / 2)
     grad_tile<4, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, d, gsh, part, h, dh);
   else
@@ -364,7 +364,7 @@ hipError_t launch(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qwe
   const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
   const unsigned nblk = (unsigned)((d + kN - 1) / kN);
   const unsigned tiles = nblk * (unsigned)expert_blocks(t, kM);
-  hipLaunchKernelGGL((experts_grad_kernel<GATHER, SHARE>), dim3((tiles + 7) / 8 * 8), dim3(256), 0, stream,
+  hipLaunchKernelGGL((experts_grad_kernel<GATHER, SHARE>), dim3((tiles + 7) / 8 * 8 + 8), dim3(256), 0, stream,
                      ExpertRows<GATHER>{t}, qweight, scales, zeros, dz, (int)P, (int)d, gsh, (int)nblk, part, h, dh);
   return hipGetLastError();
 }

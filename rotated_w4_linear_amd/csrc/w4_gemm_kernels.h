@@ -1043,7 +1043,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
     int m0 = mb * GW_M;
     if constexpr (ROWS::kExperts) {
       ExpertTile tile;
-      if (!rows_of.find_tile(blockIdx.x, GW_M, nblk, tile, nb)) return;
+      if (!rows_of.find_tile_halves(blockIdx.x, GW_M, nblk, tile, nb)) return;
       m0 = tile.first;
       M = tile.end;
       const size_t row0 = (size_t)tile.expert * (GT ? 2 * N : N);  // the expert's first weight row
@@ -1216,7 +1216,7 @@ hipError_t launch_w4_experts_wide_epi(const ExpertRouting& t, const uint16_t* x,
   // (an expert's scales and zeros start at a multiple of 16 rows' groups)
   const bool panel = groups <= kPanelGroups && groups % 8 == 0;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(((unsigned)nblk * (unsigned)mblk + 7) / 8 * 8), dim3(256), 0, stream, x, qweight,
+    hipLaunchKernelGGL(kernel, dim3(((unsigned)nblk * (unsigned)mblk + 7) / 8 * 8 + 8), dim3(256), 0, stream, x, qweight,
                        scales, zeros, bias, (uint16_t*)y, t.R, (int)N, (int)d, gsh, mblk, nblk, 0, nullptr, nullptr, 0,
                        ep.aux, act_form(ep.act), (int)(ep.act == PARO_ACT_GELU), ExpertRows<GATHER>{t});
   };
