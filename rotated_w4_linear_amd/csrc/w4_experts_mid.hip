@@ -6,8 +6,8 @@
 // 64 gate rows, and the same channels' up rows), four wavefronts of 32 weight rows
 // each, and goes over k in chunks of 128. Codes and X' come by load-to-LDS DMA into
 // two stages, each an LDS object of its own; X' is shared by the wavefronts, so there
-// is one barrier a chunk. Four workgroups fit a CU (TT = 4: three) and keep its loads
-// coming. Measured against it, gated 2048 -> 1024, 8 of 64 experts, 768 tokens (90 us)
+// is one barrier a chunk. Four workgroups fit a CU and keep its loads coming. Measured
+// against it, gated 2048 -> 1024, 8 of 64 experts, 768 tokens (64 rows a tile, 90 us)
 // and 16 (28 us): four stages, whose LDS leaves room for fewer workgroups, 161 and
 // 29; 256 weight rows instead of 128, 99 and 38.
 // (w4_tiles_kernel, whose wavefronts share out k and meet in LDS, holds a CU alone
@@ -37,12 +37,11 @@ using namespace w4;
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kRsrcWord3 = 0x00020000;  // gfx9 buffer resource word 3
 constexpr int kWaitVmLgkm0 = 0x70;      // s_waitcnt vmcnt(0) lgkmcnt(0)
-// workgroups that fit a CU at once
-constexpr int mid_slots(int tt) { return tt == 4 ? 3 : 4; }
+constexpr int kSlots = 4;               // workgroups that fit a CU at once
 
 // GSH: log2(group / 64).
 template <int EPI, int TT, int GSH, class ROWS>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(mid_slots(TT))))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kSlots)))
 void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint8_t* __restrict__ qw,
                         const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
                         const uint16_t* __restrict__ bias, uint16_t* y, int N, int d, int nblk, const uint16_t* aux,
@@ -285,16 +284,20 @@ hipError_t launch_group(const ExpertRouting& t, const uint16_t* x, const uint8_t
   return go(t, x, qweight, scales, zeros, bias, y, N, d, ep, stream);
 }
 
-// Rows per tile (blocks of 16) by the mean number of an expert's rows: 16, 32 and 64
-// at the means 12 / 24 / 96 of gated 2048 -> 1024, 64 experts, take 36, 37 and - / 46,
-// 43 and - / -, 109 and 90 us; at 14336 -> 4096, 8 experts, - / 93, 82 and - / -, 197
-// and 172.
+// Rows per tile (blocks of 16) by the mean number of an expert's rows: a tile's rows
+// share the dequantization, which is most of the work from a dozen rows on. 16 | 32 |
+// 48 | 64 rows, microseconds, random numbers of rows:
+//   gated 2048 -> 1024, 64 experts: a mean of 12 32 | 31 | 34 | 39, 24 45 | 44 | 44 |
+//     51, 48 - | 62 | 59 | 61, 96 - | 97 | 90 | 90;
+//   gated 4096 -> 14336, 8 experts: 12 148 | 118 | 122 | 132, 32 - | 179 | 171 | 188,
+//     64 - | 274 | 235 | 234;
+//   1024 -> 512, 128 experts: 12 20 | 21 | 21 | 23, 32 - | 25 | 25 | 28, 96 - | 39 | 39 | 43.
 template <int EPI>
 hipError_t launch_epi(const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight, const uint16_t* scales,
                       const uint8_t* zeros, const uint16_t* bias, void* y, int64_t N, int64_t d, int group,
                       const W4Epilogue& ep, hipStream_t stream) {
   const int64_t E = t.E;
-  auto go = t.R <= 16 * E ? launch_group<EPI, 1> : t.R <= 64 * E ? launch_group<EPI, 2> : launch_group<EPI, 4>;
+  auto go = t.R <= 8 * E ? launch_group<EPI, 1> : t.R <= 32 * E ? launch_group<EPI, 2> : launch_group<EPI, 3>;
   return go(t, x, qweight, scales, zeros, bias, y, N, d, group, ep, stream);
 }
 
