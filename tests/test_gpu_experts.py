@@ -51,7 +51,8 @@ TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
 # ---------------------------------------------------------------------------
 
 ROUTES = [(1, 1, 1), (1, 128, 8), (3, 2, 2), (7, 8, 2), (63, 65, 3), (64, 64, 16), (65, 64, 6), (300, 1000, 8),
-          (1000, 8, 2), (777, 129, 5), (5000, 256, 8), (130, 1024, 16), (128, 1024, 16), (129, 100, 2), (256, 1024, 16), (257, 100, 2), (600, 1024, 16), (70000, 7, 2), (20000, 30, 3), (70, 3, 3), (2000, 200, 7)]
+          (1000, 8, 2), (777, 129, 5), (5000, 256, 8), (130, 1024, 16), (128, 1024, 16), (129, 100, 2), (256, 1024, 16), (257, 100, 2), (600, 1024, 16), (70000, 7, 2), (20000, 30, 3), (70, 3, 3), (2000, 200, 7),
+          (33000, 1024, 16)]
 
 
 def logits_of(rng, M, E, kind):
