@@ -513,7 +513,7 @@ typedef struct paro_routing {
  * order is exact.
  *   logits   device [M][E] of a paro_type, aligned to it.
  *   ids, weights, offsets, order, place: outputs, as above (M == 0: offsets = 0).
- *   1 <= k <= E <= 1024, k <= 16, R <= 2^30.
+ *   1 <= k <= E <= 1024, k <= 16, R < 2^24.
  *   workspace: paro_experts_route_workspace_size(M, E, k) bytes (0 up to 128
  *            tokens), 256-byte aligned; scratch, not shared by calls that may
  *            run at the same time.
@@ -566,7 +566,8 @@ int paro_experts_route_backward(const void* logits, int32_t type, int64_t M, int
  *   residual device fp16 [M][N] or NULL; may be y itself, no other overlap;
  *   y        device fp16 [M][N]; tokens without an expert get the residual, or 0.
  *   N % 16 == 0, d % 128 == 0, d % group == 0, P and d <= 2^21, P d < 2^31; the
- *   tokens times their channels (gated d, combine N) < 2^30, R max(P, d) < 2^38;
+ *   tokens times their channels (gated d, combine N) < 2^30, R max(P, d) < 2^34,
+ *   E max(P, d) < 2^27;
  *   tensors 16-byte aligned. M == 0 is a no-op.
  *   workspace: at least the ..._workspace_size bytes (combine: its rows in fp32,
  *   4 R N bytes, so that a token's sum is rounded once), 256-byte aligned;
@@ -641,7 +642,7 @@ int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t
  *   loss     device fp32 [M].
  *   dz       device [M][V] of z's type, 16-byte aligned: grad_scale dL/dz (the
  *            scale keeps fp16 gradients normal), or NULL; may be z itself.
- *   M < 2^31, 1 <= V <= 2^20, 1 <= K <= 1024; T > 0.
+ *   M < 2^22, 1 <= V <= 2^20, 1 <= K <= 1024; T > 0.
  * Arithmetic: exponentials and their sums over the row in fp32, the entries in
  * fp64; results do not depend on timing. One launch, no workspace.
  * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE, PARO_ERR_ALIGN,

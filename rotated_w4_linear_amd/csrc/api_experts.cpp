@@ -23,7 +23,12 @@ size_t a256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 bool known_type(int32_t t) { return t >= PARO_TYPE_F32 && t <= PARO_TYPE_BF16; }
 
-constexpr int64_t kMaxPairs = int64_t(1) << 30;  // (token, slot) pairs of a call
+// Limits under which every launch has fewer than 2^32 lanes in its grid: pairs of a call;
+// pairs, and experts, times the wider of an expert's sides (a tile of the products has
+// 2048 values by 256 lanes or more, and every expert may end in one that is nearly
+// empty); rows of the loss.
+constexpr int64_t kMaxPairs = (int64_t(1) << 24) - 1, kMaxRowValues = int64_t(1) << 34,
+                  kMaxStack = int64_t(1) << 27, kMaxLossRows = (int64_t(1) << 22) - 1;
 
 bool good_experts(int64_t M, int32_t E, int32_t k) {
   return M >= 0 && E >= 1 && k >= 1 && k <= E;
@@ -33,7 +38,7 @@ int check_experts(const std::string& f, int64_t M, int32_t E, int32_t k, bool* n
   if (!good_experts(M, E, k)) return fail(PARO_ERR_SHAPE, f + ": M >= 0 and 1 <= k <= E");
   if (E > kExpertsMax || k > kExpertsMaxK)
     return fail(PARO_ERR_UNSUPPORTED, f + ": at most 1024 experts, 16 of them for a token");
-  if (M > kMaxPairs / k) return fail(PARO_ERR_UNSUPPORTED, f + ": at most 2^30 pairs of token and expert");
+  if (M > kMaxPairs / k) return fail(PARO_ERR_UNSUPPORTED, f + ": fewer than 2^24 pairs of token and expert");
   *noop = M == 0;
   return PARO_OK;
 }
@@ -62,8 +67,8 @@ int check_product(const std::string& f, const paro_routing* r, const void* x, co
     return fail(PARO_ERR_UNSUPPORTED, f + ": an expert's weights: at most 2^21 rows or channels, fewer than 2^31 values");
   if (r->M * by_token >= (int64_t(1) << 30))
     return fail(PARO_ERR_UNSUPPORTED, f + ": tokens times their channels must be below 2^30");
-  if (r->M * r->k * std::max(P, d) >= (int64_t(1) << 38))
-    return fail(PARO_ERR_UNSUPPORTED, f + ": pairs times channels must be below 2^38");
+  if (r->M * r->k * std::max(P, d) >= kMaxRowValues || r->E * std::max(P, d) >= kMaxStack)
+    return fail(PARO_ERR_UNSUPPORTED, f + ": pairs times channels must be below 2^34, experts times channels below 2^27");
   if (*noop) return PARO_OK;
   if (!x || !qweight || !scales || !zeros || !y) return fail(PARO_ERR_NULL, f + ": NULL tensor");
   if (!r->offsets || !r->order || !r->place || !r->ids || (wants && !r->weights))
@@ -81,7 +86,7 @@ int check_product(const std::string& f, const paro_routing* r, const void* x, co
 bool good_sizes(int64_t M, int32_t E, int32_t k, int64_t P, int64_t d) {
   return good_experts(M, E, k) && M > 0 && E <= kExpertsMax && k <= kExpertsMaxK && M <= kMaxPairs / k && P > 0 &&
          P % 16 == 0 && d > 0 && d % 128 == 0 && P <= (int64_t(1) << 21) && d <= (int64_t(1) << 21) &&
-         P * d < (int64_t(1) << 31) && M * k * std::max(P, d) < (int64_t(1) << 38);
+         P * d < (int64_t(1) << 31) && M * k * std::max(P, d) < kMaxRowValues && E * std::max(P, d) < kMaxStack;
 }
 
 ExpertRouting sizes_only(int64_t M, int32_t E, int32_t k) {
@@ -281,8 +286,8 @@ int paro_distill_loss(const void* z, int32_t z_type, const void* values, int32_t
   const std::string f("paro_distill_loss");
   if (!known_type(z_type) || !known_type(value_type)) return fail(PARO_ERR_VALUE, f + ": unknown type");
   if (M < 0 || V < 1 || K < 1) return fail(PARO_ERR_SHAPE, f + ": M >= 0, V >= 1 and K >= 1");
-  if (M > INT32_MAX || V > (int64_t(1) << 20) || K > 1024)
-    return fail(PARO_ERR_UNSUPPORTED, f + ": at most 2^31 - 1 rows, 2^20 logits and 1024 of the teacher's");
+  if (M > kMaxLossRows || V > (int64_t(1) << 20) || K > 1024)
+    return fail(PARO_ERR_UNSUPPORTED, f + ": fewer than 2^22 rows, at most 2^20 logits and 1024 of the teacher's");
   const float T = (float)temperature, scale = (float)grad_scale;
   if (!(T > 0) || !std::isfinite(T) || !std::isfinite(1.0f / T) || !std::isfinite(scale))
     return fail(PARO_ERR_VALUE, f + ": temperature must be positive, and it and grad_scale finite in fp32");

@@ -133,6 +133,7 @@ def test_route_refusals(paro):
                         ({"type": 3}, VALUE), ({"type": -1}, VALUE), ({"M": -1}, SHAPE), ({"E": 0}, SHAPE),
                         ({"k": 0}, SHAPE), ({"k": 9}, SHAPE), ({"E": 1025}, UNSUPPORTED),
                         ({"E": 64, "k": 17}, UNSUPPORTED), ({"M": 1 << 30}, UNSUPPORTED),
+                        ({"M": 1 << 23}, UNSUPPORTED),
                         ({"logits": A + 2}, ALIGN), ({"ids": A + 2}, ALIGN), ({"ws": None}, WORKSPACE),
                         ({"ws_bytes": 17}, WORKSPACE), ({"ws": A + 128}, ALIGN)]:
         refused(paro, fn, args(**bad), status)
@@ -196,8 +197,13 @@ def test_product_refusals(paro, call):
         refused(paro, fn, product_args(call, routing(paro, **{name: None})), NULL)
         refused(paro, fn, product_args(call, routing(paro, **{name: A + 2})), ALIGN)
     for M, E, k, status in [(-1, 8, 2, SHAPE), (10, 0, 1, SHAPE), (10, 4, 5, SHAPE), (10, 2000, 2, UNSUPPORTED),
-                            (10, 64, 17, UNSUPPORTED), (1 << 30, 8, 2, UNSUPPORTED), (1 << 24, 8, 2, UNSUPPORTED)]:
+                            (10, 64, 17, UNSUPPORTED), (1 << 30, 8, 2, UNSUPPORTED), (1 << 23, 8, 2, UNSUPPORTED)]:
         refused(paro, fn, product_args(call, routing(paro, M=M, E=E, k=k)), status)
+    # limits that keep every grid below 2^32 lanes
+    big = dict(N=1 << 16, d=1 << 13) if call.startswith("gated") else dict(N=1 << 17, d=1 << 13)
+    refused(paro, fn, product_args(call, routing(paro, M=100, E=1024), **big), UNSUPPORTED)  # E P = 2^27
+    wide = dict(N=128, d=1 << 16) if call.startswith("gated") else dict(N=1 << 12, d=1 << 16)
+    refused(paro, fn, product_args(call, routing(paro, M=1 << 14, k=16, E=16), **wide), UNSUPPORTED)  # R d = 2^34
     if call != "gated":
         refused(paro, fn, product_args(call, r, ws=None), WORKSPACE)
         refused(paro, fn, product_args(call, r, ws_bytes=255), WORKSPACE)
@@ -224,7 +230,8 @@ def test_workspace_sizes_of_refused_sizes(paro, call):
     for M, E, k, N, d in [(0, 8, 2, 64, 256), (-1, 8, 2, 64, 256), (10, 0, 2, 64, 256), (10, 8, 0, 64, 256),
                           (10, 8, 9, 64, 256), (10, 8, 2, 0, 256), (10, 8, 2, 24, 256), (10, 8, 2, 64, 0),
                           (10, 8, 2, 64, 64), (10, 8, 2, 1 << 40, 256), (10, 8, 2, 64, 1 << 40),
-                          (1 << 40, 8, 2, 64, 256), (10, 2000, 2, 64, 256)]:
+                          (1 << 40, 8, 2, 64, 256), (10, 2000, 2, 64, 256), (1 << 23, 8, 2, 64, 256),
+                          (10, 1024, 2, 1 << 17, 1 << 13), (1 << 14, 16, 16, 128, 1 << 16)]:
         assert size(M, E, k, N, d) == 0, (M, E, k, N, d)
     if call != "gated":
         assert size(10, 8, 2, 64, 256) >= 10 * 2 * 4 * (256 if call.endswith("backward") else 64)
@@ -241,7 +248,7 @@ def test_distill_refusals(paro):
                         ({"T": inf}, VALUE), ({"T": nan}, VALUE), ({"T": 1e-60}, VALUE), ({"T": 1e-42}, VALUE),
                         ({"scale": inf}, VALUE), ({"scale": 1e40}, VALUE), ({"M": -1}, SHAPE), ({"V": 0}, SHAPE),
                         ({"K": 0}, SHAPE), ({"K": 1025}, UNSUPPORTED), ({"V": (1 << 20) + 1}, UNSUPPORTED),
-                        ({"M": 1 << 31}, UNSUPPORTED), ({"z": A + 4}, ALIGN), ({"dz": A + 8}, ALIGN),
+                        ({"M": 1 << 31}, UNSUPPORTED), ({"M": 1 << 22}, UNSUPPORTED), ({"z": A + 4}, ALIGN), ({"dz": A + 8}, ALIGN),
                         ({"values": A + 2}, ALIGN), ({"index": A + 2}, ALIGN), ({"lse": A + 1}, ALIGN),
                         ({"w": A + 2}, ALIGN), ({"loss": A + 2}, ALIGN)]:
         refused(paro, fn, args(**bad), status)
