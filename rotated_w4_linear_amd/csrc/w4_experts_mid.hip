@@ -11,7 +11,9 @@
 // and 16 (28 us): four stages, whose LDS leaves room for fewer workgroups, 161 and
 // 29; 256 weight rows instead of 128, 99 and 38.
 // (w4_tiles_kernel, whose wavefronts share out k and meet in LDS, holds a CU alone
-// and does nothing else while its operands arrive: 64 tokens, 80 us for 36.)
+// and does nothing else while its operands arrive: 64 tokens, 76 us for 32.)
+// What bounds it: few rows, the stream of the weights (64 tokens: 133 MB in 33 us, 4.0
+// TB/s); from a dozen rows of an expert on the dequantization (777 tokens below).
 //  * X' [16 TT rows][16 pieces of 8 channels], piece p of row t at p ^ t (low four
 //    bits);
 //  * codes of a wavefront [2 tiles][16 rows][4 pieces of 32 codes], piece p of row r at
@@ -19,7 +21,7 @@
 // Scales and zeros: lane l has weight row l of its wavefront, four chunks' at a
 // time in registers, and passes them on: a load touches a line per row, so that
 // loads group by group keep the address path longer than the codes do (777 tokens,
-// 4 of 60 experts, groups of 64, 1408 -> 2064: 74 us).
+// 4 of 60 experts, groups of 64, 1408 -> 2064: 74 us, at the time, for 55).
 #include <type_traits>
 
 #include "expert_rows.h"
@@ -83,18 +85,18 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     woff[j] = (uint32_t)(weight_row(j, row) * half + 16 * ((lane & 3) ^ (row >> 2)));
   }
   // (past the last chunk: the last one again, never read)
-  auto dma_x = [&](int c, uint8_t* xs) {
+  auto dma_x = [&](int c, uint8_t* xs, auto blocks) {
     const int k = min(c, segs - 1);
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+    for (int t = 0; t < decltype(blocks)::value; ++t)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(xs + 4096 * t + 1024 * w), 16, xoff[t], 256 * k, 0, 0);
   };
-  auto dma = [&](int c, uint8_t* xs, uint8_t* cs) {
+  auto dma = [&](int c, uint8_t* xs, uint8_t* cs, auto blocks) {
     const int k = min(c, segs - 1);
 #pragma unroll
     for (int j = 0; j < TC; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(cs + CB * w + 1024 * j), 16, woff[j], 64 * k, 0, 0);
-    dma_x(c, xs);
+    dma_x(c, xs, blocks);
   };
 
   // scales and zeros of weight row `lane` of the wavefront, of four chunks: GQ
@@ -154,10 +156,10 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
   for (int j = 0; j < TC; ++j)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[j][t] = f4{0.f, 0.f, 0.f, 0.f};
-  const int used = (rows + 15) >> 4;  // blocks of 16 rows that there are
 
-  // chunk c, the cq-th of its four
-  auto compute = [&](const uint8_t* xs, const uint8_t* cs, const Scales& q, int cq) {
+  // a chunk, the cq-th of its four, with so many blocks of 16 rows
+  auto compute = [&](const uint8_t* xs, const uint8_t* cs, const Scales& q, int cq, auto blocks) {
+    constexpr int U = decltype(blocks)::value;
     uint32_t mine, second = 0;
     if constexpr (GSH == 0) {
       mine = cq == 0 ? group_of(q, 0) : cq == 1 ? group_of(q, 2) : cq == 2 ? group_of(q, 4) : group_of(q, 6);
@@ -184,16 +186,14 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      h8 b[TT];
+      h8 b[4];
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (t == 0 || t < used) b[t] = *(const h8*)(xs + 4096 * t + 256 * r + 16 * ((4 * kq + i) ^ r));
+      for (int t = 0; t < U; ++t) b[t] = *(const h8*)(xs + 4096 * t + 256 * r + 16 * ((4 * kq + i) ^ r));
 #pragma unroll
       for (int j = 0; j < TC; ++j) {
         const h8 a = dequant8(v[j][i], zz[j], zz64[j], ss[j], one);
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-          if (t == 0 || t < used) acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[t], acc[j][t], 0, 0, 0);
+        for (int t = 0; t < U; ++t) acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[t], acc[j][t], 0, 0, 0);
       }
     }
   };
@@ -204,28 +204,32 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  if (!any) {
-    dma_x(0, X0);
-    for (int c = 0; c < segs; ++c) {
-      sync();
-      dma_x(c + 1, c & 1 ? X0 : X1);
+  // all chunks, with so many blocks of 16 rows (a loop for each: branches between the
+  // products would cost more than they do)
+  auto run = [&](auto blocks) {
+    if (!any) {
+      dma_x(0, X0, blocks);
+      for (int c = 0; c < segs; ++c) {
+        sync();
+        dma_x(c + 1, c & 1 ? X0 : X1, blocks);
+      }
+      return;
     }
-  } else {
     Scales now, next;
     load_scales(0, now);
-    dma(0, X0, C0);
+    dma(0, X0, C0, blocks);
     // chunk c + i in its stage, the other one takes chunk c + i + 1. (Four chunks,
     // which share their scales' loads, in a row and without a branch: the waits stay
     // where they are here.)
     auto chunk = [&](int c, auto at) {
       constexpr int i = decltype(at)::value;
       sync();
-      dma(c + i + 1, i & 1 ? X0 : X1, i & 1 ? C0 : C1);
+      dma(c + i + 1, i & 1 ? X0 : X1, i & 1 ? C0 : C1, blocks);
       if (i == 0) {
         cut(now);
         load_scales(min(c + 4, (segs - 1) & ~3), next);
       }
-      compute(i & 1 ? X1 : X0, i & 1 ? C1 : C0, now, i);
+      compute(i & 1 ? X1 : X0, i & 1 ? C1 : C0, now, i, blocks);
     };
     int c = 0;
     for (; c + 4 <= segs; c += 4) {
@@ -238,7 +242,10 @@ void experts_mid_kernel(ROWS rows_of, const uint16_t* __restrict__ x, const uint
     if (c < segs) chunk(c, std::integral_constant<int, 0>{});
     if (c + 1 < segs) chunk(c, std::integral_constant<int, 1>{});
     if (c + 2 < segs) chunk(c, std::integral_constant<int, 2>{});
-  }
+  };
+  if (TT > 1 && rows > 32) run(std::integral_constant<int, TT>{});
+  else if (TT > 1 && rows > 16) run(std::integral_constant<int, TT < 2 ? TT : 2>{});
+  else run(std::integral_constant<int, 1>{});
   __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);  // (the last DMA lands before the workgroup's LDS is another's)
 
   // acc[j][t][e] = Z[row m0 + 16 t + r][weight row 16 j + 4 kq + e of the wavefront]
