@@ -604,7 +604,8 @@ int paro_w4_experts_combine(const paro_routing* routing, const uint16_t* h, cons
  *   expert); the residual's gradient is dY itself.
  * Arguments, limits and errors as for the forward calls. dX' is summed from dZ
  * rounded to fp16, as it is returned; a bias gradient is the sum of an expert's
- * rows of dZ, or of w dY.
+ * rows of dZ, or of w dY. A row of dZ or dY that is not finite makes gradients of
+ * its own token that are not finite: NaN also where the sum is an infinity.
  */
 size_t paro_w4_experts_gated_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d);
 int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* x, const uint8_t* qweight,

@@ -14,7 +14,8 @@ using namespace w4;
 constexpr int kThreads = 256;
 
 // y[m][n] = residual[m][n] + sum_s sum_p part[p][place[m][s]][n], four channels a
-// lane. Bound by memory: k (splits) fp32 rows read per fp16 row written.
+// lane. Bound by memory: k (splits) fp32 rows read per fp16 row written (2048 tokens,
+// 4 rows of 2048 each: 76 MB in 13 us, in part from the memory-side cache).
 __global__ __launch_bounds__(kThreads) void sum_kernel(ExpertRouting t, const float* __restrict__ part, int splits,
                                                        const uint16_t* residual, uint16_t* y, int N4) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;

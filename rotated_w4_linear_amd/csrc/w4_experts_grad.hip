@@ -33,7 +33,12 @@
 // loads of codes in step 3 beside dz: 631 -> 645 us for 2048 tokens, 2 of 8 experts
 // 14336 -> 4096.)
 // P is a multiple of 16, k-tiles of 64: the last one is the 64 rows at the end,
-// with scale 0 for those that the one before has done already.
+// with scale 0 for those that the one before has done already (an infinite dz at
+// one of those: NaN, where the sum has an infinity).
+//
+// What bounds it: the matrix cores are busy 48% of the time (2048 tokens, 2 of 8
+// experts, 14336 -> 4096: 481 GFLOP in 570 us), the fragments' instructions and
+// the waits for codes and dz beside them the rest.
 #include <algorithm>
 #include <type_traits>
 

@@ -13,7 +13,8 @@
 // (w4_tiles_kernel, whose wavefronts share out k and meet in LDS, holds a CU alone
 // and does nothing else while its operands arrive: 64 tokens, 76 us for 32.)
 // What bounds it: few rows, the stream of the weights (64 tokens: 133 MB in 33 us, 4.0
-// TB/s); from a dozen rows of an expert on the dequantization (777 tokens below).
+// TB/s); from a dozen rows of an expert on the waits for a chunk and the
+// dequantization, each some 40% of the cycles (777 tokens below: 43 us).
 //  * X' [16 TT rows][16 pieces of 8 channels], piece p of row t at p ^ t (low four
 //    bits);
 //  * codes of a wavefront [2 tiles][16 rows][4 pieces of 32 codes], piece p of row r at
