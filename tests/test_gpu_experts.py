@@ -178,6 +178,8 @@ PRODUCTS = [
     (500, 40, 2, 880, 896, 64, 0.0), (150, 50, 4, 784, 128, 128, 0.0), (300, 30, 4, 1296, 1152, 128, 0.05),
     (90, 40, 8, 1056, 768, 256, 0.0), (33, 70, 7, 528, 1408, 64, 0.0), (20, 36, 6, 1040, 1280, 256, 0.0),
     (700, 100, 4, 80, 768, 128, 0.2), (600, 64, 2, 112, 1152, 64, 0.1),
+    # no token has an expert
+    (1, 8, 2, 48, 256, 128, 1.0), (5, 70, 3, 528, 384, 64, 1.0), (700, 4, 2, 272, 512, 256, 1.0),
 ]
 
 
@@ -396,6 +398,42 @@ def test_layer_captured(paro, M, E, k):
                 assert torch.equal(a, b)
         for a, b in zip(eager, want[(i + 1) % 4]):
             assert torch.equal(a, b)
+
+
+def test_two_graphs_share_a_workspace(paro):
+    """Two captured calls of different sizes on one workspace, replayed in turn on one stream: it is scratch, nothing
+    in it outlives a call."""
+    layers = [Layer(paro, 5, 40, 6, 2, 256, 384), Layer(paro, 6, 700, 4, 2, 256, 384)]
+    data = [layer.inputs(2) for layer in layers]
+    ws = torch.randint(0, 255, (1 << 26,), dtype=torch.uint8, device="cuda")
+    log("graphs on one workspace")
+
+    def step(layer, x, logits, dy):
+        r = paro.paro_experts_route(logits, 2, workspace=ws)
+        h = paro.paro_w4_experts_gated(r, x, *layer.up, workspace=ws)
+        y = paro.paro_w4_experts_combine(r, h, *layer.down, residual=x, workspace=ws)
+        dh, dw = paro.paro_w4_experts_combine_backward(r, h, *layer.down, dy, workspace=ws)
+        dx, _ = paro.paro_w4_experts_gated_backward(r, x, *layer.up, dh, workspace=ws)
+        return y, dw, dx
+    want = [[step(layer, *d) for d in ds] for layer, ds in zip(layers, data)]
+    static = [[t.clone() for t in ds[0]] for ds in data]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for layer, st in zip(layers, static):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(layer, *st))
+        graphs.append(g)
+    for i in (1, 0, 1, 1, 0):
+        for st, ds in zip(static, data):
+            for a, b in zip(st, ds[i]):
+                a.copy_(b)
+        for g in graphs:
+            g.replay()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w[i]))
 
 
 def test_layers_on_two_streams(paro):
