@@ -94,8 +94,8 @@ ExpertRouting sizes_only(int64_t M, int32_t E, int32_t k) {
 }
 
 size_t grad_bytes(const ExpertRouting& t, int64_t P, int64_t d, bool share) {
-  if (!experts_grad_wide_fit(t, P, d)) return a256((size_t)experts_grad_rows_splits(t, P, d) * t.R * d * 4);
-  return a256(share ? experts_grad_dots(t, d) : (size_t)t.R * d * 4);
+  if (!experts_grad_wide_fit(t, P, d, share)) return a256((size_t)experts_grad_rows_splits(t, P, d) * t.R * d * 4);
+  return a256(share ? experts_grad_dots(t, d) : (size_t)experts_grad_splits(t, P, d) * t.R * d * 4);
 }
 
 bool known_act(int32_t act) { return act >= PARO_ACT_NONE && act <= PARO_ACT_RELU; }
@@ -238,8 +238,8 @@ int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* 
   ep.act = act;
   hipError_t e = launch_w4_experts(kEpiGatedGrad, t, x, qweight, scales, zeros, bias, dz, N, d, group, ep, stream);
   if (e == hipSuccess && dx) {
-    const bool wide = experts_grad_wide_fit(t, 2 * N, d);
-    const int splits = wide ? 1 : experts_grad_rows_splits(t, 2 * N, d);
+    const bool wide = experts_grad_wide_fit(t, 2 * N, d, false);
+    const int splits = wide ? experts_grad_splits(t, 2 * N, d) : experts_grad_rows_splits(t, 2 * N, d);
     float* part = (float*)workspace;
     e = wide ? launch_w4_experts_grad_part(t, dz, qweight, scales, zeros, part, 2 * N, d, group, stream)
              : launch_w4_experts_grad_rows(t, false, dz, qweight, scales, zeros, part, 2 * N, d, group, stream);
@@ -268,7 +268,7 @@ int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t
   if ((st = check_workspace(f, need, workspace, workspace_bytes)) != PARO_OK) return st;
   float* part = (float*)workspace;
   hipError_t e;
-  if (experts_grad_wide_fit(t, N, d)) {
+  if (experts_grad_wide_fit(t, N, d, true)) {
     e = launch_w4_experts_grad_share(t, dy, qweight, scales, zeros, part, h, dh, N, d, group, stream);
     if (e == hipSuccess)
       e = launch_experts_dots(t, part, (int)(experts_grad_dots(t, d) / 4 / t.R), dy, bias, dweights, N, stream);

@@ -336,9 +336,10 @@ int experts_grad_rows_splits(const ExpertRouting& t, int64_t P, int64_t d);
 hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, const uint16_t* dz,
                                        const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                                        float* part, int64_t P, int64_t d, int group, hipStream_t stream);
-// The same in large tiles for experts of many rows (w4_experts_grad.hip): part [R][d]
-// (dz by row), or dh = w U and the partial dots U . h (dy by token).
-bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d);
+// The same in large tiles for experts of many rows (w4_experts_grad.hip): part
+// [experts_grad_splits][R][d] (dz by row), or dh = w U and the partial dots U . h (dy by token).
+bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d, bool share);
+int experts_grad_splits(const ExpertRouting& t, int64_t P, int64_t d);
 size_t experts_grad_dots(const ExpertRouting& t, int64_t d);
 hipError_t launch_w4_experts_grad_part(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight,
                                        const uint16_t* scales, const uint8_t* zeros, float* part, int64_t P, int64_t d,

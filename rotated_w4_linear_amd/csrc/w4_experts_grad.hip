@@ -62,14 +62,15 @@ constexpr int kN = 256, kM = 256, kK = 64;  // channels and rows per workgroup, 
 __device__ __forceinline__ int aswap(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 // SHARE: dh[r] = w U[r] (fp16) and dots[2 nb + half][r], the sums over 128
-// channels of U[r] h[r]; else part[r] = U[r] (fp32).
+// channels of U[r] h[r]; else part[r] = U[r] (fp32). The sum goes over rows p0 ..
+// p0 + PP - 1 of the expert's P.
 template <int TM, bool GATHER, bool SHARE>
 __device__ __forceinline__ void grad_tile(const ExpertRows<GATHER>& rows_of, const ExpertTile& tile, const int nb,
                                           _Float16* A0, _Float16* A1, _Float16* B0, _Float16* B1, uint32_t* T0,
                                           uint32_t* T1, const uint8_t* __restrict__ qw,
                                           const uint16_t* __restrict__ sc, const uint8_t* __restrict__ zr,
-                                          const uint16_t* __restrict__ dz, const int P, const int d, const int gsh,
-                                          float* __restrict__ part, const uint16_t* __restrict__ h,
+                                          const uint16_t* __restrict__ dz, const int P, const int p0,
+                                          const int PP, const int d, const int gsh, float* __restrict__ part, const uint16_t* __restrict__ h,
                                           uint16_t* __restrict__ dh) {
   constexpr int BM = 64 * TM, CB = BM / 32, NF = 4 * TM;
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
@@ -77,15 +78,15 @@ __device__ __forceinline__ void grad_tile(const ExpertRows<GATHER>& rows_of, con
   const int wn = w & 1, wm = w >> 1;
   const int n0 = kN * nb, m0 = tile.first, rows = tile.end - tile.first;
   const int groups = d >> (6 + gsh), half = d >> 1;
-  const size_t first = (size_t)tile.expert * P;  // the expert's first weight row
-  const int KT = (P + kK - 1) / kK;
+  const size_t first = (size_t)tile.expert * P + p0;  // the first weight row
+  const int KT = (PP + kK - 1) / kK;
   const __amdgpu_buffer_rsrc_t rw =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(qw + first * half), (short)0, P * half, kRsrcWord3);
+      __builtin_amdgcn_make_buffer_rsrc((void*)(qw + first * half), (short)0, PP * half, kRsrcWord3);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(dz + (GATHER ? 0 : (size_t)m0 * P)), (short)0, (GATHER ? rows_tokens(rows_of) : rows) * P * 2,
-      kRsrcWord3);
+      (void*)(dz + (GATHER ? 0 : (size_t)m0 * P) + p0), (short)0,
+      ((GATHER ? rows_tokens(rows_of) : rows) * P - p0) * 2, kRsrcWord3);
   // first weight row of k-tile kt (past the last one: the last again)
-  auto row0 = [&](int kt) { return kt >= KT - 1 ? P - kK : kK * kt; };
+  auto row0 = [&](int kt) { return kt >= KT - 1 ? PP - kK : kK * kt; };
 
   // dz: DMA c of wavefront w fills rows 8 (CB w + c) .. + 7 (rows past the end
   // repeat the last one, never stored)
@@ -118,9 +119,9 @@ __device__ __forceinline__ void grad_tile(const ExpertRows<GATHER>& rows_of, con
   // (those past the last group: the last one's, never used)
   const int trow = tid & 63, tgi = min((n0 >> (6 + gsh)) + (tid >> 6), groups - 1);
   const __amdgpu_buffer_rsrc_t rs =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(sc + first * groups), (short)0, P * groups * 2, kRsrcWord3);
+      __builtin_amdgcn_make_buffer_rsrc((void*)(sc + first * groups), (short)0, PP * groups * 2, kRsrcWord3);
   const __amdgpu_buffer_rsrc_t rz =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(zr + first * groups), (short)0, P * groups, kRsrcWord3);
+      __builtin_amdgcn_make_buffer_rsrc((void*)(zr + first * groups), (short)0, PP * groups, kRsrcWord3);
   const uint32_t zoff = (uint32_t)(trow * groups + tgi);
   struct Scale {
     uint32_t s, z;
@@ -134,7 +135,7 @@ __device__ __forceinline__ void grad_tile(const ExpertRows<GATHER>& rows_of, con
   auto put_scale = [&](int done, const Scale& q, uint32_t* t) {
     t[tid] = (trow < done ? 0u : q.s & 0xffffu) | half_bits(1024.0f + (float)(q.z & 0xffu)) << 16;
   };
-  auto done_rows = [&](int kt) { return kt >= KT - 1 ? kK * KT - P : 0; };
+  auto done_rows = [&](int kt) { return kt >= KT - 1 ? kK * KT - PP : 0; };
   struct Rows {  // of a thread's eight rows: scale | 1024 + z
     u4 v[2];
   };
@@ -344,48 +345,70 @@ __device__ __forceinline__ void grad_tile(const ExpertRows<GATHER>& rows_of, con
 }
 
 // Tiles of up to 256 rows. An expert's last one may be short: up to 128 rows in
-// wavefront tiles of half the height, which take 0.6 of a whole tile's time.
+// wavefront tiles of half the height, which take 0.6 of a whole tile's time. Where
+// there are few tiles, `splits` workgroups share out a tile's sum (sums in part
+// [splits][R][d]).
 template <bool GATHER, bool SHARE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
 void experts_grad_kernel(ExpertRows<GATHER> rows_of, const uint8_t* __restrict__ qw, const uint16_t* __restrict__ sc,
                          const uint8_t* __restrict__ zr, const uint16_t* __restrict__ dz, int P, int d, int gsh,
-                         int nblk, float* __restrict__ part, const uint16_t* __restrict__ h,
+                         int nblk, int splits, float* __restrict__ part, const uint16_t* __restrict__ h,
                          uint16_t* __restrict__ dh) {
   __shared__ __attribute__((aligned(1024))) _Float16 A0[kN * kK], A1[kN * kK], B0[kM * kK], B1[kM * kK];
   __shared__ __attribute__((aligned(16))) uint32_t T0[4 * kK], T1[4 * kK];
   ExpertTile tile;
   int nb;
-  if (!rows_of.find_tile_halves(blockIdx.x, kM, nblk, tile, nb)) return;
+  int b = blockIdx.x, p0 = 0, PP = P;
+  if constexpr (!SHARE) {
+    const int per = gridDim.x / splits, sp = b / per, KT = (P + kK - 1) / kK;
+    b -= sp * per;
+    p0 = kK * (int)((int64_t)KT * sp / splits);
+    PP = (sp + 1 == splits ? P : kK * (int)((int64_t)KT * (sp + 1) / splits)) - p0;
+    part += (size_t)sp * rows_of.t.R * d;
+  }
+  if (!rows_of.find_tile_halves(b, kM, nblk, tile, nb)) return;
   if (tile.end - tile.first > kM / 2)
-    grad_tile<4, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, d, gsh, part, h, dh);
+    grad_tile<4, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, p0, PP, d, gsh, part, h,
+                                  dh);
   else
-    grad_tile<2, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, d, gsh, part, h, dh);
+    grad_tile<2, GATHER, SHARE>(rows_of, tile, nb, A0, A1, B0, B1, T0, T1, qw, sc, zr, dz, P, p0, PP, d, gsh, part, h,
+                                  dh);
 }
 
 template <bool GATHER, bool SHARE>
 hipError_t launch(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight, const uint16_t* scales,
-                  const uint8_t* zeros, int64_t P, int64_t d, int group, float* part, const uint16_t* h, uint16_t* dh,
-                  hipStream_t stream) {
+                  const uint8_t* zeros, int64_t P, int64_t d, int group, int splits, float* part, const uint16_t* h,
+                  uint16_t* dh, hipStream_t stream) {
   const int gsh = group == 64 ? 0 : group == 128 ? 1 : 2;
   const unsigned nblk = (unsigned)((d + kN - 1) / kN);
   const unsigned tiles = nblk * (unsigned)expert_blocks(t, kM);
-  hipLaunchKernelGGL((experts_grad_kernel<GATHER, SHARE>), dim3((tiles + 7) / 8 * 8 + 8), dim3(256), 0, stream,
-                     ExpertRows<GATHER>{t}, qweight, scales, zeros, dz, (int)P, (int)d, gsh, (int)nblk, part, h, dh);
+  hipLaunchKernelGGL((experts_grad_kernel<GATHER, SHARE>), dim3(((tiles + 7) / 8 * 8 + 8) * (unsigned)splits), dim3(256), 0, stream,
+                     ExpertRows<GATHER>{t}, qweight, scales, zeros, dz, (int)P, (int)d, gsh, (int)nblk, splits,
+                     part, h, dh);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Experts of enough rows, and a whole k-tile.
-// Whether the gradient is taken in these tiles, from a mean of 16 rows on if there are
-// tiles for all CUs, else of 160. Microseconds of w4_input_grad_rows_kernel's way | this:
+// Workgroups that share a tile's sum over P rows, at least 16 k-tiles each: as many as
+// make one and a half tiles a CU. (gated 4096 -> 14336, 8 experts, one workgroup a tile
+// | three: a mean of 128 rows 727 | 424 us, 192 718 | 537.)
+int experts_grad_splits(const ExpertRouting& t, int64_t P, int64_t d) {
+  const int64_t blocks = std::max<int64_t>(std::min<int64_t>(t.E, t.R), t.R / kM) * ((d + kN - 1) / kN);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({384 / blocks, P / (16 * kK), 4}));
+}
+
+// Whether the gradient is taken in these tiles (share: of combine, whose tiles are not
+// shared out), from a mean of 16 rows on if there are tiles for all CUs, else of 160.
+// Microseconds of w4_input_grad_rows_kernel's way | this:
 //   of 2048 -> 1024, 64 experts: a mean of 8 rows 47 | 46, 16: 55 | 48, 64: 107 | 67;
 //   of gated 1408 -> 2048, 60 experts: 16: 151 | 172, 48: 225 | 242, 96: 395 | 356;
-//   of gated 4096 -> 14336, 8 experts (128 tiles): 32: 532 | 604, 128: 966 | 1096,
-//     192: 1290 | 1231.
-bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d) {
-  const int64_t E = t.E;
-  return P >= kK && t.R >= (E * d >= kN * 256 ? 16 : 160) * E;
+//   of 14336 <- 4096, 8 experts (128 tiles): 32: 164 | 200, 128: 266 | 312, 192: 370 | 321;
+//   of gated 4096 -> 14336, 8 experts (128 tiles, shared out), dz included: 16: 469 | 476,
+//     32: 532 | 513, 64: 626 | 551, 128: 966 | 793.
+bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d, bool share) {
+  const int64_t E = t.E, splits = share ? 1 : experts_grad_splits(t, P, d);
+  return P >= kK && t.R >= (E * d * splits >= kN * 256 ? 16 : 160) * E;
 }
 
 // partial dots of the weights' gradients: [2 ceil(d / 256)][R]
@@ -394,13 +417,14 @@ size_t experts_grad_dots(const ExpertRouting& t, int64_t d) { return (size_t)((d
 hipError_t launch_w4_experts_grad_part(const ExpertRouting& t, const uint16_t* dz, const uint8_t* qweight,
                                        const uint16_t* scales, const uint8_t* zeros, float* part, int64_t P, int64_t d,
                                        int group, hipStream_t stream) {
-  return launch<false, false>(t, dz, qweight, scales, zeros, P, d, group, part, nullptr, nullptr, stream);
+  return launch<false, false>(t, dz, qweight, scales, zeros, P, d, group, experts_grad_splits(t, P, d), part, nullptr,
+                              nullptr, stream);
 }
 
 hipError_t launch_w4_experts_grad_share(const ExpertRouting& t, const uint16_t* dy, const uint8_t* qweight,
                                         const uint16_t* scales, const uint8_t* zeros, float* dots, const uint16_t* h,
                                         uint16_t* dh, int64_t P, int64_t d, int group, hipStream_t stream) {
-  return launch<true, true>(t, dy, qweight, scales, zeros, P, d, group, dots, h, dh, stream);
+  return launch<true, true>(t, dy, qweight, scales, zeros, P, d, group, 1, dots, h, dh, stream);
 }
 
 }  // namespace paro

@@ -178,6 +178,8 @@ PRODUCTS = [
     (500, 40, 2, 880, 896, 64, 0.0), (150, 50, 4, 784, 128, 128, 0.0), (300, 30, 4, 1296, 1152, 128, 0.05),
     (90, 40, 8, 1056, 768, 256, 0.0), (33, 70, 7, 528, 1408, 64, 0.0), (20, 36, 6, 1040, 1280, 256, 0.0),
     (700, 100, 4, 80, 768, 128, 0.2), (600, 64, 2, 112, 1152, 64, 0.1),
+    # (the gated gradient's tiles shared out: 2, 3 and 4 ways, the last range not whole k-tiles)
+    (200, 4, 1, 1552, 4096, 128, 0.0), (150, 8, 2, 1600, 2304, 64, 0.1), (140, 3, 2, 2064, 1152, 128, 0.0),
     # no token has an expert
     (1, 8, 2, 48, 256, 128, 1.0), (5, 70, 3, 528, 384, 64, 1.0), (700, 4, 2, 272, 512, 256, 1.0),
 ]
