@@ -319,7 +319,7 @@ hipError_t launch_experts_route_backward(const void* logits, int type, int64_t M
 hipError_t launch_w4_experts_rows(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                   const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                   int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);
-// The same for a few rows to some dozens of an expert (w4_experts_mid.hip).
+// The same for up to some hundred rows of an expert (w4_experts_mid.hip).
 hipError_t launch_w4_experts_mid(int epi, const ExpertRouting& t, const uint16_t* x, const uint8_t* qweight,
                                  const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias, void* y,
                                  int64_t N, int64_t d, int group, const W4Epilogue& ep, hipStream_t stream);

@@ -565,7 +565,7 @@ void w4_gemm_wide_kernel(const uint16_t* __restrict__ x, const uint8_t* __restri
   const int wn = w % NWAV, wm = w / NWAV;                   // the wavefront's n and m blocks
   // XCD-aware tile order, as in w4_gemm_kernel
   const int xcd = blockIdx.x & 7;
-  const int nbx = ROWS::kExperts ? 1 : (nblk - xcd + 7) >> 3;  // (experts: find_tile says where)
+  const int nbx = ROWS::kExperts ? 1 : (nblk - xcd + 7) >> 3;  // (experts: find_tile_halves says where)
   if (nbx <= 0) return;
   const int groups = d >> (6 + gsh);
   const int L = d / GB_K;  // k-tiles per tile
