@@ -204,8 +204,9 @@ def distill(z, values, index, lse, row_weight, T, scale, kind):
             factor = A if lse is None or left == 0 else A - P / Q
             grad = e / total * np.where(entry, A, factor) - target
             # the fp32 sum of exponentials: arguments within 3 2^-24 of their size, a few ulps of exp2, at most
-            # V / 256 + 16 additions and as many rescalings of a lane's sum, a tree over the lanes
-            span = np.abs(y[np.isfinite(y)]).max()
+            # V / 256 + 16 additions and as many rescalings of a lane's sum, a tree over the lanes. (What is more
+            # than 100 below the largest adds less than 2^20 e^-99 of the sum, whatever its argument's error.)
+            span = min(np.abs(y[np.isfinite(y)]).max(), 100.0)
             sigma = U32 * (3 * span + 2 * (V / 256) + 80)
             rho = U32 * (3 * np.where(np.isfinite(y), np.abs(y), 0.0) + 8)
             share = Q if lse is not None else 1.0

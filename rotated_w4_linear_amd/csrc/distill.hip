@@ -219,18 +219,18 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
     }
   };
 
-  // pass 1: maximum and sum of 2^(c x - shift), shift = c max rounded (0 while
-  // nothing is above -inf): one fma and one exp2 a logit, the fma's rounding alone
+  // pass 1: maximum and sum of 2^(c (x - max)) (0 for max while nothing is above -inf).
+  // The difference comes first: fma(x, c, -(c max rounded)), one instruction less, has
+  // the rounding of c max in it, which is any size where the maximum so far is a mask's
+  // large number (and NaN follows from infinity times 0).
   const float c = (float)(1.4426950408889634 * it);
   float mx = -kInf, shift = 0.0f, sum = 0.0f;
-  auto power = [&](float x, float of) { return __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, -of)); };
+  auto power = [&](float x, float of) { return __builtin_amdgcn_exp2f((x - of) * c); };
   auto taken = [&](int j) { return (bits[(j + skip) >> 5] >> ((j + skip) & 31)) & 1u; };
   auto more = [&](float hi) {
     if (hi > mx) {
-      const float to = hi * c;
-      sum = mx > -kInf ? sum * __builtin_amdgcn_exp2f(shift - to) : 0.0f;
-      mx = hi;
-      shift = to;
+      sum = mx > -kInf ? sum * power(mx, hi) : 0.0f;
+      mx = shift = hi;
     }
   };
   auto one = [&](int j) {
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   // maximum (0 where nothing is above -inf). A NaN: fmax passes over it, the sum
   // does not.
   auto rescaled = [&](float s, float of, float to) {
-    return of < to && s == s ? (of > -kInf ? s * __builtin_amdgcn_exp2f(of * c - to * c) : 0.0f) : s;
+    return of < to && s == s ? (of > -kInf ? s * power(of, to) : 0.0f) : s;
   };
   const float wtop = wave_max(mx);
   const float wtotal = wave_sum(rescaled(sum, mx, wtop));
@@ -277,19 +277,18 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   const float top = wave_max(wmax[lane & (NW - 1)]);
   const float mine = rescaled(wsum[lane & (NW - 1)], wmax[lane & (NW - 1)], top);
   const double left = wave_sum(lane < NW ? (double)mine : 0.0);
-  const float tshift = top > -kInf ? top * c : 0.0f;
+  const float tshift = top > -kInf ? top : 0.0f;
 
-  // the entries: the student's mass there, each index once (the lowest entry's).
-  // unit: log of e^(z / T) in the sum's unit of a logit equal to the largest
+  // the entries: the student's mass there, each index once (the lowest entry's), in
+  // the sum's unit, e^(top / T)
   const double g = (double)weight * a.temperature * a.grad_scale;
   double total = left;
   if (w == own) {
-    const double unit = ((double)top * (double)c - (double)tshift) * 0.6931471805599453;
     double mass = 0.0;
 #pragma unroll 1
     for (int i = lane; i < K; i += 64) {
       if (index[i] < 0) continue;
-      const double v = exp(((double)zj[i] - (double)top) * it + unit);
+      const double v = exp(((double)zj[i] - (double)top) * it);
       e[i] = v;
       bool first = true;
       if (twice)
@@ -302,14 +301,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   }
   __syncthreads();
   if (w == own) {  // the loss, and the gradient at the entries, with the masses of all entries of an index
-    const double unit = ((double)top * (double)c - (double)tshift) * 0.6931471805599453;
     double loss = 0.0;
     const double inverse = 1.0 / total;
 #pragma unroll 1
     for (int i = lane; i < K; i += 64) {
       if (index[i] < 0) continue;
       const double pi = p[i] * pscale;
-      if (pi != 0.0) loss += pi * (log(pi) - (((double)zj[i] - (double)top) * it + unit));
+      if (pi != 0.0) loss += pi * (log(pi) - ((double)zj[i] - (double)top) * it);
       double all = pi;
       if (twice) {
         all = 0.0;

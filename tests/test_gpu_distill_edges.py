@@ -1,0 +1,104 @@
+"""The distillation loss where its numbers are at an edge: finite masks, mass that only fp64 sees; on the GPU against
+the fp64 oracle, value by value, within its bounds (oracle/experts.py)."""
+import numpy as np
+import pytest
+
+from oracle import experts
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+MASKS = {"lowest": None, "-1e30": -1e30, "-1e10": -1e10, "-65504": -65504.0}
+
+
+@pytest.fixture(scope="module")
+def paro():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import rotated_w4_linear_amd as p
+    p.load_library()
+    return p
+
+
+def f64(t):
+    torch.cuda.synchronize()
+    return t.double().cpu().numpy()
+
+
+def within(got, ref, tol, what):
+    assert got.shape == ref.shape, what
+    with np.errstate(invalid="ignore"):
+        bad = ~((np.abs(got - ref) <= tol) | (got == ref))
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} outside, first at {np.argwhere(bad)[0]}: "
+                           f"{got[bad][0]} against {ref[bad][0]}, bound {np.broadcast_to(tol, ref.shape)[bad][0]}")
+
+
+def check(paro, z, values, index, lse, T, kind, what, scale=1.0):
+    print(what, flush=True)
+    ref = experts.distill(f64(z), f64(values), index.cpu().numpy(), None if lse is None else f64(lse), None, T, scale,
+                          kind)
+    assert not np.isnan(ref[0]).any() and not np.isnan(ref[2]).any() and np.isfinite(ref[3]).all(), what
+    loss, dz = paro.paro_distill_loss(z, values, index, lse=lse, temperature=T, grad_scale=scale)
+    within(f64(loss), ref[0], ref[1], what + " loss")
+    within(f64(dz), ref[2], ref[3], what + " dz")
+    over = z.clone()
+    again, _ = paro.paro_distill_loss(over, values, index, lse=lse, temperature=T, grad_scale=scale, dz=over)
+    torch.cuda.synchronize()
+    assert torch.equal(again, loss) and torch.equal(over, dz)
+
+
+def lowest(kind, mask):
+    low = torch.finfo(TYPES[kind]).min
+    return low if MASKS[mask] is None else max(MASKS[mask], low)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("mask", list(MASKS))
+@pytest.mark.parametrize("V", [2048, 4099, 131072])
+def test_finite_masks(paro, V, mask, kind, rest):
+    """Masks of finite numbers, as an attention or vocabulary mask writes them: over whole lanes, at the row's start, at
+    its end, over most of it, over every second logit, over an entry, over the whole row and over all but one."""
+    M, K = 9, 12
+    g = torch.Generator().manual_seed(V + len(mask))
+    z = torch.randn((M, V), generator=g) * 2.5
+    low = lowest(kind, mask)
+    open_ = [slice(0, V - 548), slice(548, V), slice(V // 2, V // 2 + 40), slice(3, 60), slice(V - 40, V),
+             slice(0, V, 2), slice(0, V), slice(0, 0), slice(700, 701)]
+    masked = torch.full_like(z, low)
+    index = torch.empty((M, K), dtype=torch.int32)
+    for m, s in enumerate(open_):
+        masked[m, s] = z[m, s]
+        at = torch.arange(V)[s]
+        pick = at[torch.randperm(len(at), generator=g)[:K]]
+        index[m] = -1
+        index[m, :len(pick)] = pick
+    index[7, :5] = torch.tensor([0, 9, 300, 301, V - 1])
+    index[6, 3] = 17
+    index[6, 4:] = torch.where(index[6, 4:] == 17, -1, index[6, 4:])
+    masked[6, 17] = low  # the student never takes what the teacher gives a mass
+    t = torch.gather(z, 1, index.long().clamp(min=0))
+    for T in (0.5, 1.0, 2.0):
+        if rest:
+            # (the student has mass outside the entries in every row but the last, where the teacher has none)
+            full = torch.logsumexp(t.double().masked_fill(index < 0, -float("inf")) / T, 1)
+            lse = (full + torch.tensor([0.25] * 8 + [-1e-3])).float().cuda()
+        v = t.cuda()
+        check(paro, masked.to(TYPES[kind]).cuda(), v, index.cuda(), lse if rest else None, T, kind,
+              f"finite masks V={V} {mask} {kind} rest={rest} T={T}")
+
+
+@pytest.mark.parametrize("shift", [1e6, -1e10, 1e20, -1e20])
+def test_large_logits_differ_exactly(paro, shift):
+    """Logits of which only the differences matter, however large they are: each a multiple of their spacing."""
+    M, V, K = 4, 3001, 6
+    g = torch.Generator().manual_seed(3)
+    step = float(np.spacing(np.float32(abs(shift))))
+    steps = torch.randint(-20, 1, (M, V), generator=g).double()
+    z = (shift + steps * step).float()
+    assert torch.equal((z.double() - shift).abs() <= 21 * step, torch.ones((M, V), dtype=torch.bool))
+    index = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(M)]).int()
+    values = torch.randn((M, K), generator=g)
+    check(paro, z.cuda(), values.cuda(), index.cuda(), None, 2.0 * step, "fp32", f"large logits shift={shift}")
