@@ -195,30 +195,40 @@ def distill(z, values, index, lse, row_weight, T, scale, kind):
             top = z[m].max()
             y = (z[m] - top) / T
             e = np.exp(y)
-            total, left = e.sum(), e[~entry].sum()
+            total = e.sum()
+            # the rest by itself, in the unit of its own largest: it may be far below the entries
+            far = z[m][~entry].max() if lse is not None and not entry.all() else top
+            own_y = (z[m] - far) / T if far > -np.inf else np.full(V, -np.inf)
+            outside = np.where(entry, 0.0, np.exp(own_y)) if lse is not None else e
+            left = outside.sum()
             own = np.where(p_i > 0, p_i * (np.log(p_i) - y[j]), np.where(p_i == 0, 0.0, np.nan)).sum()
             value = own + A * np.log(total)
+            log_left = np.log(left) + (far - top) / T
             if P > 0:
-                value += P * (np.log(P) - np.log(left))
-            Q = left / total
-            factor = A if lse is None or left == 0 else A - P / Q
-            grad = e / total * np.where(entry, A, factor) - target
+                value += P * (np.log(P) - log_left)
+            Q = left * np.exp((far - top) / T) / total
+            r = outside / left if left > 0 else np.zeros(V)  # the student among the rest
+            grad = np.where(entry, A * e / total, r * (A * Q - P) if lse is not None else A * e / total) - target
             # the fp32 sum of exponentials: arguments within 3 2^-24 of their size, a few ulps of exp2, at most
             # V / 256 + 16 additions and as many rescalings of a lane's sum, a tree over the lanes. (What is more
             # than 100 below the largest adds less than 2^20 e^-99 of the sum, whatever its argument's error.)
-            span = min(np.abs(y[np.isfinite(y)]).max(), 100.0)
+            span = min(np.abs(own_y[np.isfinite(own_y) & (outside > 0)]).max(initial=0.0), 100.0)
             sigma = U32 * (3 * span + 2 * (V / 256) + 80)
-            rho = U32 * (3 * np.where(np.isfinite(y), np.abs(y), 0.0) + 8)
+            rho = U32 * (3 * np.where(np.isfinite(own_y), np.abs(own_y), 0.0) + 8)
             share = Q if lse is not None else 1.0
             off = abs(Q * A - P) * sigma + P * sigma ** 2 if lse is not None else A * sigma
             loss[m] = w * T * T * value
-            size = abs(own) + abs(np.log(total)) + abs(P * np.log(max(P, 1e-300))) + 1
+            size = abs(own) + abs(np.log(total)) + abs(P * np.log(max(P, 1e-300))) + 1 + \
+                (abs(P * log_left) if P > 0 else 0.0)
             loss_tol[m] = abs(w) * T * T * (off + 1e-13 * size)
             loss_tol[m] += U32 * (abs(loss[m]) + loss_tol[m]) + 2.0 ** -150
             g = w * T * scale
             dz[m] = g * grad
-            slope = sigma * (A * share + (P / Q if lse is not None and left > 0 else 0.0))
-            err = np.abs(g) * (e / total) * np.where(entry, A * share * sigma, rho * np.abs(factor) + slope) + \
-                2 * U32 * np.abs(dz[m]) + 1e-14 * np.abs(g)
+            if lse is None:
+                err = np.abs(g) * (e / total) * np.where(entry, A * sigma, rho * A + A * sigma)
+            else:
+                err = np.abs(g) * np.where(entry, e / total * A * share * sigma,
+                                           r * (rho * abs(A * Q - P) + sigma * (A * Q * Q + P)))
+            err = err + 2 * U32 * np.abs(dz[m]) + 1e-14 * np.abs(g)
             dz_tol[m] = stored(dz[m], err, kind)
     return loss, loss_tol, dz, dz_tol

@@ -12,8 +12,9 @@
 // the rest is a class of its own); the entries are done in fp64 by one
 // wavefront, and the sum of everything is the rest's plus the entries': where
 // teacher and student agree, L is a small difference, and an error of the rest's
-// sum then enters by Q - P only. A second pass reads z again, from the memory-side
-// cache, and writes the gradient.
+// sum then enters by Q - P only. The rest has a maximum of its own: below the
+// entries' by 88 T its exponentials would all be 0, and the loss infinite. A second
+// pass reads z again, from the memory-side cache, and writes the gradient.
 //
 // What bounds it: with a gradient memory (4096 rows of 131072 bf16 in 503 us, 4.3 TB/s
 // of one read and one write, the second read in part from the cache; 574 with stores
@@ -156,6 +157,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   for (int i = tid; i < words; i += NT) bits[i] = 0;
   __syncthreads();
   double psum = 0.0, pscale = 1.0, P = 0.0, A = 1.0;
+  float zmax = -kInf;  // the student's largest at the entries
   bool twice = false;
   if (w == own) {
     float tmax = -kInf;
@@ -168,7 +170,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
       index[i] = in ? j : -1;
       p[i] = (double)t * it;
       if (!in) continue;
-      zj[i] = i < 64 ? z0 : Z::value(z[j]);
+      const float x = i < 64 ? z0 : Z::value(z[j]);
+      zj[i] = x;
+      zmax = fmaxf(zmax, x);
       entries = entries || t > -kInf || t != t;
       tmax = fmaxf(tmax, t);
       const uint32_t b = 1u << ((j + skip) & 31);
@@ -234,30 +238,29 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
     }
   };
   auto one = [&](int j) {
+    if (rest && taken(j)) return;
     const float x = Z::value(z[j]);
     more(x);
-    if (!rest || !taken(j)) sum += power(x, shift);
+    sum += power(x, shift);
   };
   for (int j = tid; j < head; j += NT) one(j);
   for (int j = tail0 + tid; j < V; j += NT) one(j);
   stream([&](const u4& v, int at) {
     float x[VE], hi = -kInf;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      x[i] = Vec<Z>::get(v, i);
-      hi = fmaxf(hi, x[i]);
-    }
-    more(hi);
+    for (int i = 0; i < VE; ++i) x[i] = Vec<Z>::get(v, i);
     uint32_t out = 0;
     if (rest) out = bits[(vbase + at) * VE >> 5] >> ((vbase + at) * VE & 31) & ((1u << VE) - 1);
-    float part = 0.0f;
-    if (out == 0) {
+    if (out != 0) {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) part += power(x[i], shift);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) part += (out >> i) & 1u ? 0.0f : power(x[i], shift);
+      for (int i = 0; i < VE; ++i) x[i] = (out >> i) & 1u ? -kInf : x[i];
     }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) hi = fmaxf(hi, x[i]);
+    more(hi);
+    float part = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) part += power(x[i], shift);
     sum += part;
   });
   // a lane's, a wavefront's, then the workgroup's: sums in the unit of the larger
@@ -280,24 +283,30 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   const float tshift = top > -kInf ? top : 0.0f;
 
   // the entries: the student's mass there, each index once (the lowest entry's), in
-  // the sum's unit, e^(top / T)
+  // the unit of the largest logit of all, e^(ref / T); below: that of the sum, in it
   const double g = (double)weight * a.temperature * a.grad_scale;
-  double total = left;
+  double total = left, ref = top, below = 0.0;
   if (w == own) {
+    if (rest) {
+      ref = fmaxf(top, wave_max(zmax));
+      below = left > 0.0 ? ((double)top - ref) * it : 0.0;
+    }
     double mass = 0.0;
 #pragma unroll 1
     for (int i = lane; i < K; i += 64) {
       if (index[i] < 0) continue;
-      const double v = exp(((double)zj[i] - (double)top) * it);
+      const double v = exp(((double)zj[i] - ref) * it);
       e[i] = v;
       bool first = true;
       if (twice)
         for (int b = 0; b < i; ++b) first = first && index[b] != index[i];
       if (rest && first) mass += v;
     }
-    total = left + wave_sum(mass);  // (left holds everything without a class for the rest)
-    // (a student without mass outside the entries has no gradient there)
-    if (lane == 0) factor = (float)(g * (rest && left > 0.0 ? A / total - P / left : A / total));
+    if (rest) total = left * exp(below) + wave_sum(mass);
+    // (left holds everything without a class for the rest; a student without mass
+    // outside the entries has no gradient there)
+    const double Q = left * exp(below) / total;
+    if (lane == 0) factor = (float)(rest ? (left == 0.0 ? 0.0 : g * (A * Q - P) / left) : g * A / total);
   }
   __syncthreads();
   if (w == own) {  // the loss, and the gradient at the entries, with the masses of all entries of an index
@@ -307,7 +316,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
     for (int i = lane; i < K; i += 64) {
       if (index[i] < 0) continue;
       const double pi = p[i] * pscale;
-      if (pi != 0.0) loss += pi * (log(pi) - ((double)zj[i] - (double)top) * it);
+      if (pi != 0.0) loss += pi * (log(pi) - ((double)zj[i] - ref) * it);
       double all = pi;
       if (twice) {
         all = 0.0;
@@ -320,6 +329,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
     const double part = lane == 0 ? total : lane == 1 ? P : left, by = lane == 0 ? A : lane == 1 ? P : -P;
     const double whole = lane < 3 && by != 0.0 ? by * log(part) : 0.0;
     loss += wave_sum(whole);
+    if (P != 0.0) loss -= P * below;
     if (lane == 0) {
       a.loss[m] = (float)(loss * ((double)weight * a.temperature * a.temperature));
     }

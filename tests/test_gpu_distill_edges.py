@@ -102,3 +102,42 @@ def test_large_logits_differ_exactly(paro, shift):
     index = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(M)]).int()
     values = torch.randn((M, K), generator=g)
     check(paro, z.cuda(), values.cuda(), index.cuda(), None, 2.0 * step, "fp32", f"large logits shift={shift}")
+
+
+@pytest.mark.parametrize("scale", [1.0, 65536.0])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("far", [60.0, 95.0, 130.0, 300.0, 20000.0])
+@pytest.mark.parametrize("V", [200, 32001])
+def test_rest_far_below_the_entries(paro, V, far, kind, scale):
+    """A student that is sure of the teacher's entries: its mass outside is far below what fp32 holds beside them, and
+    still has a logarithm and a gradient. T takes part: far is in units of it."""
+    M, K = 5, 9
+    g = torch.Generator().manual_seed(V + int(far))
+    z = torch.randn((M, V), generator=g)
+    index = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(M)]).int()
+    index[2, 4:] = -1
+    index[3, 5] = index[3, 1]
+    for T in (0.25, 1.0, 3.0):
+        at = index.long().clamp(min=0)
+        given = torch.zeros((M, V), dtype=torch.bool).scatter_(1, at, index >= 0)
+        x = torch.where(given, z + far * T, z).to(TYPES[kind])
+        values = torch.randn((M, K), generator=g)
+        lse = torch.logsumexp(values.double().masked_fill(index < 0, -float("inf")) / T, 1)
+        lse = (lse + torch.tensor([0.5, 1e-3, 0.1, 0.01, -0.1])).float().cuda()  # (the last: no rest)
+        check(paro, x.cuda(), values.cuda(), index.cuda(), lse, T, kind,
+              f"rest far below V={V} far={far} {kind} T={T} scale={scale}", scale)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("mask", list(MASKS))
+def test_rest_masked_by_finite_numbers(paro, mask, kind):
+    """All that is outside the entries masked with one large number, where the teacher has a rest: a loss of that size,
+    and the rest's gradient spread over the masked logits."""
+    M, V, K = 3, 5003, 7
+    g = torch.Generator().manual_seed(1)
+    index = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(M)]).int()
+    values = torch.randn((M, K), generator=g)
+    z = torch.full((M, V), lowest(kind, mask)).scatter_(1, index.long(), values + 0.1).to(TYPES[kind])
+    for T in (0.5, 1.0, 2.0):
+        lse = (torch.logsumexp(values.double() / T, 1) + torch.tensor([0.3, 0.01, 0.1])).float().cuda()
+        check(paro, z.cuda(), values.cuda(), index.cuda(), lse, T, kind, f"rest masked {mask} {kind} T={T}")
