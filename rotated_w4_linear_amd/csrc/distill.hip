@@ -233,7 +233,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   auto taken = [&](int j) { return (bits[(j + skip) >> 5] >> ((j + skip) & 31)) & 1u; };
   auto more = [&](float hi) {
     if (hi > mx) {
-      sum = mx > -kInf ? sum * power(mx, hi) : 0.0f;
+      sum *= mx > -kInf ? power(mx, hi) : 1.0f;  // (a sum of nothing yet: 0, or NaN, which stays)
       mx = shift = hi;
     }
   };
@@ -304,9 +304,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
     }
     if (rest) total = left * exp(below) + wave_sum(mass);
     // (left holds everything without a class for the rest; a student without mass
-    // outside the entries has no gradient there)
+    // outside the entries has no gradient there, but a NaN's)
     const double Q = left * exp(below) / total;
-    if (lane == 0) factor = (float)(rest ? (left == 0.0 ? 0.0 : g * (A * Q - P) / left) : g * A / total);
+    if (lane == 0) factor = (float)(rest ? (left == 0.0 ? 0.0 * total : g * (A * Q - P) / left) : g * A / total);
   }
   __syncthreads();
   if (w == own) {  // the loss, and the gradient at the entries, with the masses of all entries of an index

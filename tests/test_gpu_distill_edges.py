@@ -141,3 +141,31 @@ def test_rest_masked_by_finite_numbers(paro, mask, kind):
     for T in (0.5, 1.0, 2.0):
         lse = (torch.logsumexp(values.double() / T, 1) + torch.tensor([0.3, 0.01, 0.1])).float().cuda()
         check(paro, z.cuda(), values.cuda(), index.cuda(), lse, T, kind, f"rest masked {mask} {kind} T={T}")
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("V", [1, 7, 64, 2049, 40003])
+def test_nan_is_never_lost(paro, V, kind, rest):
+    """A logit that is NaN makes its row's loss and gradient NaN wherever it stands: alone, before anything above -inf
+    that its lane reads, as a whole vector, behind masked ones, in a row that starts at any alignment."""
+    rows = [slice(0, 1), slice(0, 8), slice(V - 1, V), slice(0, V), slice(V // 2, V // 2 + 1), slice(0, 16)]
+    M, K = 2 * len(rows), min(5, V)
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn((M, V), generator=g)
+    index = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(M)]).int()
+    values = torch.randn((M, K), generator=g)
+    lse = torch.logsumexp(values, 1) + 0.1 if rest else None
+    for m, s in enumerate(rows):
+        z[m, s] = float("nan")
+        z[m + len(rows), :V // 3] = -float("inf")
+        z[m + len(rows), s] = float("nan")
+    print(f"NaN V={V} {kind} rest={rest}", flush=True)
+    loss, dz = paro.paro_distill_loss(z.to(TYPES[kind]).cuda(), values.cuda(), index.cuda(),
+                                      lse=lse.cuda() if rest else None)
+    torch.cuda.synchronize()
+    assert torch.isnan(loss).all(), loss
+    assert torch.isnan(dz).all(), torch.isnan(dz).all(1)
+    alone, _ = paro.paro_distill_loss(z.to(TYPES[kind]).cuda(), values.cuda(), index.cuda(),
+                                      lse=lse.cuda() if rest else None, gradients=False)
+    assert torch.isnan(alone).all()
