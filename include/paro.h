@@ -643,7 +643,7 @@ int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t
  *   loss     device fp32 [M].
  *   dz       device [M][V] of z's type, 16-byte aligned: grad_scale dL/dz (the
  *            scale keeps fp16 gradients normal), or NULL; may be z itself.
- *   M < 2^22, 1 <= V <= 2^20, 1 <= K <= 1024; T > 0.
+ *   M < 2^22, 1 <= V <= 2^20, 1 <= K <= 1024; T > 0 with log2(e) / T finite in fp32.
  * Arithmetic: exponentials and their sums over the row in fp32, the entries in
  * fp64; results do not depend on timing. One launch, no workspace.
  * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE, PARO_ERR_ALIGN,

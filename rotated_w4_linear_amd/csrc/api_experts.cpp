@@ -289,8 +289,9 @@ int paro_distill_loss(const void* z, int32_t z_type, const void* values, int32_t
   if (M > kMaxLossRows || V > (int64_t(1) << 20) || K > 1024)
     return fail(PARO_ERR_UNSUPPORTED, f + ": fewer than 2^22 rows, at most 2^20 logits and 1024 of the teacher's");
   const float T = (float)temperature, scale = (float)grad_scale;
-  if (!(T > 0) || !std::isfinite(T) || !std::isfinite(1.0f / T) || !std::isfinite(scale))
-    return fail(PARO_ERR_VALUE, f + ": temperature must be positive, and it and grad_scale finite in fp32");
+  // (log2(e) / T is the factor of the kernel's exponents)
+  if (!(T > 0) || !std::isfinite(T) || !std::isfinite((float)(1.4426950408889634 / (double)T)) || !std::isfinite(scale))
+    return fail(PARO_ERR_VALUE, f + ": temperature must be positive and above 4.3e-39, and it and grad_scale finite in fp32");
   if (M == 0) return PARO_OK;
   if (!z || !values || !index || !loss) return fail(PARO_ERR_NULL, f + ": NULL tensor");
   if (!aligned(z, 16) || !aligned(dz, 16) || !aligned(values, value_type == PARO_TYPE_F32 ? 4 : 2) ||
