@@ -534,7 +534,9 @@ int paro_experts_sort(const int32_t* ids, int64_t M, int32_t E, int32_t k, int32
  * is constant): with normalize dl_i = w_i (dw_i - sum_s w_s dw_s) for the token's
  * experts and 0 for the others (logits may be NULL), else
  * dl_j = p_j (dw_j [j is one of them] - sum_s p_s dw_s). Pairs without an expert
- * take no part, and a token without experts has a gradient of 0.
+ * take no part, and a token without experts has a gradient of 0. Where a logit of
+ * a token with experts is NaN or +inf, the p are NaN, and so is the gradient at
+ * every expert (normalize: at the token's).
  *   ids, weights, normalize: the forward call's; dweights device fp32 [M][k];
  *   dlogits device [M][E], of the logits' type, overwritten (may be logits).
  * Errors: as paro_experts_route, without a workspace.

@@ -366,7 +366,8 @@ __global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__
 
 // Gradient at the logits, a wavefront per token. Normalised weights:
 //   dl_i = w_i (dw_i - sum_S w dw) for i in S, else 0;
-// p itself: dl_j = [j in S] p_j dw_j - p_j sum_S p dw.
+// p itself: dl_j = [j in S] p_j dw_j - p_j sum_S p dw, NaN at every expert where a
+// logit is NaN or +inf, and 0 for a token without an expert.
 template <class T>
 __global__ __launch_bounds__(256) void route_backward_kernel(const typename T::raw* __restrict__ logits,
                                                                   const int* __restrict__ ids,
@@ -394,13 +395,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const typename T::r
     for (int e = lane; e < E; e += 64) top = fmaxf(top, T::value(l[e]));
 #pragma unroll
     for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-    for (int e = lane; e < E; e += 64) total += top > -__builtin_inff() ? expf(T::value(l[e]) - top) : 0.0f;
+    for (int e = lane; e < E; e += 64) {
+      const float x = T::value(l[e]);
+      total += x == -__builtin_inff() ? 0.0f : expf(x - top);
+    }
     total = wave_sum(total);
   }
+  const bool any = __ballot(id >= 0) != 0 && total != 0.0f;  // (a NaN is not 0)
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
     float v = 0.0f;
-    if (!normalize && e < E && total > 0.0f) v = -(expf(T::value(l[e]) - top) / total) * inner;
+    if (!normalize && e < E && any) v = -(expf(T::value(l[e]) - top) / total) * inner;
     for (int s = 0; s < k; ++s) {
       const int i = __shfl(id, s);
       const float t = __shfl(taken, s);
