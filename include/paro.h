@@ -560,11 +560,16 @@ int paro_experts_route_backward(const void* logits, int32_t type, int64_t M, int
  *            experts of a layer share the transform);
  *   h        device fp16 [R][N] (gated's output; rows from offsets[E] on are left
  *            as they were) and [R][d] (combine's input, transformed if its
- *            weights are);
+ *            weights are: like X's, one transform for all experts of a layer).
  *   qweight  device uint8 [E][P][d/2], scales [E][P][d/group], zeros likewise,
  *            bias fp16 [E][P] or NULL, with P = 2 N (gated) or N (combine): what
  *            paro_quantize_weights makes of the E [P][d] weights, one after the
  *            other;
+ *            Rows from offsets[E] on and a transform of h: how many there are is
+ *            known on the device alone, and paro_rotation_backward over h and dh
+ *            sums all R rows. A caller that makes it zero-fills h and dh before
+ *            the calls that write them (which leave those rows as they were).
+ *            paro_rotate may be run over all rows, whatever those hold.
  *   residual device fp16 [M][N] or NULL; may be y itself, no other overlap;
  *   y        device fp16 [M][N]; tokens without an expert get the residual, or 0.
  *   N % 16 == 0, d % 128 == 0, d % group == 0, P and d <= 2^21, P d < 2^31; the

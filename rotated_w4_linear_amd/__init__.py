@@ -771,16 +771,17 @@ def _experts_weights(r, qweight, scales, zeros, bias, P, d, group, dev):
 
 def paro_w4_experts_gated(routing: Routing, x, qweight, scales, zeros, bias=None, act: str = "silu", h=None,
                           group: int = 128, workspace=None, stream=None):
-    """H = act(x Wg^T + bg) * (x Wu^T + bu) of every (token, expert) pair (fp16 [M k][N], rows in expert order; those
-    behind the last pair with an expert are left as they were) for the transformed activations ``x`` [M][d] and the
-    experts' weight blocks [E][2 N][d / 2] (gate, then up)."""
+    """H = act(x Wg^T + bg) * (x Wu^T + bu) of every (token, expert) pair (fp16 [M k][N], rows in expert order) for the
+    transformed activations ``x`` [M][d] and the experts' weight blocks [E][2 N][d / 2] (gate, then up). Rows behind the
+    last pair with an expert are 0 in an ``h`` that is made here, and left as they were in one that is given (which
+    saves filling it). paro_rotation_backward over h sums all its rows: zero-fill a given one before the call."""
     import torch
     M, d = routing.M, x.shape[1]
     N = qweight.shape[1] // 2
     dev, f16 = torch.cuda.current_device(), torch.float16
     if h is None:
         with _made_on(stream):
-            h = x.new_empty((M * routing.k, N))
+            h = torch.zeros((M * routing.k, N), dtype=x.dtype, device=x.device)
         _handed_out(stream, h)
     # (the call needs no workspace)
     workspace, ws_ptr, ws_bytes = _workspace(workspace, 0, x.device, dev)
@@ -828,7 +829,8 @@ def paro_w4_experts_gated_backward(routing: Routing, x, qweight, scales, zeros, 
                                    dz=None, dx=None, want_dx: bool = True, group: int = 128, workspace=None,
                                    stream=None):
     """Gradients of paro_w4_experts_gated for dh = dL/dH ([M k][N], by row): returns (dx fp16 [M][d] or None, dz fp16
-    [M k][2 N]: the gate's columns, then the up projection's; rows behind the last pair are left as they were)."""
+    [M k][2 N]: the gate's columns, then the up projection's; rows behind the last pair are left as they were, and hold
+    anything in a ``dz`` that is made here)."""
     import torch
     M, d = routing.M, x.shape[1]
     N = qweight.shape[1] // 2
@@ -855,8 +857,9 @@ def paro_w4_experts_gated_backward(routing: Routing, x, qweight, scales, zeros, 
 
 def paro_w4_experts_combine_backward(routing: Routing, h, qweight, scales, zeros, dy, bias=None, dh=None,
                                      dweights=None, group: int = 128, workspace=None, stream=None):
-    """Gradients of paro_w4_experts_combine for dy = dL/dY ([M][N]): returns (dh fp16 [M k][d], rows in expert order,
-    those behind the last pair left as they were; dweights fp32 [M][k])."""
+    """Gradients of paro_w4_experts_combine for dy = dL/dY ([M][N]): returns (dh fp16 [M k][d], rows in expert order;
+    dweights fp32 [M][k]). Rows behind the last pair with an expert are 0 in a ``dh`` that is made here, and left as
+    they were in one that is given: zero-fill that one before the call where paro_rotation_backward sums its rows."""
     import torch
     M, d = routing.M, h.shape[1]
     N = qweight.shape[1]
@@ -865,7 +868,7 @@ def paro_w4_experts_combine_backward(routing: Routing, h, qweight, scales, zeros
     made = []
     with _made_on(stream):
         if dh is None:
-            dh = h.new_empty((R, d))
+            dh = torch.zeros((R, d), dtype=h.dtype, device=h.device)
             made.append(dh)
         dweights = _given(dweights, "dweights", (M, routing.k), h.device, made)
         workspace, ws_ptr, ws_bytes = _scratch("combine_backward", routing, N, d, workspace, h.device, dev)

@@ -49,3 +49,54 @@ def test_route_gradient_of_rows_that_are_not_finite(paro, E, k, kind, normalize)
     ref, err = experts.route_backward(xd.double().cpu().numpy()[fine], ids[fine], host(r.weights).astype(np.float64)[fine],
                                       dw.astype(np.float64)[fine], normalize)
     within(got[fine], ref, experts.stored(ref, err, kind), "dlogits")
+
+
+# ---------------------------------------------------------------------------
+# the transform of the down projections' input, with tokens that have no expert
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("M,E,k,d,H,padded", [(600, 8, 2, 256, 512, 0.3), (900, 4, 2, 128, 768, 0.9), (600, 8, 2, 256, 512, 1.0),
+                                              (700, 3, 1, 256, 1024, 0.1)])
+def test_gradient_of_the_transform_between_the_products(paro, M, E, k, d, H, padded, given):
+    """X through the experts' gated block, its rows transformed, the down projections on them, and back to the angles
+    and scales of that transform: it sums over all rows, those that no pair has included. Memory that held NaN before."""
+    import oracle
+    import synthetic
+    from oracle import metrics
+    G = 128
+    rng = np.random.default_rng(M + E)
+    _, lay, _ = synthetic.linear_case(seed=5, M=1, d=H, N=16, group=G, K=4)
+    rot = paro.Rotation(lay.pairs, lay.theta, lay.alpha, G)
+    half = lambda *s: dev((rng.standard_normal(s) / np.sqrt(s[-1])).astype(np.float16))  # noqa: E731
+    up = [t.view(E, 2 * H, -1) for t in paro.paro_quantize_weights(None, half(E * 2 * H, d), G)]
+    down = [t.view(E, d, -1) for t in paro.paro_quantize_weights(rot, half(E * d, H), G)]
+    x, dy = half(M, d) * 8, half(M, d)
+    logits = rng.standard_normal((M, E)).astype(np.float32)
+    logits[rng.random(M) < padded] = -np.inf
+    r = paro.paro_experts_route(dev(logits), k)
+    R = M * k
+    log(f"transform between the products M={M} E={E} k={k} H={H} padded={padded} given={given}")
+    torch.cuda.empty_cache()
+    held = torch.full((1 << 26,), float("nan"), dtype=torch.float16, device="cuda")
+    h = dh = None
+    if given:  # a caller's own memory, zero-filled as the header says
+        h, dh = (torch.full((R, H), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2))
+        h.zero_()
+        dh.zero_()
+    del held
+    h = paro.paro_w4_experts_gated(r, x, *up, h=h)
+    hr = paro.paro_rotate(rot, h)
+    y = paro.paro_w4_experts_combine(r, hr, *down)
+    dh, dw = paro.paro_w4_experts_combine_backward(r, hr, *down, dy, dh=dh)
+    gh, dth, dal = paro.paro_rotation_backward(rot, h, dh.float())
+    torch.cuda.synchronize()
+    n = int(host(r.offsets)[-1])
+    assert torch.isfinite(y).all() and not host(h)[n:].any() and not host(dh)[n:].any() and not host(gh)[n:].any()
+    want = oracle.rotation_backward(host(h)[:n], host(dh)[:n], lay.pairs, lay.theta, lay.alpha)
+    metrics.assert_grad_close(host(gh)[:n], want[0], "gh")
+    for got, ref, name in ((dth, want[1], "dtheta"), (dal, want[2], "dalpha")):
+        if n == 0:
+            assert not host(got).any()
+        else:
+            metrics.assert_grad_close(host(got), ref, name)
