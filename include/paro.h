@@ -516,7 +516,8 @@ typedef struct paro_routing {
  *   1 <= k <= E <= 1024, k <= 16, R < 2^24.
  *   workspace: paro_experts_route_workspace_size(M, E, k) bytes (0 up to 128
  *            tokens), 256-byte aligned; scratch, not shared by calls that may
- *            run at the same time.
+ *            run at the same time. The size never shrinks with M: one for the
+ *            largest batch serves every smaller one.
  * paro_experts_sort makes the tables of given ids (a router of the caller's, or
  * the experts e0 .. e0 + E - 1 that one device holds, from ids - e0).
  * Errors: PARO_ERR_NULL, PARO_ERR_SHAPE, PARO_ERR_VALUE (unknown type),
@@ -578,7 +579,9 @@ int paro_experts_route_backward(const void* logits, int32_t type, int64_t M, int
  *   tensors 16-byte aligned. M == 0 is a no-op.
  *   workspace: at least the ..._workspace_size bytes (combine: its rows in fp32,
  *   4 R N bytes, so that a token's sum is rounded once), 256-byte aligned;
- *   scratch, not shared by calls that may run at the same time.
+ *   scratch, not shared by calls that may run at the same time. The sizes, those of
+ *   the gradients below too, never shrink with M: for the same E, k, N and d a
+ *   workspace for the largest batch serves every smaller one.
  * Arithmetic: fp32 sums of exact fp16 products, one rounding to fp16; results do
  * not depend on timing, nor a row's on the other rows' values.
  * The calls read the numbers of rows on the device: they do not synchronise, and

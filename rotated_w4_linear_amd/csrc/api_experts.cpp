@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <vector>
 
 #include "paro_internal.h"
 #include "w4_epilogue.h"
@@ -98,6 +99,20 @@ size_t grad_bytes(const ExpertRouting& t, int64_t P, int64_t d, bool share) {
   return a256(share ? experts_grad_dots(t, d) : (size_t)experts_grad_splits(t, P, d) * t.R * d * 4);
 }
 
+// The most that grad_bytes asks for up to M tokens, so that a workspace for the
+// largest batch serves every smaller one: its size grows with M but where the rules
+// choose another way, so that the last M before each step, and M itself, are looked at.
+size_t grad_peak(int64_t M, int32_t E, int32_t k, int64_t P, int64_t d, bool share) {
+  std::vector<int64_t> rows;
+  rows.reserve(64);
+  experts_grad_rows_steps(E, d, rows);
+  experts_grad_wide_steps(E, d, rows);
+  size_t most = grad_bytes(sizes_only(M, E, k), P, d, share);
+  for (const int64_t r : rows)
+    if (r / k >= 1 && r / k < M) most = std::max(most, grad_bytes(sizes_only(r / k, E, k), P, d, share));
+  return most;
+}
+
 bool known_act(int32_t act) { return act >= PARO_ACT_NONE && act <= PARO_ACT_RELU; }
 
 }  // namespace
@@ -109,7 +124,11 @@ extern "C" {
 
 size_t paro_experts_route_workspace_size(int64_t M, int32_t E, int32_t k) {
   if (!good_experts(M, E, k) || E > kExpertsMax || k > kExpertsMaxK || M > kMaxPairs / k) return 0;
-  return experts_route_scratch(M, E);
+  // (the most of any number of tokens up to M: chunks get larger at 16384 and 32768)
+  size_t most = experts_route_scratch(M, E);
+  for (const int64_t m : {int64_t(16384), int64_t(32768)})
+    if (m < M) most = std::max(most, experts_route_scratch(m, E));
+  return most;
 }
 
 int paro_experts_route(const void* logits, int32_t type, int64_t M, int32_t E, int32_t k, int32_t normalize,
@@ -214,7 +233,7 @@ int paro_w4_experts_combine(const paro_routing* routing, const uint16_t* h, cons
 
 size_t paro_w4_experts_gated_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d) {
   if (N > (int64_t(1) << 20) || !good_sizes(M, E, k, 2 * N, d) || N % 16) return 0;
-  return grad_bytes(sizes_only(M, E, k), 2 * N, d, false);
+  return grad_peak(M, E, k, 2 * N, d, false);
 }
 
 int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* x, const uint8_t* qweight,
@@ -231,7 +250,7 @@ int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* 
   if (st != PARO_OK || none) return st;
   if (!dh) return fail(PARO_ERR_NULL, f + ": NULL tensor");
   if (!aligned(dh, 16) || !aligned(dx, 16)) return fail(PARO_ERR_ALIGN, f + ": dh and dx must be 16-byte aligned");
-  const size_t need = dx ? paro_w4_experts_gated_backward_workspace_size(t.M, t.E, t.k, N, d) : 0;
+  const size_t need = dx ? grad_bytes(t, 2 * N, d, false) : 0;
   if ((st = check_workspace(f, need, workspace, workspace_bytes)) != PARO_OK) return st;
   W4Epilogue ep;
   ep.aux = dh;
@@ -249,7 +268,7 @@ int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* 
 }
 
 size_t paro_w4_experts_combine_backward_workspace_size(int64_t M, int32_t E, int32_t k, int64_t N, int64_t d) {
-  return good_sizes(M, E, k, N, d) ? grad_bytes(sizes_only(M, E, k), N, d, true) : 0;
+  return good_sizes(M, E, k, N, d) ? grad_peak(M, E, k, N, d, true) : 0;
 }
 
 int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t* h, const uint8_t* qweight,
@@ -264,7 +283,7 @@ int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t
   if (!dy || !dweights) return fail(PARO_ERR_NULL, f + ": NULL tensor");
   if (!aligned(dy, 16) || !aligned(dweights, 4))
     return fail(PARO_ERR_ALIGN, f + ": dy must be 16-byte aligned, dweights 4-byte");
-  const size_t need = paro_w4_experts_combine_backward_workspace_size(t.M, t.E, t.k, N, d);
+  const size_t need = grad_bytes(t, N, d, true);
   if ((st = check_workspace(f, need, workspace, workspace_bytes)) != PARO_OK) return st;
   float* part = (float*)workspace;
   hipError_t e;

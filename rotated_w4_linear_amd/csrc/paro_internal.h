@@ -333,6 +333,10 @@ hipError_t launch_w4_experts(int epi, const ExpertRouting& t, const uint16_t* x,
 // part [splits][R][d] = dz W_hat of each row's expert, in pieces of the
 // contraction (w4_input_grad_rows.hip); gather: dz by token, else by row.
 int experts_grad_rows_splits(const ExpertRouting& t, int64_t P, int64_t d);
+// Row counts R up to which (one at least of each pair of choices) the rules above and
+// those of the large tiles choose alike: more rows can need less room behind one.
+void experts_grad_rows_steps(int64_t E, int64_t d, std::vector<int64_t>& rows);
+void experts_grad_wide_steps(int64_t E, int64_t d, std::vector<int64_t>& rows);
 hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, const uint16_t* dz,
                                        const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                                        float* part, int64_t P, int64_t d, int group, hipStream_t stream);

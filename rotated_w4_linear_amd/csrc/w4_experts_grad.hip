@@ -398,6 +398,14 @@ int experts_grad_splits(const ExpertRouting& t, int64_t P, int64_t d) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({384 / blocks, P / (16 * kK), 4}));
 }
 
+void experts_grad_wide_steps(int64_t E, int64_t d, std::vector<int64_t>& rows) {
+  rows.insert(rows.end(), {E, 16 * E - 1, 160 * E - 1});
+  for (int64_t s = 1; s <= 4; ++s) {
+    const int64_t q = 384 / s / ((d + kN - 1) / kN);
+    rows.insert(rows.end(), {q, kM * (q + 1) - 1});
+  }
+}
+
 // Whether the gradient is taken in these tiles (share: of combine, whose tiles are not
 // shared out), from a mean of 16 rows on if there are tiles for all CUs, else of 160.
 // Microseconds of w4_input_grad_rows_kernel's way | this:

@@ -282,6 +282,14 @@ int experts_grad_rows_splits(const ExpertRouting& t, int64_t P, int64_t d) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({kCus / blocks, chunks / 8, 8}));
 }
 
+void experts_grad_rows_steps(int64_t E, int64_t d, std::vector<int64_t>& rows) {
+  rows.insert(rows.end(), {E, 9 * E - 1, 25 * E - 1});  // (a block per row; a mean of 8; of 24)
+  for (int64_t s = 1; s <= 8; ++s) {
+    const int64_t q = kCus / s / (d / 128);  // most blocks of rows that s ranges are made for
+    rows.insert(rows.end(), {q, 16 * (q + 1) - 1, 32 * (q + 1) - 1, 64 * (q + 1) - 1});
+  }
+}
+
 hipError_t launch_w4_experts_grad_rows(const ExpertRouting& t, bool gather, const uint16_t* dz,
                                        const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                                        float* part, int64_t P, int64_t d, int group, hipStream_t stream) {

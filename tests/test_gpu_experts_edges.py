@@ -100,3 +100,39 @@ def test_gradient_of_the_transform_between_the_products(paro, M, E, k, d, H, pad
             assert not host(got).any()
         else:
             metrics.assert_grad_close(host(got), ref, name)
+
+
+@pytest.mark.parametrize("E,k,N,d,tokens", [(2, 1, 128, 256, (1, 5, 31, 32, 33, 129, 319, 320, 321, 700)),
+                                            (8, 2, 1040, 512, (1, 8, 9, 35, 36, 63, 64, 65, 100, 640, 641, 700)),
+                                            (3, 2, 2064, 1152, (2, 24, 36, 37, 140, 240, 241, 400))])
+def test_one_workspace_for_every_batch(paro, E, k, N, d, tokens):
+    """The workspace of the largest number of tokens serves all of them, and nothing is written behind the room that a
+    call's own sizes ask for; results as with a workspace that the call makes."""
+    most = max(tokens)
+    new = {"combine": paro.new_experts_combine_workspace, "gated_backward": paro.new_experts_gated_backward_workspace,
+           "combine_backward": paro.new_experts_combine_backward_workspace}
+    room = max([f(most, E, k, N, d).numel() for f in new.values()] +
+               [t.numel() for t in [paro.new_experts_route_workspace(most, E, k)] if t is not None])
+    ws = torch.empty(room, dtype=torch.uint8, device="cuda")
+    g, c = Case(paro, 1, 1, E, k, 2 * N, d, 128), Case(paro, 2, 1, E, k, N, d, 128)
+    rng = np.random.default_rng(E)
+    half = lambda *s: dev(rng.standard_normal(s).astype(np.float16))  # noqa: E731
+
+    def same(name, M, call):
+        need = new[name](M, E, k, N, d).numel()
+        ws.fill_(171)
+        got, own = call(ws), call(None)
+        torch.cuda.synchronize()
+        assert (ws[need:] == 171).all(), (name, M)
+        for a, b in zip(got, own):
+            assert torch.equal(a, b), (name, M)
+    for M in tokens:
+        log(f"one workspace E={E} k={k} N={N} d={d} M={M}")
+        logits = dev(rng.standard_normal((M, E)).astype(np.float32))
+        r, s = paro.paro_experts_route(logits, k, workspace=ws), paro.paro_experts_route(logits, k)
+        assert all(torch.equal(getattr(r, n), getattr(s, n)) for n in ("ids", "weights", "offsets", "order", "place"))
+        x, h, dh, dy = half(M, d), half(M * k, d), half(M * k, N), half(M, N)
+        same("combine", M, lambda w: (paro.paro_w4_experts_combine(r, h, *c.dev, bias=c.bd, workspace=w),))
+        same("gated_backward", M, lambda w: paro.paro_w4_experts_gated_backward(r, x, *g.dev, dh, bias=g.bd, workspace=w))
+        same("combine_backward", M,
+             lambda w: paro.paro_w4_experts_combine_backward(r, h, *c.dev, dy, bias=c.bd, workspace=w))
