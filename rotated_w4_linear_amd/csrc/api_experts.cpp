@@ -124,10 +124,10 @@ extern "C" {
 
 size_t paro_experts_route_workspace_size(int64_t M, int32_t E, int32_t k) {
   if (!good_experts(M, E, k) || E > kExpertsMax || k > kExpertsMaxK || M > kMaxPairs / k) return 0;
-  // (the most of any number of tokens up to M: chunks get larger at 16384 and 32768)
-  size_t most = experts_route_scratch(M, E);
-  for (const int64_t m : {int64_t(16384), int64_t(32768)})
-    if (m < M) most = std::max(most, experts_route_scratch(m, E));
+  // (the most of any number of tokens up to M: chunks get larger behind these)
+  size_t most = experts_route_scratch(M, E, k);
+  for (const int64_t m : {int64_t(16384), int64_t(32768), int64_t(1) << 18})
+    if (m < M) most = std::max(most, experts_route_scratch(m, E, k));
   return most;
 }
 
@@ -144,7 +144,7 @@ int paro_experts_route(const void* logits, int32_t type, int64_t M, int32_t E, i
   if (!aligned(logits, type == PARO_TYPE_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4) ||
       !aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4))
     return fail(PARO_ERR_ALIGN, f + ": a tensor is not aligned to its type");
-  if ((st = check_workspace(f, experts_route_scratch(M, E), workspace, workspace_bytes)) != PARO_OK) return st;
+  if ((st = check_workspace(f, experts_route_scratch(M, E, k), workspace, workspace_bytes)) != PARO_OK) return st;
   // (no tokens: every expert's rows are empty)
   const hipError_t e = none ? launch_fill_zero((float*)offsets, E + 1, stream)
                             : launch_experts_route(logits, type, M, E, k, normalize != 0, ids, weights, offsets, order,
@@ -161,7 +161,7 @@ int paro_experts_sort(const int32_t* ids, int64_t M, int32_t E, int32_t k, int32
   if (!offsets || (!none && (!ids || !order || !place))) return fail(PARO_ERR_NULL, f + ": NULL tensor");
   if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4))
     return fail(PARO_ERR_ALIGN, f + ": a tensor is not aligned to its type");
-  if ((st = check_workspace(f, experts_route_scratch(M, E), workspace, workspace_bytes)) != PARO_OK) return st;
+  if ((st = check_workspace(f, experts_route_scratch(M, E, k), workspace, workspace_bytes)) != PARO_OK) return st;
   const hipError_t e = none ? launch_fill_zero((float*)offsets, E + 1, stream)
                             : launch_experts_route(nullptr, 0, M, E, k, 0, const_cast<int32_t*>(ids), nullptr, offsets,
                                                    order, place, workspace, stream);

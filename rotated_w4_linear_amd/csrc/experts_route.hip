@@ -25,9 +25,18 @@ namespace paro {
 namespace {
 
 // Tokens per chunk: few, so that the chunks fill the CUs, and more where there are
-// so many chunks that adding up their counts would take longer.
-constexpr int kOneChunk = 128;
-int chunk_tokens(int64_t M) { return M <= kOneChunk ? kOneChunk : M <= 16384 ? 64 : M <= 32768 ? 128 : 256; }
+// so many chunks that adding up their counts would take longer: that work is the
+// chunks' number squared, so that they stay at 1024 or fewer for as long as a chunk
+// has at most 4096 pairs (its tables fill the LDS), and at 4096 in all. (Given ids of
+// 2^20 tokens, chunks of 256 | these: 2 of 256 experts 687 | 72 us, 1 of 1024 2929 |
+// 217, 8 of 60 225 | 114.)
+constexpr int kOneChunk = 128, kChunkPairs = 4096;
+int chunk_tokens(int64_t M, int k) {
+  if (M <= kOneChunk) return kOneChunk;
+  int n = M <= 16384 ? 64 : M <= 32768 ? 128 : 256;
+  while (M > 1024 * (int64_t)n && 2 * n * k <= kChunkPairs) n *= 2;
+  return n;
+}
 // Counts of a chunk: whole words of two
 __host__ __device__ __forceinline__ int count_stride(int E) { return (E + 2) & ~1; }
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
@@ -452,15 +461,15 @@ hipError_t launch_route(int chunk, int chunks, hipStream_t stream, const void* l
 
 }  // namespace
 
-size_t experts_route_scratch(int64_t M, int E) {
-  const int64_t chunk = chunk_tokens(M), chunks = (M + chunk - 1) / chunk;
+size_t experts_route_scratch(int64_t M, int E, int k) {
+  const int64_t chunk = chunk_tokens(M, k), chunks = (M + chunk - 1) / chunk;
   return chunks > 1 ? (size_t)chunks * count_stride(E) * 2 : 0;
 }
 
 hipError_t launch_experts_route(const void* logits, int type, int64_t M, int E, int k, int normalize, int* ids,
                                 float* weights, int* offsets, int* order, int* place, void* scratch,
                                 hipStream_t stream) {
-  const int chunk = chunk_tokens(M), chunks = (int)((M + chunk - 1) / chunk);
+  const int chunk = chunk_tokens(M, k), chunks = (int)((M + chunk - 1) / chunk);
   uint16_t* counts = (uint16_t*)scratch;
   hipError_t e = hipSuccess;
   if (!logits)

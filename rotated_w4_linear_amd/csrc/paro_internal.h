@@ -306,8 +306,8 @@ inline int64_t expert_blocks(const ExpertRouting& t, int bm) {
   return full + used < t.R ? full + used : t.R;
 }
 // The router (logits NULL: the tables of given ids) and its gradient
-// (experts_route.hip); scratch holds experts_route_scratch(M, E) bytes.
-size_t experts_route_scratch(int64_t M, int E);
+// (experts_route.hip); scratch holds experts_route_scratch(M, E, k) bytes.
+size_t experts_route_scratch(int64_t M, int E, int k);
 hipError_t launch_experts_route(const void* logits, int type, int64_t M, int E, int k, int normalize, int* ids,
                                 float* weights, int* offsets, int* order, int* place, void* scratch,
                                 hipStream_t stream);

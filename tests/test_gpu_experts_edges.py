@@ -136,3 +136,13 @@ def test_one_workspace_for_every_batch(paro, E, k, N, d, tokens):
         same("gated_backward", M, lambda w: paro.paro_w4_experts_gated_backward(r, x, *g.dev, dh, bias=g.bd, workspace=w))
         same("combine_backward", M,
              lambda w: paro.paro_w4_experts_combine_backward(r, h, *c.dev, dy, bias=c.bd, workspace=w))
+
+
+@pytest.mark.parametrize("M,E,k", [((1 << 18) + 1, 60, 2), (1 << 20, 7, 1), ((1 << 20) + 77, 256, 2), (1 << 21, 1024, 1),
+                                   ((1 << 20) - 1, 40, 16), ((1 << 24) - 1, 3, 1)])
+def test_tables_of_very_many_tokens(paro, M, E, k):
+    """Chunks of more tokens, up to the most pairs that a routing can have."""
+    rng = np.random.default_rng(M % 1000 + E)
+    log(f"tables M={M} E={E} k={k}")
+    ids = rng.integers(-1, E, (M, k)).astype(np.int32)
+    check_tables(paro.paro_experts_sort(dev(ids), E), ids)
