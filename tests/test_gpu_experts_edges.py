@@ -3,8 +3,9 @@ scales, one workspace for many sizes; on the GPU against the fp64 oracle (oracle
 import numpy as np
 import pytest
 
-from oracle import block, experts
-from test_gpu_experts import TYPES, Case, Layer, check_tables, dev, guarded, host, log, paro, seed_of, within  # noqa: F401
+import test_gpu_experts as base
+from oracle import experts
+from test_gpu_experts import TYPES, Case, check_tables, dev, host, log, paro, seed_of, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +147,42 @@ def test_tables_of_very_many_tokens(paro, M, E, k):
     log(f"tables M={M} E={E} k={k}")
     ids = rng.integers(-1, E, (M, k)).astype(np.int32)
     check_tables(paro.paro_experts_sort(dev(ids), E), ids)
+
+
+# ---------------------------------------------------------------------------
+# the large tiles with their panel of scales and zeros: a mean of 144 rows an expert and more, up to 64 groups along k,
+# a multiple of 8
+# ---------------------------------------------------------------------------
+
+PANELS = [
+    (400, 2, 1, 272, 1024, 128, 0.0), (700, 3, 1, 144, 512, 64, 0.0), (330, 2, 1, 80, 4096, 64, 0.0),
+    (600, 2, 2, 272, 2048, 128, 0.0), (450, 3, 1, 528, 2048, 256, 0.0), (500, 4, 2, 16, 1536, 64, 0.05),
+    (320, 2, 1, 1040, 8192, 128, 0.0), (200, 1, 1, 400, 1024, 64, 0.3), (900, 4, 2, 304, 4096, 256, 0.1),
+    # (beside them: 72 groups, and 12, without a panel)
+    (330, 2, 1, 80, 4608, 64, 0.0), (330, 2, 1, 80, 1536, 128, 0.0),
+]
+
+
+@pytest.mark.parametrize("M,E,k,N,d,G,padded", PANELS)
+def test_gated_with_a_panel(paro, M, E, k, N, d, G, padded):
+    base.test_gated(paro, M, E, k, N, d, G, padded)
+
+
+@pytest.mark.parametrize("M,E,k,N,d,G,padded", PANELS)
+def test_combine_with_a_panel(paro, M, E, k, N, d, G, padded):
+    base.test_combine(paro, M, E, k, N, d, G, padded)
+
+
+def test_panels_have_tiles_of_both_heights(paro):
+    """An expert's rows in tiles of 256, its last up to 128 in ones of half the height: on panels of every group size."""
+    seen = set()
+    for M, E, k, N, d, G, padded in PANELS:
+        assert M * k >= 144 * E and d >= 256
+        if d // G % 8 == 0 and d // G <= 64:
+            for seed in (0, 1):  # the two tests'
+                c = Case(paro, seed_of(M, E, k, N, d, G, padded) + seed, M, E, k, (2 - seed) * N, d, G, padded)
+                for n in np.diff(c.offsets):
+                    rest = n % 256
+                    seen |= {(G, seed, "whole")} if n >= 256 else set()
+                    seen |= {(G, seed, "short" if rest <= 128 else "tall")} if rest else set()
+    assert seen == {(G, s, h) for G in (64, 128, 256) for s in (0, 1) for h in ("whole", "short", "tall")}, sorted(seen)
