@@ -52,6 +52,39 @@ def test_route_gradient_of_rows_that_are_not_finite(paro, E, k, kind, normalize)
     within(got[fine], ref, experts.stored(ref, err, kind), "dlogits")
 
 
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("M,E,k,kind", [(1, 3, 2, "fp32"), (77, 64, 6, "bf16"), (300, 1000, 8, "fp16"), (9, 65, 65 % 16, "fp32")])
+def test_route_gradient_in_place(paro, M, E, k, kind, normalize):
+    """dlogits may be the logits."""
+    rng = np.random.default_rng(M + E)
+    x = base.logits_of(rng, M, E, kind).cuda()
+    log(f"route gradient in place M={M} E={E} k={k} {kind} normalize={normalize}")
+    r = paro.paro_experts_route(x, k, normalize=normalize)
+    dw = dev(rng.standard_normal((M, k)).astype(np.float32))
+    want = paro.paro_experts_route_backward(x, r.ids, r.weights, dw, normalize=normalize)
+    got = paro.paro_experts_route_backward(x, r.ids, r.weights, dw, normalize=normalize, dlogits=x)
+    bits = torch.int32 if x.element_size() == 4 else torch.int16
+    torch.cuda.synchronize()
+    assert got is x and torch.equal(got.view(bits), want.view(bits))
+
+
+def test_route_captured_with_the_largest_tables(paro):
+    """More LDS than a launch takes by itself, inside a capture; other logits at each replay."""
+    M, E, k = 33000, 1024, 16
+    x = torch.empty((M, E), device="cuda", dtype=torch.bfloat16)
+    log("captured router")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = paro.paro_experts_route(x, k)
+    for seed in range(3):
+        x.normal_(generator=torch.Generator(device="cuda").manual_seed(seed))
+        g.replay()
+        s = paro.paro_experts_route(x, k)
+        torch.cuda.synchronize()
+        assert all(torch.equal(getattr(r, n), getattr(s, n)) for n in ("ids", "weights", "offsets", "order", "place"))
+
+
 # ---------------------------------------------------------------------------
 # the transform of the down projections' input, with tokens that have no expert
 # ---------------------------------------------------------------------------
@@ -186,3 +219,91 @@ def test_panels_have_tiles_of_both_heights(paro):
                     seen |= {(G, seed, "whole")} if n >= 256 else set()
                     seen |= {(G, seed, "short" if rest <= 128 else "tall")} if rest else set()
     assert seen == {(G, s, h) for G in (64, 128, 256) for s in (0, 1) for h in ("whole", "short", "tall")}, sorted(seen)
+
+
+# ---------------------------------------------------------------------------
+# what is not finite stays with its token
+# ---------------------------------------------------------------------------
+
+# every kernel of the products and of the gradients; numbers of weight rows that are no multiple of 64
+ISOLATED = {"few rows": (3, 8, 2, 48, 1024, 128), "tiles of 16": (20, 8, 2, 272, 512, 128),
+            "tiles of 32": (60, 6, 2, 272, 512, 64), "tiles of 48": (130, 4, 2, 528, 256, 128),
+            "large tiles": (400, 2, 1, 272, 512, 128), "large tiles, panel": (700, 3, 1, 144, 1024, 64),
+            "gradient shared out": (200, 4, 1, 1552, 4096, 128), "many experts": (600, 64, 2, 112, 1152, 64),
+            "one expert": (260, 1, 1, 48, 256, 256)}
+
+
+def spoilt(a, row, how):
+    b = a.copy()
+    if how == "mixed":
+        b[row, ::3], b[row, 1::3] = np.nan, np.inf
+    else:
+        b[row, a.shape[1] // 2] = {"nan": np.nan, "inf": np.inf}[how]
+    return b
+
+
+@pytest.mark.parametrize("how", ["mixed", "nan", "inf"])
+@pytest.mark.parametrize("name", list(ISOLATED))
+def test_what_is_not_finite_stays_with_its_token(paro, name, how):
+    """One token of X, one row of dH, one row of H, one token of dY, one weight: all that belongs to other tokens has the
+    same bits as without it, and what belongs to this one is not finite."""
+    M, E, k, N, d, G = ISOLATED[name]
+    c = Case(paro, 31 + M, M, E, k, 2 * N, d, G, padded=0.05 if M > 100 else 0.0)
+    pairs = c.order[:c.n]
+    token = pairs // k
+    x, dh = c.half(M, d), c.half(M * k, N)
+    row = c.n // 2
+    bad = token[row]
+    others, rest = np.arange(M) != bad, token != bad
+    bits = lambda t: host(t).view(np.int16 if t.element_size() == 2 else np.int32)  # noqa: E731
+    spoils = lambda t: ~np.isfinite(host(t).astype(np.float32))  # noqa: E731
+
+    def same(a, b, keep, what):
+        assert np.array_equal(bits(a)[:len(keep)][keep], bits(b)[:len(keep)][keep]), f"{name} {how}: {what}"
+    log(f"isolation {name} {how}: gated")
+    gated = lambda x: paro.paro_w4_experts_gated(c.r, dev(x), *c.dev, bias=c.bd, group=G)  # noqa: E731
+    back = lambda x, dh: paro.paro_w4_experts_gated_backward(c.r, dev(x), *c.dev, dev(dh), bias=c.bd, group=G)  # noqa: E731
+    clean, worse = gated(x), gated(spoilt(x, bad, how))
+    same(clean, worse, rest, "h")
+    assert spoils(worse)[:c.n][~rest].any(1).all()
+    log("  backward, X")
+    (dx, dz), (dx1, dz1) = back(x, dh), back(spoilt(x, bad, how), dh)
+    same(dz, dz1, rest, "dz")
+    same(dx, dx1, others, "dx")
+    assert spoils(dx1)[bad].any()
+    log("  backward, dH")
+    dx2, dz2 = back(x, spoilt(dh, row, how))
+    same(dz, dz2, np.arange(c.n) != row, "dz")
+    same(dx, dx2, others, "dx")
+    assert spoils(dz2)[row].any() and spoils(dx2)[bad].all()
+    c = Case(paro, 32 + M, M, E, k, N, d, G, padded=0.05 if M > 100 else 0.0)
+    pairs = c.order[:c.n]
+    token = pairs // k
+    h, dy, res = c.half(M * k, d), c.half(M, N), c.half(M, N)
+    row = c.n // 2
+    bad = token[row]
+    others, rest = np.arange(M) != bad, token != bad
+    log("  combine")
+    combine = lambda h: paro.paro_w4_experts_combine(c.r, dev(h), *c.dev, bias=c.bd, residual=dev(res), group=G)  # noqa: E731
+    y, y1 = combine(h), combine(spoilt(h, row, how))
+    same(y, y1, others, "y")
+    assert spoils(y1)[bad].all()
+    log("  backward, H")
+    back = lambda h, dy: paro.paro_w4_experts_combine_backward(c.r, dev(h), *c.dev, dev(dy), bias=c.bd, group=G)  # noqa: E731
+    (g, dw), (g1, dw1) = back(h, dy), back(spoilt(h, row, how), dy)
+    same(g, g1, np.ones(c.n, bool), "dh")
+    keep = np.arange(M * k) != pairs[row]
+    same(dw.view(-1, 1), dw1.view(-1, 1), keep, "dweights")
+    assert spoils(dw1).reshape(-1)[pairs[row]]
+    log("  backward, dY")
+    g2, dw2 = back(h, spoilt(dy, bad, how))
+    same(g, g2, rest, "dh")
+    same(dw, dw2, others, "dweights")
+    assert spoils(g2)[:c.n][~rest].all() and spoils(dw2).reshape(-1)[pairs[~rest]].all()
+    log("  a weight")
+    c.r.weights.view(-1)[int(pairs[row])] = {"mixed": float("nan"), "nan": float("nan"), "inf": float("inf")}[how]
+    y2, (g3, dw3) = combine(h), back(h, dy)
+    same(y, y2, others, "y")
+    same(g, g3, np.arange(c.n) != row, "dh")
+    same(dw, dw3, np.ones(M, bool), "dweights")
+    assert spoils(y2)[bad].all() and spoils(g3)[row].all()
