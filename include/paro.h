@@ -642,7 +642,9 @@ int paro_w4_experts_combine_backward(const paro_routing* routing, const uint16_t
  *   dL/dz_j = w T (A q_j - sum of p_i with j_i = j), outside the entries with a
  *   rest w T q_j (A - P / Q); A = sum p + P.
  *   z        device [M][V] of a paro_type, 16-byte aligned; student logits of
- *            -inf are classes that it cannot take.
+ *            -inf are classes that it cannot take, finite ones may be of any size
+ *            (a mask of the type's lowest number), and a NaN or +inf makes its row's
+ *            loss NaN.
  *   values   device [M][K] of a paro_type (t), index device int32 [M][K] (j): an
  *            index outside 0 .. V - 1 (-1) means no entry, a value of -inf an
  *            entry of mass 0; an index that comes twice adds its masses.

@@ -255,6 +255,9 @@ int paro_w4_experts_gated_backward(const paro_routing* routing, const uint16_t* 
   W4Epilogue ep;
   ep.aux = dh;
   ep.act = act;
+  // dX' is the product of dZ as it is returned, rounded to fp16: half a step, 2^-11, of
+  // each term, at random, which the sum keeps beside its own rounding (2.9e-4 of the
+  // norm against 2.1e-4 for an operand in fp32, that would take the matrix cores twice).
   hipError_t e = launch_w4_experts(kEpiGatedGrad, t, x, qweight, scales, zeros, bias, dz, N, d, group, ep, stream);
   if (e == hipSuccess && dx) {
     const bool wide = experts_grad_wide_fit(t, 2 * N, d, false);

@@ -16,12 +16,12 @@
 // entries' by 88 T its exponentials would all be 0, and the loss infinite. A second
 // pass reads z again, from the memory-side cache, and writes the gradient.
 //
-// What bounds it: with a gradient memory (4096 rows of 131072 bf16 in 503 us, 4.3 TB/s
-// of one read and one write, the second read in part from the cache; 574 with stores
-// that go through it); on short rows the entries' chain of latencies, 10 us, which
-// the other workgroups of the CU cover. (Reductions over the whole workgroup for the
-// entries too: 14 us a row. Rows kept in registers between the passes, 1024 lanes
-// a row: 706 us, nothing then covers the chain.)
+// What bounds it: with a gradient memory (4096 rows of 131072 bf16 in 476 us, 4.5 TB/s
+// of one read and one write, the second read in part from the cache; 8% longer with
+// stores that go through it); on short rows the entries' chain of latencies, 8 us,
+// which the other workgroups of the CU cover. (In an earlier form, 650 us: reductions
+// over the whole workgroup for the entries too, 14 us a row; rows kept in registers
+// between the passes, 1024 lanes a row, 706 us, nothing then covers the chain.)
 #include "paro_internal.h"
 #include "paro_types.h"
 
@@ -360,10 +360,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
 // Lanes per row. Many rows: as few as keep a CU's memory path busy with several
 // rows, so that they cover each other's latencies; with a gradient the rows in flight
 // have to stay in the memory-side cache until the second pass, so that long rows
-// take more lanes (4096 bf16 rows with 256 / 512 / 1024 lanes: of 131072 630 / 514 /
-// 503 us, of 32000 133 / 131 / 155, of 8000 50 / 60 / 95; the loss alone, of 131072,
-// 209 / 231 / 253). Few rows: the row itself is the latency (16 rows of 131072 40 /
-// 27 / 24).
+// take more lanes (4096 bf16 rows with the rest and 256 / 512 / 1024 lanes: of 131072
+// 623 / 510 / 482 us, of 32000 141 / 128 / 138, of 8000 39 / 49 / 71; the loss alone,
+// of 131072 195 / 187 / 195, of 32000 65 / 66 / 88, of 8000 28 / 37 / 57). Few rows:
+// the row itself is the latency (16 rows of 131072 44 / 30 / 24).
 hipError_t launch_distill(const DistillArgs& a, int z_type, int value_type, hipStream_t stream) {
   with_type(z_type, [&](auto z) {
     typedef decltype(z) Z;

@@ -160,9 +160,10 @@ struct ExpertRows {
 
   // The same where a block of at most bm / 2 rows takes half the time: those come
   // last, in eight runs of their own, so that the XCDs' work is even and ends with the
-  // short tiles (4096 tokens through 8 experts, skewed, 4096 -> 14336: 1.92 -> 1.77
-  // ms; a gradient of 2048 tokens, 32 experts, 2048 -> 1536: 0.199 -> 0.161). At most
-  // 16 workgroups more than tiles.
+  // short tiles (calls in a row, find_tile's walk | this: 4096 tokens through 8 experts,
+  // skewed, 4096 -> 14336 1932 | 1817 us; a whole gradient of 2048 tokens, 32 experts,
+  // 2048 -> 1536, 360 | 324 by the first product's tiles and 336 | 324 by the second's).
+  // At most 16 workgroups more than tiles.
   __device__ __forceinline__ bool find_tile_halves(int b, int bm, int nblk, ExpertTile& out, int& nb) const {
     int all = count_blocks<false>(bm) * nblk, per = (all + 7) >> 3, idx = b >> 3, tile = (b & 7) * per + idx;
     if (idx < per) {

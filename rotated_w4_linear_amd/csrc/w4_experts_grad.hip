@@ -414,6 +414,8 @@ void experts_grad_wide_steps(int64_t E, int64_t d, std::vector<int64_t>& rows) {
 //   of 14336 <- 4096, 8 experts (128 tiles): 32: 164 | 200, 128: 266 | 312, 192: 370 | 321;
 //   of gated 4096 -> 14336, 8 experts (128 tiles, shared out), dz included: 16: 469 | 476,
 //     32: 532 | 513, 64: 626 | 551, 128: 966 | 793.
+// (The rule goes by rows and tiles: with 60 experts of 1408 -> 2048 it is wrong up to
+// some 50 rows, by 14% at 16.)
 bool experts_grad_wide_fit(const ExpertRouting& t, int64_t P, int64_t d, bool share) {
   const int64_t E = t.E, splits = share ? 1 : experts_grad_splits(t, P, d);
   return P >= kK && t.R >= (E * d * splits >= kN * 256 ? 16 : 160) * E;
